@@ -57,7 +57,7 @@ enum lora_status {
     LORA_EBUSY = -5,    /* adapter still has users                                             */
     LORA_EEXIST = -6,   /* adapter already resident at another rank                            */
     LORA_EHIP = -7,     /* a HIP runtime call failed (message has the HIP error string)        */
-    LORA_EDEVICE = -8   /* an earlier projection found bad ids/ranks/pages on the device       */
+    LORA_EDEVICE = -8   /* earlier work found bad ids/ranks/pages/lengths on the device            */
 };
 
 enum lora_dtype {
@@ -342,6 +342,147 @@ int lora_debug_gather(lora_pool *pool, const int32_t *page_table, const int32_t 
 int lora_project_noalloc(lora_pool *pool, const void *x, const void *W, const int32_t *page_table,
                          const int32_t *adapter_ids, const int32_t *ranks, const float *scale, int64_t T,
                          void *y, void *stream);
+
+/* ---- the KV cache: writing it, reading it, thinning it out -------------------------------------- */
+
+/*
+ * "S-LoRA, in depth", section "Unified paging": KV cache and adapters share one pool; a token takes
+ * one K and one V vector per layer.  The calls below put the K and V rows of new tokens into the
+ * pages lora_pool_grow_kv handed out, attend over them, and thin a cache out by the attention its
+ * tokens received, so that its pages go back to the free list the adapters also draw from.
+ *
+ * One call serves one layer (lora_kv_evict: several) and n_seq sequences.
+ *   layout       how heads lie in a page (lora_kv_layout_t).
+ *   table        device int32 [n_seq][2][max_pages], 4-byte aligned, caller-owned: row (b, 0) lists
+ *                sequence b's K pages of this layer in token order, row (b, 1) its V pages.  Token t
+ *                of a sequence is the (t % tokens_per_page)-th of the page in entry
+ *                t / tokens_per_page; entries behind the last token's are not read.  Sequences may
+ *                share pages (a common prefix).  lora_pool_grow_kv's ids come in (K, V) pairs, layer
+ *                by layer: entry 2 l is layer l's K page, 2 l + 1 its V page.
+ *   lens         device int32 [n_seq]: tokens of each sequence in the cache, the new ones included.
+ *                0 = an unused row of a padded batch: nothing is written for it, its output is zero.
+ *   q_start      device int32 [n_seq + 1]: sequence b's new tokens are the rows q_start[b] up to (not
+ *                with) q_start[b + 1] of k, v, q and out, and the LAST tokens of its cache.  Rows
+ *                outside every sequence (behind q_start[n_seq]) are neither read nor written.
+ * Page ids, lengths and row ranges are checked on the device, as the projection's ids are: a page id
+ * outside the pool hides its tokens (they are not written, and get no weight); a length that is
+ * negative, above the capacity or below the number of new tokens counts as 0; a q_start range that
+ * does not lie in [0, T] counts as empty.  Each is recorded in the pool's device error word
+ * (lora_check_device_errors).
+ * Pool dtype throughout (k, v, q, out); products are summed, and softmax statistics and scores held,
+ * in float32.  Rows are `ld` elements apart (a column range of a wider matrix, such as the output of
+ * one projection for q, k and v, is fine); every row starts on a 16-byte boundary.
+ * Row counts up to LORA_MAX_TOKENS, n_seq up to LORA_MAX_SEQS, and max_pages * tokens_per_page up to
+ * LORA_MAX_KV_TOKENS.  n_seq == 0 or no rows: nothing is done.
+ */
+#define LORA_MAX_SEQS (1 << 16)
+#define LORA_MAX_KV_TOKENS (1 << 24)
+#define LORA_MAX_TOKENS_PER_PAGE 256
+#define LORA_MAX_HEADS 1024
+
+typedef struct lora_kv_layout {
+    int32_t n_heads;            /* query heads                                                  */
+    int32_t n_kv_heads;         /* K/V heads; divides n_heads.  Query head h reads K/V head
+                                   h / (n_heads / n_kv_heads)                                   */
+    int32_t head_dim;           /* 64, 128 or 256                                               */
+    int32_t tokens_per_page;    /* >= 1: tokens one page holds, one behind the other, each
+                                   n_kv_heads * head_dim elements; what is left of the page's
+                                   `hidden` elements stays unused                               */
+} lora_kv_layout_t;
+
+/*
+ * Put the new tokens' K and V rows into their pages: token i of sequence b goes to position
+ * lens[b] - (q_start[b + 1] - q_start[b]) + i.
+ *   k, v         device [T][n_kv_heads * head_dim], rows ldk (ldv) elements apart; outside the pool's pages
+ *   q_start      NULL: one new token per sequence (T == n_seq), as in a decode step
+ * Two new tokens for one place (sequences that share the page they write) is the caller's error.
+ * Errors: LORA_EINVAL, LORA_EHIP.
+ */
+int lora_kv_write(lora_pool *pool, const lora_kv_layout_t *layout, const void *k, int64_t ldk,
+                  const void *v, int64_t ldv, const int32_t *table, int32_t max_pages,
+                  const int32_t *q_start, const int32_t *lens, int32_t n_seq, int64_t T, void *stream);
+
+/* Bytes of device workspace (256-byte aligned) lora_kv_attend needs; 0 if an argument is out of
+ * range.  with_scores: whether the call collects scores. */
+size_t lora_kv_attend_workspace_size(const lora_pool *pool, const lora_kv_layout_t *layout,
+                                     int32_t n_seq, int64_t max_len, int32_t with_scores);
+
+/*
+ * Attention of one new token per sequence over its cached tokens (the decode step), each head h with
+ * its K/V head's vectors:
+ *     p_t = softmax over t < lens[b] of (scale * q_h . k_t),   out_h = sum_t p_t v_t
+ * The new token's own K and V are in the cache already (lora_kv_write first).
+ *   q, out       device [n_seq][n_heads * head_dim], rows ldq (ldo) elements apart; row b belongs to
+ *                sequence b; they may not overlap each other or the pool's pages
+ *   max_len      no length in this call is above it (1 .. max_pages * tokens_per_page): the call's
+ *                work is split, and its workspace sized, for it.  It fixes nothing else, so a
+ *                captured call may be replayed with any lengths up to it.
+ *   scores       device float32 [n_seq][max_pages * tokens_per_page] or NULL: scores[b][t] = prior[b][t]
+ *                + the sum over the heads of p_t, for t < lens[b]; the other entries stay as they were
+ *   prior        the same shape; NULL: zeros.  May be `scores` itself (accumulate in place); must not
+ *                overlap it otherwise
+ *   workspace    as lora_project's
+ * The out element is rounded once from float32.  Where every weight is zero (no token, or each
+ * product is -inf) the output is zero.  Results do not change from call to call of the same shape.
+ * Errors: LORA_EINVAL, LORA_EHIP.
+ */
+int lora_kv_attend(lora_pool *pool, const lora_kv_layout_t *layout, const void *q, int64_t ldq,
+                   const int32_t *table, int32_t max_pages, const int32_t *lens, int32_t n_seq,
+                   int64_t max_len, float scale, void *out, int64_t ldo, const float *prior,
+                   float *scores, void *workspace, size_t workspace_bytes, void *stream);
+
+/* As lora_kv_attend_workspace_size, for lora_kv_attend_chunk with T rows. */
+size_t lora_kv_attend_chunk_workspace_size(const lora_pool *pool, const lora_kv_layout_t *layout,
+                                           int32_t n_seq, int64_t T, int64_t max_len,
+                                           int32_t with_scores);
+
+/*
+ * Attention of many new tokens per sequence (a prompt, or the next part of one) over its cached
+ * tokens, causal: the new token at position p reads the tokens at positions 0 .. p.  A token's K and V
+ * reach no row before it, whatever they hold (infinities and NaN included).
+ *   q, out       device [T][n_heads * head_dim]; sequence b's rows as q_start says
+ *   scores       as lora_kv_attend's, summed over the sequence's new tokens too
+ * bfloat16 pools: the weights are rounded to bfloat16 for the product with V (scores take them
+ * unrounded).  The rest as lora_kv_attend.  Errors: LORA_EINVAL, LORA_EHIP.
+ */
+int lora_kv_attend_chunk(lora_pool *pool, const lora_kv_layout_t *layout, const void *q, int64_t ldq,
+                         const int32_t *table, int32_t max_pages, const int32_t *q_start,
+                         const int32_t *lens, int32_t n_seq, int64_t T, int64_t max_len, float scale,
+                         void *out, int64_t ldo, const float *prior, float *scores, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * Thin the caches of n_seq sequences out, in `layers` layers at once, to about `budget` tokens each:
+ * in every layer the pages whose tokens received the least attention leave the table.  Only pages
+ * that lie wholly in [keep_first, lens[b] - keep_last) can go (the first tokens and the latest ones
+ * stay).  From a sequence go, in every layer,
+ *     n_dropped[b] = min(max_drop, pages that can go, ceil((lens[b] - budget) / tokens_per_page)),
+ * (0 if lens[b] <= budget): the ones with the lowest sums of their tokens' scores, added in token
+ * order in float64; of equal sums the earlier page goes, and NaN counts as the highest.  The tokens that stay keep their
+ * order: nothing is moved in the pages, the tables close up.
+ *   table        device int32 [layers][n_seq][2][max_pages]; table_out the same shape: the entries
+ *                that stay, -1 behind them.  It may be `table` itself (in place).
+ *   scores       device float32 [layers][n_seq][max_pages * tokens_per_page]; scores_out the same: the scores of
+ *                the tokens that stay, 0 behind them.  It may be `scores` itself.
+ *   lens_out     device int32 [n_seq]: lens[b] - n_dropped[b] * tokens_per_page; must not be `lens`
+ *   dropped      device int32 [layers][n_seq][2][max_drop]: the K and V pages that left, in token
+ *                order, -1 behind them; copy them to the host and give them to lora_pool_drop_kv
+ *   n_dropped    device int32 [n_seq]
+ * A sequence whose length is out of range is recorded as above and left as it is.  The
+ * table's entries are not checked here.  Errors: LORA_EINVAL, LORA_EHIP.
+ */
+int lora_kv_evict(lora_pool *pool, const lora_kv_layout_t *layout, int32_t layers, int32_t n_seq,
+                  const int32_t *table, int32_t *table_out, int32_t max_pages, const float *scores,
+                  float *scores_out, const int32_t *lens, int32_t *lens_out, int32_t budget,
+                  int32_t keep_first, int32_t keep_last, int32_t *dropped, int32_t max_drop,
+                  int32_t *n_dropped, void *stream);
+
+/* Give `n` of request `request_id`'s KV pages back: they leave its page list (the others keep their
+ * order) and go to the end of the free list in the order given.  page_ids: host int64 [n].  All or
+ * none: a page that the request does not hold, or that is named twice, is LORA_EINVAL.  A request
+ * without pages stays known until lora_pool_free_kv.  The caller must not give back pages that
+ * queued, unfinished work still reads.  Errors: LORA_ENOENT, LORA_EINVAL. */
+int lora_pool_drop_kv(lora_pool *pool, int64_t request_id, const int64_t *page_ids, int64_t n);
 
 /* Wait for all device work, then report and clear the pool's device error word:
  * LORA_OK, or LORA_EDEVICE with a message naming the kinds of fault seen. */

@@ -24,6 +24,7 @@ LORA_MAX_RANK, LORA_MAX_ADAPTERS, LORA_MAX_TOKENS = 64, 8192, 1 << 22
 LORA_VICTIM_LOAD_ORDER, LORA_VICTIM_LRU, LORA_VICTIM_FARTHEST = 0, 1, 2
 LORA_MAX_CALL_SLOTS = 4
 LORA_NOALLOC_SCRATCH_MB = 32
+LORA_MAX_SEQS, LORA_MAX_KV_TOKENS, LORA_MAX_TOKENS_PER_PAGE, LORA_MAX_HEADS = 1 << 16, 1 << 24, 256, 1024
 STATUS_NAMES = {0: "ok", -1: "einval", -2: "enomem", -3: "enoent", -4: "erank", -5: "ebusy",
                 -6: "eexist", -7: "ehip", -8: "edevice"}
 
@@ -53,6 +54,12 @@ class lora_profile_t(ctypes.Structure):
                 ("ms_second", ctypes.c_double)]
 
 
+class lora_kv_layout_t(ctypes.Structure):
+    """How heads lie in a page: lora_kv_layout_t(n_heads, n_kv_heads, head_dim, tokens_per_page)."""
+    _fields_ = [("n_heads", _i32), ("n_kv_heads", _i32), ("head_dim", _i32), ("tokens_per_page", _i32)]
+
+
+_f32 = ctypes.c_float
 _SIGS = {
     "lora_pool_create": (ctypes.c_int, [_vp, _i64, _i32, _i32, _i32, _i32, _i32, _vp, _vp, ctypes.POINTER(_vp)]),
     "lora_pool_free": (ctypes.c_int, [_vp]),
@@ -79,6 +86,16 @@ _SIGS = {
     "lora_debug_gather": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _vp, _vp]),
     "lora_debug_project": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp, _vp, _vp]),
     "lora_project_noalloc": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "lora_kv_write": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _i64, _vp]),
+    "lora_kv_attend_workspace_size": (_sz, [_vp, _vp, _i32, _i64, _i32]),
+    "lora_kv_attend": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _i32, _vp, _i32, _i64, _f32, _vp, _i64, _vp, _vp,
+                                      _vp, _sz, _vp]),
+    "lora_kv_attend_chunk_workspace_size": (_sz, [_vp, _vp, _i32, _i64, _i64, _i32]),
+    "lora_kv_attend_chunk": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _i64, _i64, _f32, _vp,
+                                            _i64, _vp, _vp, _vp, _sz, _vp]),
+    "lora_kv_evict": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp,
+                                     _i32, _vp, _vp]),
+    "lora_pool_drop_kv": (ctypes.c_int, [_vp, _i64, _vp, _i64]),
     "lora_check_device_errors": (ctypes.c_int, [_vp]),
     "lora_profile_start": (ctypes.c_int, [_vp, _i32]),
     "lora_profile_stop": (ctypes.c_int, [_vp, ctypes.POINTER(lora_profile_t)]),
@@ -196,6 +213,12 @@ def lora_pool_grow_kv(pool, request_id, layers, check=True):
 def lora_pool_free_kv(pool, request_id, check=True):
     rc = _lib.lora_pool_free_kv(pool, request_id)
     return _check(rc, "lora_pool_free_kv") if check else rc
+
+
+def lora_pool_drop_kv(pool, request_id, page_ids, check=True):
+    ids = np.ascontiguousarray(page_ids, dtype=np.int64)
+    rc = _lib.lora_pool_drop_kv(pool, request_id, ids.ctypes.data if ids.size else None, ids.size)
+    return _check(rc, "lora_pool_drop_kv") if check else rc
 
 
 def lora_pool_pages_for(rank, projections, layers):
@@ -326,6 +349,48 @@ def lora_project_noalloc(pool, x, W, page_table, adapter_ids, ranks, scale, T, y
     return _check(rc, "lora_project_noalloc") if check else rc
 
 
+def lora_kv_write(pool, layout, k, ldk, v, ldv, table, max_pages, q_start, lens, n_seq, T, stream=None, check=True):
+    rc = _lib.lora_kv_write(pool, ctypes.byref(layout), _ptr(k), ldk, _ptr(v), ldv, _ptr(table), max_pages,
+                            _ptr(q_start), _ptr(lens), n_seq, T, _stream(stream))
+    return _check(rc, "lora_kv_write") if check else rc
+
+
+def lora_kv_attend_workspace_size(pool, layout, n_seq, max_len, with_scores=False):
+    return _lib.lora_kv_attend_workspace_size(pool, ctypes.byref(layout), n_seq, max_len, int(with_scores))
+
+
+def lora_kv_attend(pool, layout, q, ldq, table, max_pages, lens, n_seq, max_len, scale, out, ldo, prior=None,
+                   scores=None, workspace=None, workspace_bytes=None, stream=None, check=True):
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = _lib.lora_kv_attend(pool, ctypes.byref(layout), _ptr(q), ldq, _ptr(table), max_pages, _ptr(lens), n_seq,
+                             max_len, scale, _ptr(out), ldo, _ptr(prior), _ptr(scores), _ptr(workspace),
+                             workspace_bytes, _stream(stream))
+    return _check(rc, "lora_kv_attend") if check else rc
+
+
+def lora_kv_attend_chunk_workspace_size(pool, layout, n_seq, T, max_len, with_scores=False):
+    return _lib.lora_kv_attend_chunk_workspace_size(pool, ctypes.byref(layout), n_seq, T, max_len, int(with_scores))
+
+
+def lora_kv_attend_chunk(pool, layout, q, ldq, table, max_pages, q_start, lens, n_seq, T, max_len, scale, out, ldo,
+                         prior=None, scores=None, workspace=None, workspace_bytes=None, stream=None, check=True):
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = _lib.lora_kv_attend_chunk(pool, ctypes.byref(layout), _ptr(q), ldq, _ptr(table), max_pages, _ptr(q_start),
+                                   _ptr(lens), n_seq, T, max_len, scale, _ptr(out), ldo, _ptr(prior), _ptr(scores),
+                                   _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "lora_kv_attend_chunk") if check else rc
+
+
+def lora_kv_evict(pool, layout, layers, n_seq, table, table_out, max_pages, scores, scores_out, lens, lens_out, budget,
+                  keep_first, keep_last, dropped, max_drop, n_dropped, stream=None, check=True):
+    rc = _lib.lora_kv_evict(pool, ctypes.byref(layout), layers, n_seq, _ptr(table), _ptr(table_out), max_pages,
+                            _ptr(scores), _ptr(scores_out), _ptr(lens), _ptr(lens_out), budget, keep_first, keep_last,
+                            _ptr(dropped), max_drop, _ptr(n_dropped), _stream(stream))
+    return _check(rc, "lora_kv_evict") if check else rc
+
+
 def lora_check_device_errors(pool, check=True):
     rc = _lib.lora_check_device_errors(pool)
     return _check(rc, "lora_check_device_errors") if check else rc
@@ -446,3 +511,122 @@ class Pool:
         ws = self.workspace(T)
         lora_project(self.handle, x, W, self.table[slot], adapter_ids, ranks, scale, T, y, ws, stream=stream)
         return y
+
+    # ---- the KV cache ----------------------------------------------------------------------------
+    # layout: lora_kv_layout_t.  table: int32 [n_seq, 2, max_pages]; lens: int32 [n_seq]; q_start: int32
+    # [n_seq + 1].  Workspace and outputs are allocated per call on the call's stream, so calls on
+    # several streams, and calls captured into several graphs, share none.
+
+    def _where(self, stream):
+        """(stream handle, whether the call runs on the current stream of the current device)."""
+        torch, dev = self.torch, self.pages.device
+        if stream is None:
+            return torch.cuda.current_stream(dev).cuda_stream, True
+        return (stream if isinstance(stream, int) else stream.cuda_stream), False
+
+    def _empty(self, here, stream, shape, dtype):
+        """Memory that belongs to the call's stream, as its allocator sees it."""
+        torch, dev = self.torch, self.pages.device
+        if here:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+    def _kv_rows(self, what, t, width):
+        if t.dim() != 2 or t.shape[1] != width or t.dtype != self.tdtype or t.device != self.pages.device \
+                or (t.stride(1) != 1 and t.numel()):
+            raise ValueError(f"{what}: rows of {width} {self.tdtype} elements on {self.pages.device} are wanted, not "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+        return t.stride(0)
+
+    def _kv_ints(self, what, t, shape, dtype=None):
+        dtype = self.torch.int32 if dtype is None else dtype
+        if tuple(t.shape) != shape or t.dtype != dtype or t.device != self.pages.device or not t.is_contiguous():
+            raise ValueError(f"{what}: contiguous {dtype} {shape} on {self.pages.device} is wanted, not {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+
+    def _kv_table(self, table, lens, q_start):
+        n, mp = table.shape[0], table.shape[-1]
+        self._kv_ints("table", table, (n, 2, mp))
+        self._kv_ints("lens", lens, (n,))
+        if q_start is not None:
+            self._kv_ints("q_start", q_start, (n + 1,))
+        return n, mp
+
+    def kv_write(self, layout, k, v, table, lens, q_start=None, stream=None):
+        """K and V rows of new tokens into their pages (lora_kv_write)."""
+        n, mp = self._kv_table(table, lens, q_start)
+        width = layout.n_kv_heads * layout.head_dim
+        ldk, ldv = self._kv_rows("k", k, width), self._kv_rows("v", v, width)
+        if k.shape[0] != v.shape[0]:
+            raise ValueError(f"k has {k.shape[0]} rows and v {v.shape[0]}")
+        lora_kv_write(self.handle, layout, k, ldk, v, ldv, table, mp, q_start, lens, n, k.shape[0],
+                      stream=self._where(stream)[0])
+
+    def _kv_attend(self, layout, q, table, lens, q_start, scale, max_len, out, scores, prior, workspace, stream):
+        n, mp = self._kv_table(table, lens, q_start)
+        T, width, cap = q.shape[0], layout.n_heads * layout.head_dim, mp * layout.tokens_per_page
+        ldq = self._kv_rows("q", q, width)
+        if q_start is None and T != n:
+            raise ValueError(f"q has {T} rows for {n} sequences")
+        for what, t in (("scores", scores), ("prior", prior)):
+            if t is not None:
+                self._kv_ints(what, t, (n, cap), self.torch.float32)
+        handle, here = self._where(stream)
+        if out is None:
+            out = self._empty(here, stream, (T, width), self.tdtype)
+        ldo = self._kv_rows("out", out, width)
+        if out.shape[0] != T:
+            raise ValueError(f"out has {out.shape[0]} rows and q {T}")
+        scale = layout.head_dim ** -0.5 if scale is None else scale
+        max_len = cap if max_len is None else max_len
+        if workspace is None:
+            need = lora_kv_attend_workspace_size(self.handle, layout, n, max_len, scores is not None) \
+                if q_start is None else \
+                lora_kv_attend_chunk_workspace_size(self.handle, layout, n, T, max_len, scores is not None)
+            workspace = self._empty(here, stream, need, self.torch.uint8) if need else None
+        if q_start is None:
+            lora_kv_attend(self.handle, layout, q, ldq, table, mp, lens, n, max_len, scale, out, ldo, prior, scores,
+                           workspace, stream=handle)
+        else:
+            lora_kv_attend_chunk(self.handle, layout, q, ldq, table, mp, q_start, lens, n, T, max_len, scale, out, ldo,
+                                 prior, scores, workspace, stream=handle)
+        return out
+
+    def kv_attend(self, layout, q, table, lens, scale=None, max_len=None, out=None, scores=None, prior=None,
+                  workspace=None, stream=None):
+        """Attention of one new token per sequence (lora_kv_attend).  scale None: head_dim ** -0.5; max_len
+        None: the table's capacity; scores: float32 [n_seq, max_pages * tokens_per_page], written as
+        prior + this call's weights (prior=scores accumulates in place)."""
+        return self._kv_attend(layout, q, table, lens, None, scale, max_len, out, scores, prior, workspace, stream)
+
+    def kv_attend_chunk(self, layout, q, table, lens, q_start, scale=None, max_len=None, out=None, scores=None,
+                        prior=None, workspace=None, stream=None):
+        """Causal attention of many new tokens per sequence (lora_kv_attend_chunk); arguments as kv_attend's."""
+        return self._kv_attend(layout, q, table, lens, q_start, scale, max_len, out, scores, prior, workspace, stream)
+
+    def kv_evict(self, layout, table, scores, lens, budget, keep_first=0, keep_last=0, max_drop=None, in_place=False,
+                 stream=None):
+        """Thin the caches out by accumulated attention (lora_kv_evict).  table: int32 [layers, n_seq, 2,
+        max_pages]; scores: float32 [layers, n_seq, max_pages * tokens_per_page].  Returns (table, scores, lens,
+        dropped, n_dropped), the first two the tensors passed in if in_place."""
+        torch = self.torch
+        layers, n, mp = table.shape[0], table.shape[1], table.shape[-1]
+        self._kv_ints("table", table, (layers, n, 2, mp))
+        self._kv_ints("scores", scores, (layers, n, mp * layout.tokens_per_page), torch.float32)
+        self._kv_ints("lens", lens, (n,))
+        max_drop = mp if max_drop is None else max_drop
+        handle, here = self._where(stream)
+        table_out = table if in_place else self._empty(here, stream, table.shape, torch.int32)
+        scores_out = scores if in_place else self._empty(here, stream, scores.shape, torch.float32)
+        lens_out = self._empty(here, stream, (n,), torch.int32)
+        dropped = self._empty(here, stream, (layers, n, 2, max_drop), torch.int32)
+        n_dropped = self._empty(here, stream, (n,), torch.int32)
+        lora_kv_evict(self.handle, layout, layers, n, table, table_out, mp, scores, scores_out, lens, lens_out, budget,
+                      keep_first, keep_last, dropped, max_drop, n_dropped, stream=handle)
+        return table_out, scores_out, lens_out, dropped, n_dropped
+
+
+from .kv_cache import KvCache  # noqa: E402,F401

@@ -30,6 +30,7 @@ enum : int {
     DEV_ERR_RANK = 2,      // ranks[a] < 0 or > max_rank
     DEV_ERR_TABLE = 4,     // page-table row does not hold exactly 2*ranks[a] pages
     DEV_ERR_PAGE = 8,      // page id outside [0, num_pages)
+    DEV_ERR_LEN = 16,      // a sequence length or row range out of bounds
 };
 
 // ---- the pool ----------------------------------------------------------------------------------

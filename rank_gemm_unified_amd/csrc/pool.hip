@@ -400,6 +400,38 @@ extern "C" int lora_pool_free_kv(lora_pool *p, int64_t rid) {
     return LORA_OK;
 }
 
+extern "C" int lora_pool_drop_kv(lora_pool *p, int64_t rid, const int64_t *ids, int64_t n) {
+    clear_error();
+    if (!p) return set_error(LORA_EINVAL, "lora_pool_drop_kv: pool is NULL");
+    if (n < 0 || (n > 0 && !ids)) return set_error(LORA_EINVAL, "lora_pool_drop_kv: %lld pages at %p", (long long)n, (const void *)ids);
+    std::lock_guard<std::mutex> lk(p->mu);
+    auto it = p->kv.find(rid);
+    if (it == p->kv.end()) return set_error(LORA_ENOENT, "lora_pool_drop_kv: request %lld holds no KV pages", (long long)rid);
+    std::vector<int64_t> &held = it->second;
+    try {
+        std::unordered_map<int64_t, bool> go;   // page -> seen in the request's list
+        go.reserve((size_t)n);
+        for (int64_t i = 0; i < n; ++i)
+            if (!go.emplace(ids[i], false).second)
+                return set_error(LORA_EINVAL, "lora_pool_drop_kv: page %lld is named twice", (long long)ids[i]);
+        int64_t found = 0;
+        for (int64_t pg : held) {
+            auto g = go.find(pg);
+            if (g != go.end() && !g->second) { g->second = true; ++found; }
+        }
+        if (found != n)
+            return set_error(LORA_EINVAL, "lora_pool_drop_kv: request %lld holds %lld of the %lld pages", (long long)rid,
+                             (long long)found, (long long)n);
+        p->free_list.reserve(p->free_list.size() + (size_t)n);   // nothing below throws
+        held.erase(std::remove_if(held.begin(), held.end(), [&](int64_t pg) { return go.count(pg) != 0; }), held.end());
+        p->free_list.insert(p->free_list.end(), ids, ids + n);
+    } catch (...) {
+        return set_error(LORA_ENOMEM, "lora_pool_drop_kv: out of host memory");
+    }
+    p->kv_total -= n;
+    return LORA_OK;
+}
+
 // ---- queries --------------------------------------------------------------------------------------
 
 extern "C" int lora_pool_stats(const lora_pool *pc, lora_pool_stats_t *out) {
