@@ -375,7 +375,7 @@ int lora_project_noalloc(lora_pool *pool, const void *x, const void *W, const in
  * Row counts up to LORA_MAX_TOKENS, n_seq up to LORA_MAX_SEQS, and max_pages * tokens_per_page up to
  * LORA_MAX_KV_TOKENS.  n_seq == 0 or no rows: nothing is done.
  */
-#define LORA_MAX_SEQS (1 << 16)
+#define LORA_MAX_SEQS 65535
 #define LORA_MAX_KV_TOKENS (1 << 24)
 #define LORA_MAX_TOKENS_PER_PAGE 256
 #define LORA_MAX_HEADS 1024

@@ -1,129 +1,553 @@
-// Attention over the paged cache: one row of queries at a time.
+// Attention of one new token per sequence over the paged cache (the decode step).
+//
+// The work is reading K and V once: 4 * len * n_heads * head_dim operations on 2 * len * n_kv * head_dim
+// elements, a few operations a byte, so HBM bounds it.  The tiles (TT tokens) of all sequences, one
+// sequence behind the other, are cut into R equal ranges whatever the lengths; one wave takes one range
+// of one K/V head, so every wave reads the same amount, and waves next to each other read neighbouring
+// heads of the same pages.  A range ends inside a sequence as a rule: what a wave has of a sequence it
+// did not see whole goes to the workspace with its maximum and sum, and k_kv_join puts the pieces
+// together (split and joined, no atomics: results do not change from call to call).
+#include <algorithm>
+
 #include "kv_device.h"
 
 namespace lorapool {
 
-// One workgroup per (row, head): its four waves take the tokens in turn, each with a running maximum
-// and sum of its own; the four are joined in LDS.
-template <typename E, int HD>
-__global__ __launch_bounds__(256) void k_kv_rows(KvArgs a, KvAttend at, float2 *__restrict__ stats) {
-    constexpr int PER = HD / 64;
-    __shared__ int32_t sh;
-    __shared__ float part[4][HD], pm[4], pl[4];
-    const int32_t t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (t == 0 && h == 0) check_seqs(a);
-    const int32_t b = find_seq(a, t, &sh);
-    if (b < 0) return;
-    const SeqRows s = seq_rows(a, b);
-    const int32_t seen = s.n == 0 ? 0 : s.n - s.m + (t - s.first) + 1;   // tokens this row reads
-    const int32_t *krow = a.table + (int64_t)b * 2 * a.max_pages, *vrow = krow + a.max_pages;
-    const int64_t head_bytes = (int64_t)(h / a.group) * HD * sizeof(E);
-    const E *q = (const E *)at.q + t * at.ldq + (int64_t)h * HD;
-    float qf[PER], acc[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        qf[i] = to_f32(q[lane * PER + i]);
-        acc[i] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    int bad = 0;
-    for (int32_t j = wave; j < seen; j += 4) {
-        const int64_t ko = token_offset(a, krow, j), vo = token_offset(a, vrow, j);
-        if (ko < 0 || vo < 0) { bad = DEV_ERR_PAGE; continue; }
-        const E *kp = (const E *)(a.pages + ko + head_bytes), *vp = (const E *)(a.pages + vo + head_bytes);
-        float d = 0.f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) d += qf[i] * to_f32(kp[lane * PER + i]);
-        const float x = wave_sum(d) * at.scale;
-        const float mn = fmaxf(m, x), ms = mn == -INFINITY ? 0.f : mn;
-        const float c = __expf(m - ms), p = __expf(x - ms);
-        l = l * c + p;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = acc[i] * c + p * to_f32(vp[lane * PER + i]);
-        m = mn;
-    }
-    if (bad && lane == 0) record(a, bad);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) part[wave][lane * PER + i] = acc[i];
-    if (lane == 0) { pm[wave] = m; pl[wave] = l; }
-    __syncthreads();
-    float M = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-    const float Ms = M == -INFINITY ? 0.f : M;
-    float L = 0.f, w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = __expf(pm[i] - Ms);
-        L += pl[i] * w[i];
-    }
-    E *o = (E *)at.out + t * at.ldo + (int64_t)h * HD;
-    for (int32_t d = threadIdx.x; d < HD; d += 256) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v += part[i][d] * w[i];
-        from_f32(o + d, L == 0.f ? 0.f : v / L);
-    }
-    if (stats && threadIdx.x == 0) stats[(int64_t)t * a.n_heads + h] = make_float2(Ms, L == 0.f ? 0.f : 1.f / L);
+struct KvSplit {
+    int32_t R;                // ranges
+    int32_t ncb;              // blocks of 16 query heads of one K/V head
+    int32_t hu;               // K/V heads * ncb
+    float *part_o;            // [R][2][n_heads][head_dim]: slot 0 a range's first piece, 1 its last
+    float2 *part_ml;          // [R][2][n_heads]: maximum (base-2 logits), sum
+    float2 *done_ml;          // [n_seq][n_heads]: of the sequences one range saw whole
+    float *logits;            // [tile][n_heads][TT] base-2 logits, for the scores
+};
+
+template <typename E, int HD> struct Tile;   // tokens per step: K and V of a step take 64 (head_dim 256: 128) registers
+template <int HD> struct Tile<uint16_t, HD> { static constexpr int TT = HD == 64 ? 64 : 32; };
+template <int HD> struct Tile<float, HD> { static constexpr int TT = HD == 64 ? 32 : 16; };
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The tiles of all sequences: their number, and where each of up to four places (one per wave of the
+// workgroup) lies.  All 256 threads call.
+struct Places {
+    int64_t total;
+    int32_t b[4], j[4];
+};
+template <int TT>
+__device__ __forceinline__ int32_t seq_tiles(const KvArgs &a, int32_t b) {
+    const int32_t n = a.lens[b];
+    return n <= 0 || n > a.cap ? 0 : (n + TT - 1) / TT;
 }
 
-// scores[b][t] = prior + sum over the sequence's new rows and heads of the weight of token t.  One wave
-// per token; the weights are computed again from the rows' statistics.
-template <typename E, int HD>
-__global__ __launch_bounds__(256) void k_kv_scores(KvArgs a, KvAttend at, const float2 *__restrict__ stats) {
-    constexpr int PER = HD / 64;
-    const int32_t b = blockIdx.y, lane = threadIdx.x & 63, j = blockIdx.x * 4 + (threadIdx.x >> 6);
-    const SeqRows s = seq_rows(a, b);
-    if (j >= s.n) return;
-    const int32_t *krow = a.table + (int64_t)b * 2 * a.max_pages;
-    const int64_t ko = token_offset(a, krow, j), vo = token_offset(a, krow + a.max_pages, j);
-    float sum = 0.f;
-    if (ko >= 0 && vo >= 0) {
-        const int32_t r0 = max(0, j - (s.n - s.m));   // the first new row that sees token j
-        for (int32_t h = 0; h < a.n_heads; ++h) {
-            const E *kp = (const E *)(a.pages + ko) + (h / a.group) * HD;
-            float kf[PER];
+// Sum over the sequences before `upto` (and over all) of their tiles, by a workgroup of 256.
+template <int TT>
+__device__ __forceinline__ int64_t tiles_before(const KvArgs &a, int32_t upto, int64_t *sh, int64_t *total) {
+    int64_t before = 0, all = 0;
+    for (int32_t b = threadIdx.x; b < a.n_seq; b += 256) {
+        const int32_t t = seq_tiles<TT>(a, b);
+        all += t;
+        before += b < upto ? t : 0;
+    }
 #pragma unroll
-            for (int i = 0; i < PER; ++i) kf[i] = to_f32(kp[lane * PER + i]);
-            for (int32_t r = r0; r < s.m; ++r) {
-                const int64_t t = s.first + r;
-                const E *q = (const E *)at.q + t * at.ldq + (int64_t)h * HD;
-                float d = 0.f;
+    for (int o = 32; o > 0; o >>= 1) {
+        all += __shfl_xor(all, o, 64);
+        before += __shfl_xor(before, o, 64);
+    }
+    if ((threadIdx.x & 63) == 0) {
+        sh[threadIdx.x >> 6] = all;
+        sh[4 + (threadIdx.x >> 6)] = before;
+    }
+    __syncthreads();
+    *total = sh[0] + sh[1] + sh[2] + sh[3];
+    const int64_t r = sh[4] + sh[5] + sh[6] + sh[7];
+    __syncthreads();
+    return r;
+}
+
+// First tile of range r of R over `total` tiles, and the range a tile lies in.  R is at most the number of
+// tiles (ranges_of), so that no range is empty.
+__device__ __forceinline__ int32_t ranges_of(int32_t R, int64_t total) { return (int32_t)(total < R ? total : R); }
+__device__ __forceinline__ int64_t range_start(int64_t r, int64_t total, int32_t R) { return r * total / R; }
+__device__ __forceinline__ int32_t range_of(int64_t tile, int64_t total, int32_t R) {
+    return (int32_t)(((tile + 1) * R - 1) / total);
+}
+
+// Pieces of the sequence whose tiles are [t0, t1): from range r0's slot s0, then slot 0 of r0 + 1 .. r1.
+// r0 == r1: one wave saw it whole.
+struct Pieces {
+    int32_t r0, r1, s0;
+};
+__device__ __forceinline__ Pieces pieces_of(int64_t t0, int64_t t1, int64_t total, int32_t R) {
+    Pieces p;
+    p.r0 = range_of(t0, total, R);
+    p.r1 = range_of(t1 - 1, total, R);
+    p.s0 = range_start(p.r0, total, R) == t0 ? 0 : 1;
+    return p;
+}
+
+template <typename E, int HD, bool SCORES>
+__global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_split(KvArgs a, KvAttend at, KvSplit sp) {
+    constexpr int TT = Tile<E, HD>::TT, NS = TT / 16;
+    constexpr bool BF = sizeof(E) == 2;
+    constexpr int KS = HD * (int)sizeof(E) / 64;           // 16-byte loads of a lane per token row of K
+    constexpr int NV = BF ? (TT / 32) * 8 : NS * 4;        // tokens of V a lane holds parts of
+    constexpr int VC = BF ? (HD == 64 ? 1 : HD / 128) : HD / 64;   // 16-byte (bf16, 64: 8-byte) parts of each
+    constexpr int NA = HD / 16;                            // accumulators: 16 dims x 16 heads each
+    __shared__ int64_t sh_sum[4];
+    __shared__ int64_t sh_total;
+    __shared__ int32_t sh_b[4], sh_j[4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+
+    if (blockIdx.x == 0) check_seqs(a);
+    // ---- where this workgroup's waves begin ----
+    {
+        if (tid < 4) sh_b[tid] = sh_j[tid] = 0;
+        const int32_t per = (a.n_seq + 255) / 256, b0 = tid * per, b1 = min(a.n_seq, b0 + per);
+        int64_t mine = 0;
+        for (int32_t b = b0; b < b1; ++b) mine += seq_tiles<TT>(a, b);
+        int64_t incl = mine;
 #pragma unroll
-                for (int i = 0; i < PER; ++i) d += to_f32(q[lane * PER + i]) * kf[i];
-                const float2 st = stats[t * a.n_heads + h];
-                sum += __expf(wave_sum(d) * at.scale - st.x) * st.y;
+        for (int o = 1; o < 64; o <<= 1) {
+            const int64_t x = __shfl_up(incl, o, 64);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 63) sh_sum[wave] = incl;
+        __syncthreads();
+        int64_t excl = incl - mine;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) excl += i < wave ? sh_sum[i] : 0;
+        const int64_t total = sh_sum[0] + sh_sum[1] + sh_sum[2] + sh_sum[3];
+        if (tid == 0) sh_total = total;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int64_t r = ((int64_t)blockIdx.x * 4 + w) / sp.hu;
+            const int32_t R = ranges_of(sp.R, total);
+            const int64_t s = R > 0 ? range_start(r, total, R) : 0;
+            if (r < R && mine > 0 && s >= excl && s < excl + mine) {   // one thread at most
+                int64_t at0 = excl;
+                int32_t b = b0;
+                for (; b < b1; ++b) {
+                    const int32_t t = seq_tiles<TT>(a, b);
+                    if (s < at0 + t) break;
+                    at0 += t;
+                }
+                sh_b[w] = b;
+                sh_j[w] = (int32_t)(s - at0);
             }
         }
+        __syncthreads();
     }
-    const int64_t at_ = (int64_t)b * at.score_ld + j;
-    if (lane == 0) at.scores[at_] = (at.prior ? at.prior[at_] : 0.f) + sum;
+    const int64_t job = (int64_t)blockIdx.x * 4 + wave;
+    const int32_t range = (int32_t)(job / sp.hu), hu = (int32_t)(job - (int64_t)range * sp.hu);
+    const int64_t total = sh_total;
+    const int32_t R = ranges_of(sp.R, total);
+    if (range >= R) return;
+    int64_t gtile = range_start(range, total, R);
+    const int32_t count = uniform((int32_t)(range_start(range + 1, total, R) - gtile));
+
+    const int32_t kvh = uniform(hu / sp.ncb), cb = uniform(hu - kvh * sp.ncb);
+    const int32_t head = kvh * a.group + cb * 16 + col;
+    const bool mine = cb * 16 + col < a.group;             // this lane's column is a query head
+    const int64_t head_bytes = (int64_t)kvh * HD * sizeof(E);
+    const uint32_t page_units = (uint32_t)(a.page_bytes >> 7), tok_units = (uint32_t)(a.tok_bytes >> 7);
+    const float scale2 = at.scale * 1.4426950408889634f;
+
+    struct Pos { int32_t b, j, n; };
+    auto len_of = [&](int32_t b) { const int32_t n = a.lens[b]; return n <= 0 || n > a.cap ? 0 : n; };
+    auto next = [&](Pos p) {                               // only called while there is a next tile
+        p.j++;
+        if (p.j * TT >= p.n) {
+            p.j = 0;
+            do { p.b++; p.n = len_of(p.b); } while (p.n == 0 && p.b + 1 < a.n_seq);
+        }
+        return p;
+    };
+    // page ids of a tile's tokens, each lane those of token lane % TT; -1 behind the sequence's end
+    auto load_ids = [&](const Pos &p, int32_t *kid, int32_t *vid) {
+        const int32_t t = p.j * TT + (lane & (TT - 1));
+        int32_t e, slot;
+        page_of(a, t, &e, &slot);
+        const int32_t *row = a.table + (int64_t)p.b * 2 * a.max_pages + e;
+        *kid = *vid = -1;
+        if (t < p.n) { *kid = row[0]; *vid = row[a.max_pages]; }
+    };
+    int bad = 0;
+    // addresses in units of 128 bytes (every token row starts on one), and which tokens are there
+    auto to_units = [&](const Pos &p, int32_t kid, int32_t vid, uint32_t *ku, uint32_t *vu) -> uint64_t {
+        const int32_t t = p.j * TT + (lane & (TT - 1));
+        int32_t e, slot;
+        page_of(a, t, &e, &slot);
+        const bool ok = kid >= 0 && vid >= 0 && kid < a.num_pages && vid < a.num_pages;
+        if (t < p.n && !ok) bad = DEV_ERR_PAGE;
+        *ku = ok ? (uint32_t)kid * page_units + (uint32_t)slot * tok_units : 0u;
+        *vu = ok ? (uint32_t)vid * page_units + (uint32_t)slot * tok_units : 0u;
+        return __ballot(ok);
+    };
+    const char *base = a.pages + head_bytes;
+    u32x4_t K[NS][KS], Vr[NV][VC];
+    auto load_k = [&](uint32_t ku) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            const uint32_t u = __shfl(ku, 16 * s + col, 64);
+            const char *p = base + ((uint64_t)u << 7) + 16 * g;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) K[s][i] = load16(p + 64 * i);
+        }
+    };
+    auto v_token = [&](int j) { return BF ? 32 * (j >> 3) + 16 * ((j >> 2) & 1) + 4 * g + (j & 3) : 16 * (j >> 2) + 4 * g + (j & 3); };
+    auto load_v = [&](uint32_t vu) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const uint32_t u = __shfl(vu, v_token(j), 64);
+            const char *p = base + ((uint64_t)u << 7);
+            if constexpr (BF && HD == 64) {
+                const uint2 x = *(const uint2 *)(p + 8 * col);
+                Vr[j][0][0] = x.x;
+                Vr[j][0][1] = x.y;
+            } else {
+#pragma unroll
+                for (int c = 0; c < VC; ++c) Vr[j][c] = load16(p + 16 * col + 256 * c);
+            }
+        }
+    };
+
+    u32x4_t Q[KS];
+    f32x4_t acc[NA];
+    float m = -INFINITY, l = 0.f;
+    auto begin = [&](int32_t b) {
+        const char *p = (const char *)at.q + ((int64_t)b * at.ldq + (int64_t)(mine ? head : 0) * HD) * sizeof(E) + 16 * g;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            Q[i] = load16(p + 64 * i);
+            if (!mine) Q[i] = u32x4_t{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < NA; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        m = -INFINITY;
+        l = 0.f;
+    };
+    // four values of consecutive dims at `d` in `o`: which accumulators hold them
+    auto finish = [&](const Pos &p, bool whole, int slot) {
+        float L = l + __shfl_xor(l, 16, 64);
+        L += __shfl_xor(L, 32, 64);
+        if (!mine) return;
+        const int64_t pl = ((int64_t)range * 2 + slot) * a.n_heads + head;
+        if (g == 0) (whole ? sp.done_ml[(int64_t)p.b * a.n_heads + head] : sp.part_ml[pl]) = make_float2(m, L);
+        const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+        float *po = sp.part_o + pl * HD;
+        E *o = (E *)at.out + (int64_t)p.b * at.ldo + (int64_t)head * HD;
+        constexpr int W = BF && HD >= 128 ? 8 : 4;         // consecutive dims of one row of the accumulators
+#pragma unroll
+        for (int c = 0; c < NA / W; ++c)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int d = 16 * W * c + W * (4 * g + r);
+                float v[W];
+#pragma unroll
+                for (int i = 0; i < W; ++i) v[i] = acc[W * c + i][r] * inv;
+                if (!whole) {
+#pragma unroll
+                    for (int i = 0; i < W; i += 4) *(float4 *)(po + d + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                } else if constexpr (BF && W == 8) {
+                    store16(o + d, pack_bf16x8(v));
+                } else if constexpr (BF) {
+                    *(uint2 *)(o + d) = make_uint2(f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
+                                                   f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16);
+                } else {
+                    *(float4 *)(o + d) = make_float4(v[0], v[1], v[2], v[3]);
+                }
+            }
+    };
+
+    // ---- the pipeline: page ids two tiles ahead, K one tile ahead, V behind the K of the same tile ----
+    Pos p0{uniform(sh_b[wave]), uniform(sh_j[wave]), 0};
+    p0.n = len_of(p0.b);
+    Pos p1 = p0, p2;
+    int32_t kid, vid;
+    uint32_t ku, vu, vu1 = 0;
+    uint64_t there, there1 = 0;
+    load_ids(p0, &kid, &vid);
+    begin(p0.b);
+    there = to_units(p0, kid, vid, &ku, &vu);
+    if (count > 1) { p1 = next(p0); load_ids(p1, &kid, &vid); }
+    p2 = p1;
+    load_k(ku);
+    load_v(vu);
+    int32_t first_j = p0.j;      // the tile this wave began the sequence at
+    bool first_piece = true;
+    for (int32_t i = 0; i < count; ++i) {
+        // logits: rows are tokens, columns heads
+        f32x4_t S[NS];
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            S[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                if constexpr (BF) {
+                    S[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, K[s][k]),
+                                                                   __builtin_bit_cast(bf16x8_t, Q[k]), S[s], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        S[s] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(K[s][k][e]), __uint_as_float(Q[k][e]), S[s], 0, 0, 0);
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + 1 < count) {
+            uint32_t ku1;
+            there1 = to_units(p1, kid, vid, &ku1, &vu1);
+            if (i + 2 < count) { p2 = next(p1); load_ids(p2, &kid, &vid); }
+            load_k(ku1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // softmax statistics of this lane's head; the four lane groups hold different tokens
+        const bool full = (TT == 64 ? ~there : (~there & ((1ull << (TT & 63)) - 1))) == 0;
+        float mt = -INFINITY;
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float x = S[s][r] * scale2;
+                if (!full && !((there >> (16 * s + 4 * g + r)) & 1)) x = -INFINITY;
+                S[s][r] = x;
+                mt = fmaxf(mt, x);
+            }
+        if (SCORES && mine) {
+            float *lg = sp.logits + (gtile * a.n_heads + head) * TT + 4 * g;
+#pragma unroll
+            for (int s = 0; s < NS; ++s) *(f32x4_t *)(lg + 16 * s) = S[s];
+        }
+        mt = fmaxf(mt, __shfl_xor(mt, 16, 64));
+        mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
+        const float mn = fmaxf(m, mt), ms = mn == -INFINITY ? 0.f : mn;
+        const float c = exp2_hw(m - ms);
+        m = mn;
+        float ps = 0.f;
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                S[s][r] = exp2_hw(S[s][r] - ms);
+                ps += S[s][r];
+            }
+        l = l * c + ps;
+#pragma unroll
+        for (int x = 0; x < NA; ++x) acc[x] *= c;
+        if (!full) {                                       // what lies where no token is must not reach the products
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (!((there >> v_token(j)) & 1))
+#pragma unroll
+                    for (int cc = 0; cc < VC; ++cc) Vr[j][cc] = u32x4_t{0, 0, 0, 0};
+        }
+        // out^T += V^T P^T: rows are dims, columns heads
+        if constexpr (BF) {
+#pragma unroll
+            for (int q = 0; q < TT / 32; ++q) {
+                // weights as the sum of two bfloat16 numbers, so that they are off by at most 2^-15: the
+                // first their leading bits, cut off, the second the rest, rounded and never zero -- both have
+                // the weight's sign, so that an infinite value times a weight stays that infinity
+                u32x4_t hi, lo;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float a0 = S[2 * q + x / 2][2 * (x & 1)], a1 = S[2 * q + x / 2][2 * (x & 1) + 1];
+                    const uint32_t h0 = __float_as_uint(a0) & 0xffff0000u, h1 = __float_as_uint(a1) & 0xffff0000u;
+                    hi[x] = h0 >> 16 | h1;
+                    lo[x] = f32_to_bf16_bits(fmaxf(a0 - __uint_as_float(h0), 0x1p-100f)) |
+                            f32_to_bf16_bits(fmaxf(a1 - __uint_as_float(h1), 0x1p-100f)) << 16;
+                }
+                constexpr int W = HD == 64 ? 4 : 8;
+#pragma unroll
+                for (int cc = 0; cc < VC; ++cc)
+#pragma unroll
+                    for (int x = 0; x < W; ++x) {
+                        u32x4_t f;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            f[y] = __builtin_amdgcn_perm(Vr[8 * q + 2 * y + 1][cc][x / 2], Vr[8 * q + 2 * y][cc][x / 2],
+                                                         x & 1 ? 0x07060302u : 0x05040100u);
+                        acc[W * cc + x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8_t, f), __builtin_bit_cast(bf16x8_t, lo), acc[W * cc + x], 0, 0, 0);
+                        acc[W * cc + x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8_t, f), __builtin_bit_cast(bf16x8_t, hi), acc[W * cc + x], 0, 0, 0);
+                    }
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int cc = 0; cc < VC; ++cc)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[4 * cc + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(Vr[4 * s + r][cc][e]), S[s][r],
+                                                                                   acc[4 * cc + e], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + 1 < count) load_v(vu1);
+        __builtin_amdgcn_sched_barrier(0);
+        const bool ends = (p0.j + 1) * TT >= p0.n;
+        if (ends || i + 1 == count) {
+            finish(p0, ends && first_j == 0, first_piece ? 0 : 1);
+            first_piece = false;
+            if (i + 1 < count) { begin(p1.b); first_j = 0; }
+        }
+        p0 = p1;
+        p1 = p2;
+        there = there1;
+        ++gtile;
+    }
+    if (bad) record(a, bad);
 }
 
-size_t kv_attend_ws_bytes(int, const lora_kv_layout_t &l, int32_t n_seq, int64_t, bool scores) {
-    return scores ? (size_t)n_seq * l.n_heads * 8 : 0;
+// Put the pieces of a sequence (blockIdx.y) together, and form its scores.  Workgroups below n_heads take a
+// head: each of the four waves a part of the pieces, joined in LDS.  The others take 256 tokens' scores.
+template <typename E, int HD>
+__global__ __launch_bounds__(256) void k_kv_join(KvArgs a, KvAttend at, KvSplit sp) {
+    constexpr int TT = Tile<E, HD>::TT;
+    extern __shared__ float2 sh_ml[];
+    __shared__ int64_t sh[8];
+    __shared__ float sh_o[4][HD], sh_m[4], sh_l[4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int32_t b = blockIdx.y, h = blockIdx.x, first = (h - a.n_heads) * 256;
+    const int32_t n = a.lens[b], nt = seq_tiles<TT>(a, b);
+    if (first >= 0 && (nt == 0 || first >= n)) return;
+    int64_t total;
+    const int64_t t0 = tiles_before<TT>(a, b, sh, &total);
+    if (first < 0) {
+        E *o = (E *)at.out + (int64_t)b * at.ldo + (int64_t)h * HD;
+        if (nt == 0) {
+            for (int d = tid; d < HD; d += 256) from_f32(o + d, 0.f);
+            return;
+        }
+        const Pieces p = pieces_of(t0, t0 + nt, total, ranges_of(sp.R, total));
+        if (p.r0 == p.r1) return;
+        constexpr int PER = HD / 64;
+        float m = -INFINITY, l = 0.f, acc[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+        for (int32_t r = p.r0 + wave; r <= p.r1; r += 4) {
+            const int64_t pl = ((int64_t)r * 2 + (r == p.r0 ? p.s0 : 0)) * a.n_heads + h;
+            const float2 ml = sp.part_ml[pl];
+            float v[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) v[i] = sp.part_o[pl * HD + 64 * i + lane];
+            const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+            const float c = exp2_hw(m - ms), w = exp2_hw(ml.x - ms);
+            l = l * c + ml.y * w;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) acc[i] = acc[i] * c + v[i] * w;
+            m = mn;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) sh_o[wave][64 * i + lane] = acc[i];
+        if (lane == 0) { sh_m[wave] = m; sh_l[wave] = l; }
+        __syncthreads();
+        const float M = fmaxf(fmaxf(sh_m[0], sh_m[1]), fmaxf(sh_m[2], sh_m[3])), Ms = M == -INFINITY ? 0.f : M;
+        float L = 0.f, w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = exp2_hw(sh_m[i] - Ms);
+            L += sh_l[i] * w[i];
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        for (int d = tid; d < HD; d += 256) {
+            float v = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v += sh_o[i][d] * w[i];
+            from_f32(o + d, v * inv);
+        }
+        return;
+    }
+    const Pieces p = pieces_of(t0, t0 + nt, total, ranges_of(sp.R, total));
+    for (int32_t hh = tid; hh < a.n_heads; hh += 256) {    // each head's final maximum and 1 / sum
+        float m = -INFINITY, l = 0.f;
+        if (p.r0 == p.r1) {
+            const float2 ml = sp.done_ml[(int64_t)b * a.n_heads + hh];
+            m = ml.x;
+            l = ml.y;
+        } else {
+            for (int32_t r = p.r0; r <= p.r1; ++r) {
+                const float2 ml = sp.part_ml[((int64_t)r * 2 + (r == p.r0 ? p.s0 : 0)) * a.n_heads + hh];
+                const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+                l = l * exp2_hw(m - ms) + ml.y * exp2_hw(ml.x - ms);
+                m = mn;
+            }
+        }
+        sh_ml[hh] = make_float2(m == -INFINITY ? 0.f : m, l == 0.f ? 0.f : 1.f / l);
+    }
+    __syncthreads();
+    const int32_t t = first + tid;
+    if (t >= n) return;
+    const float *lg = sp.logits + ((t0 + t / TT) * a.n_heads) * TT + (t & (TT - 1));
+    float sum = 0.f;
+    for (int32_t hh = 0; hh < a.n_heads; ++hh) {
+        const float2 ml = sh_ml[hh];
+        sum += exp2_hw(lg[(int64_t)hh * TT] - ml.x) * ml.y;
+    }
+    const int64_t si = (int64_t)b * at.score_ld + t;
+    at.scores[si] = (at.prior ? at.prior[si] : 0.f) + sum;
 }
-size_t kv_chunk_ws_bytes(int, const lora_kv_layout_t &l, int32_t, int64_t T, int64_t, bool scores) {
-    return scores ? (size_t)T * l.n_heads * 8 : 0;
+
+// ---- host ----------------------------------------------------------------------------------------
+namespace {
+
+int tile_tokens(int dtype, int hd) { return dtype == LORA_F32 ? (hd == 64 ? 32 : 16) : (hd == 64 ? 64 : 32); }
+
+struct SplitPlan {
+    int32_t R, ncb, hu;
+    size_t off_ml, off_done, off_logits, total;
+};
+SplitPlan split_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int64_t max_len, bool scores) {
+    SplitPlan s;
+    const int tt = tile_tokens(dtype, hd), group = n_heads / n_kv;
+    const int64_t tiles = (max_len + tt - 1) / tt * n_seq;    // at most
+    s.ncb = (group + 15) / 16;
+    s.hu = n_kv * s.ncb;
+    // eight waves a CU; no more ranges than tiles
+    s.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, 2048 / s.hu));
+    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+    s.off_ml = up((size_t)s.R * 2 * n_heads * hd * 4);
+    s.off_done = s.off_ml + up((size_t)s.R * 2 * n_heads * 8);
+    s.off_logits = s.off_done + up((size_t)n_seq * n_heads * 8);
+    s.total = s.off_logits + (scores ? up((size_t)tiles * tt * n_heads * 4) : 0);
+    return s;
 }
 
 template <typename E, int HD>
-static hipError_t rows(const KvArgs &a, const KvAttend &at, hipStream_t s) {
-    float2 *stats = at.scores ? (float2 *)at.ws : nullptr;
-    hipLaunchKernelGGL((k_kv_rows<E, HD>), dim3(a.T, a.n_heads), dim3(256), 0, s, a, at, stats);
-    if (at.scores)
-        hipLaunchKernelGGL((k_kv_scores<E, HD>), dim3((a.cap + 3) / 4, a.n_seq), dim3(256), 0, s, a, at, stats);
+hipError_t run(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s) {
+    const SplitPlan pl = split_plan(dtype, a.n_heads, a.n_kv, HD, a.n_seq, a.cap, at.scores != nullptr);
+    char *ws = (char *)at.ws;
+    const KvSplit sp{pl.R, pl.ncb, pl.hu, (float *)ws, (float2 *)(ws + pl.off_ml), (float2 *)(ws + pl.off_done),
+                     (float *)(ws + pl.off_logits)};
+    const dim3 grid((unsigned)(((int64_t)pl.R * pl.hu + 3) / 4));
+    if (at.scores) hipLaunchKernelGGL((k_kv_split<E, HD, true>), grid, dim3(256), 0, s, a, at, sp);
+    else hipLaunchKernelGGL((k_kv_split<E, HD, false>), grid, dim3(256), 0, s, a, at, sp);
+    const int32_t sb = at.scores ? (a.cap + 255) / 256 : 0;
+    hipLaunchKernelGGL((k_kv_join<E, HD>), dim3(a.n_heads + sb, a.n_seq), dim3(256),
+                       at.scores ? a.n_heads * sizeof(float2) : 0, s, a, at, sp);
     return hipGetLastError();
 }
 
 template <typename E>
-static hipError_t by_dim(const KvArgs &a, const KvAttend &at, hipStream_t s) {
-    return a.head_dim == 64 ? rows<E, 64>(a, at, s) : a.head_dim == 128 ? rows<E, 128>(a, at, s) : rows<E, 256>(a, at, s);
+hipError_t by_dim(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s) {
+    return a.head_dim == 64 ? run<E, 64>(dtype, a, at, s) : a.head_dim == 128 ? run<E, 128>(dtype, a, at, s)
+                                                                              : run<E, 256>(dtype, a, at, s);
+}
+
+}  // namespace
+
+size_t kv_attend_ws_bytes(int dtype, const lora_kv_layout_t &l, int32_t n_seq, int64_t max_len, bool scores) {
+    return split_plan(dtype, l.n_heads, l.n_kv_heads, l.head_dim, n_seq, max_len, scores).total;
 }
 
 hipError_t launch_kv_attend(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s) {
-    return dtype == LORA_F32 ? by_dim<float>(a, at, s) : by_dim<uint16_t>(a, at, s);
-}
-hipError_t launch_kv_chunk(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s) {
-    return dtype == LORA_F32 ? by_dim<float>(a, at, s) : by_dim<uint16_t>(a, at, s);
+    return dtype == LORA_F32 ? by_dim<float>(dtype, a, at, s) : by_dim<uint16_t>(dtype, a, at, s);
 }
 
 }  // namespace lorapool

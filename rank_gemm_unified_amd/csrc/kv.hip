@@ -50,6 +50,9 @@ int common(lora_pool *p, const char *fn, const lora_kv_layout_t *l, const int32_
     if (!table || !lens) return set_error(LORA_EINVAL, "%s: NULL pointer argument", fn);
     if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(q_start, 4))
         return set_error(LORA_EINVAL, "%s: misaligned pointer (table, q_start, lens: 4 B)", fn);
+    // kernels address token rows in 32-bit units of 128 bytes
+    if ((int64_t)p->num_pages * p->hidden * p->elem > (int64_t(1) << 39))
+        return set_error(LORA_EINVAL, "%s: pool of more than 512 GiB", fn);
     a->pages = (char *)p->pages;
     a->num_pages = p->num_pages;
     a->page_bytes = (int64_t)p->hidden * p->elem;

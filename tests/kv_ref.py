@@ -7,6 +7,12 @@ import numpy as np
 import torch
 
 EPS32 = 2.0 ** -24          # half a float32 step, relative
+# The weights in the product with V.  A chunk of a bfloat16 pool takes them rounded to bfloat16: half a step,
+# 2^-8.  One token per sequence takes them as two bfloat16 numbers: the first is the weight cut off to 8 bits, so
+# the rest is below 2^-7 of it, and the second is the rest rounded, off by at most 2^-8 of it: 2^-15 in all.
+# float32 pools take them as they are.
+ROUNDED = {(torch.bfloat16, True): 2.0 ** -8, (torch.bfloat16, False): 2.0 ** -15, (torch.float32, True): 0.0,
+           (torch.float32, False): 0.0}
 HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
 
 
@@ -26,9 +32,10 @@ def cached(pages, layout, table_row, n):
     return out[0], out[1], there
 
 
-def attend(pages, layout, q, table, lens, q_start, scale, chunk):
+def attend(pages, layout, q, table, lens, q_start, scale, rounded):
     """Outputs, bounds on their error before the last rounding, weights summed over rows and heads, and
-    their bounds.  q [T][heads * dim] tensor; rows outside every sequence come back as NaN."""
+    their bounds.  q [T][heads * dim] tensor; rows outside every sequence come back as NaN.  rounded: how far the
+    weights are off, relatively, in the product with V (ROUNDED)."""
     nh, dim, group = layout.n_heads, layout.head_dim, layout.n_heads // layout.n_kv_heads
     q = q.detach().to("cpu", torch.float32).numpy().astype(np.float64)
     T, n_seq, cap = q.shape[0], len(lens), table.shape[-1] * layout.tokens_per_page
@@ -60,7 +67,6 @@ def attend(pages, layout, q, table, lens, q_start, scale, chunk):
             rel = (2 * dx + (n + 64) * EPS32 + 16 * EPS32)[:, None]
             cols = slice(h * dim, (h + 1) * dim)
             out[r0:r1, cols] = np.where(seen.any(1)[:, None], p @ np.where(there[:, None], v, 0), 0)
-            rounded = 2.0 ** -8 if chunk else 0.0     # the weights' rounding to bfloat16
             tol[r0:r1, cols] = (rel + rounded) * (p @ np.abs(np.where(there[:, None], v, 0)))
             sc[b, :n] += p.sum(0)
             sc_tol[b, :n] += (p * rel).sum(0)

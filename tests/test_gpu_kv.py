@@ -80,8 +80,8 @@ class Case:
                                          prior=prior, out=out, **kw)
 
     def ref(self):
-        chunk = self.q_start is not None and self.dt is torch.bfloat16
-        return kv_ref.attend(self.pool.pages, self.layout, self.q, self.table, self.lens, self.q_start, self.scale, chunk)
+        return kv_ref.attend(self.pool.pages, self.layout, self.q, self.table, self.lens, self.q_start, self.scale,
+                             kv_ref.ROUNDED[self.dt, self.q_start is not None])
 
     def errors(self):
         return rg.lora_check_device_errors(self.pool.handle, check=False)
@@ -324,10 +324,10 @@ def test_far_pages():
     pool.kv_write(layout, k, v, t, lens, starts)
     assert torch.equal(pool.pages[P - 2 * n:P - n, :256], k) and torch.equal(pool.pages[P - n:, :256], v)
     out = pool.kv_attend_chunk(layout, q, t, lens, starts)
-    want, tol, _, _ = kv_ref.attend(pool.pages, layout, q, ids, [n], [0, n], 0.125, True)
+    want, tol, _, _ = kv_ref.attend(pool.pages, layout, q, ids, [n], [0, n], 0.125, 2.0 ** -8)
     close(out, want, tol, torch.bfloat16, "far chunk")
     out = pool.kv_attend(layout, q[-1:], t, lens)
-    want, tol, _, _ = kv_ref.attend(pool.pages, layout, q[-1:], ids, [n], None, 0.125, False)
+    want, tol, _, _ = kv_ref.attend(pool.pages, layout, q[-1:], ids, [n], None, 0.125, 2.0 ** -15)
     close(out, want, tol, torch.bfloat16, "far token")
     assert rg.lora_check_device_errors(pool.handle, check=False) == 0
 
@@ -417,7 +417,7 @@ def test_a_run_of_them_together(geo, dtype):
                 one = rg.lora_kv_layout_t(nh, nkv, dim, 1)
                 want, tol, sw, stol = kv_ref.attend(torch.cat([held[0], held[1]]), one, q[sl],
                                                     np.arange(2 * n, dtype=np.int32).reshape(1, 2, n), [n], [0, m], dim ** -0.5,
-                                                    chunk and dtype == "bf16")
+                                                    kv_ref.ROUNDED[DT[dtype], chunk])
                 close(out[sl], want, tol, DT[dtype], f"request {rid} layer {layer} ({n} tokens)")
                 held[2] = np.concatenate([held[2], np.zeros(m)]) + sw[0]
             if not chunk:

@@ -163,7 +163,7 @@ def test_reference_forms_agree_with_loops():
     table = rng.permutation(20).astype(np.int32).reshape(1, 2, 10)
     q = torch.as_tensor(rng.standard_normal((3, 256)).astype(np.float32))
     n = 7
-    out, _, sc, _ = kv_ref.attend(pages, lay, q, table, [n], [0, 3], 0.3, False)
+    out, _, sc, _ = kv_ref.attend(pages, lay, q, table, [n], [0, 3], 0.3, 0.0)
     want_sc = np.zeros(n)
     for r in range(3):
         for h in range(4):
