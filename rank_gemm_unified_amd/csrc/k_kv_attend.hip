@@ -20,11 +20,13 @@ struct KvSplit {
     float *part_o;            // [R][2][n_heads][head_dim]: slot 0 a range's first piece, 1 its last
     float2 *part_ml;          // [R][2][n_heads]: maximum (base-2 logits), sum
     float2 *done_ml;          // [n_seq][n_heads]: of the sequences one range saw whole
-    float *logits;            // [tile][n_heads][TT] base-2 logits, for the scores
+    int32_t cols;             // query heads of a block, at most
+    int64_t tiles;            // at most
+    float *logits;            // [hu][tiles][cols][TT] base-2 logits, for the scores
 };
 
-template <typename E, int HD> struct Tile;   // tokens per step: K and V of a step take 64 (head_dim 256: 128) registers
-template <int HD> struct Tile<uint16_t, HD> { static constexpr int TT = HD == 64 ? 64 : 32; };
+template <typename E, int HD> struct Tile;   // tokens per step
+template <int HD> struct Tile<uint16_t, HD> { static constexpr int TT = 32; };
 template <int HD> struct Tile<float, HD> { static constexpr int TT = HD == 64 ? 32 : 16; };
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -67,12 +69,25 @@ __device__ __forceinline__ int64_t tiles_before(const KvArgs &a, int32_t upto, i
     return r;
 }
 
-// First tile of range r of R over `total` tiles, and the range a tile lies in.  R is at most the number of
-// tiles (ranges_of), so that no range is empty.
-__device__ __forceinline__ int32_t ranges_of(int32_t R, int64_t total) { return (int32_t)(total < R ? total : R); }
-__device__ __forceinline__ int64_t range_start(int64_t r, int64_t total, int32_t R) { return r * total / R; }
-__device__ __forceinline__ int32_t range_of(int64_t tile, int64_t total, int32_t R) {
-    return (int32_t)(((tile + 1) * R - 1) / total);
+// The ranges: R of them (no more than there are tiles), base tiles each and one more in the first `rem`.
+struct Ranges {
+    int64_t base;
+    int32_t rem, R;
+    __device__ __forceinline__ int64_t start(int64_t r) const { return r * base + (r < rem ? r : rem); }
+    __device__ __forceinline__ int32_t of(int64_t tile) const {            // the range a tile lies in
+        const int64_t longer = rem * (base + 1);
+        return tile < longer ? (int32_t)div(tile, base + 1) : rem + (int32_t)div(tile - longer, base);
+    }
+    static __device__ __forceinline__ int64_t div(int64_t a, int64_t b) {  // 32 bits as a rule: a third of the time
+        return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+    }
+};
+__device__ __forceinline__ Ranges ranges_of(int64_t total, int32_t R) {
+    Ranges r;
+    r.R = (int32_t)(total < R ? total : R);
+    r.base = r.R ? Ranges::div(total, r.R) : 0;
+    r.rem = (int32_t)(total - r.base * r.R);
+    return r;
 }
 
 // Pieces of the sequence whose tiles are [t0, t1): from range r0's slot s0, then slot 0 of r0 + 1 .. r1.
@@ -80,16 +95,19 @@ __device__ __forceinline__ int32_t range_of(int64_t tile, int64_t total, int32_t
 struct Pieces {
     int32_t r0, r1, s0;
 };
-__device__ __forceinline__ Pieces pieces_of(int64_t t0, int64_t t1, int64_t total, int32_t R) {
+__device__ __forceinline__ Pieces pieces_of(int64_t t0, int64_t t1, const Ranges &rg) {
     Pieces p;
-    p.r0 = range_of(t0, total, R);
-    p.r1 = range_of(t1 - 1, total, R);
-    p.s0 = range_start(p.r0, total, R) == t0 ? 0 : 1;
+    p.r0 = rg.of(t0);
+    p.r1 = rg.of(t1 - 1);
+    p.s0 = rg.start(p.r0) == t0 ? 0 : 1;
     return p;
 }
 
+// waves a SIMD holds: what the registers of K, two V tiles, the accumulators and the queries leave room for
+constexpr int split_waves(int elem, int hd) { return hd == 256 ? 1 : hd == 64 && elem == 2 ? 3 : 2; }
+
 template <typename E, int HD, bool SCORES>
-__global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_split(KvArgs a, KvAttend at, KvSplit sp) {
+__global__ __launch_bounds__(256, split_waves(sizeof(E), HD)) void k_kv_split(KvArgs a, KvAttend at, KvSplit sp) {
     constexpr int TT = Tile<E, HD>::TT, NS = TT / 16;
     constexpr bool BF = sizeof(E) == 2;
     constexpr int KS = HD * (int)sizeof(E) / 64;           // 16-byte loads of a lane per token row of K
@@ -99,6 +117,10 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_split(KvArgs a, K
     __shared__ int64_t sh_sum[4];
     __shared__ int64_t sh_total;
     __shared__ int32_t sh_b[4], sh_j[4];
+    // logits on their way to memory.  Stores are waited for in their turn with the loads around them, and take
+    // longest where loads fill the queues, so a wave gathers what it can hold first (8 x 32768 tokens, 32 heads on
+    // 8 K/V heads: 222 us stored tile by tile, 218 gathered in 4 KiB, 202 in 15 KiB, 189 without logits).
+    __shared__ __align__(16) float sh_log[4][SCORES ? 3840 : 4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
 
     if (blockIdx.x == 0) check_seqs(a);
@@ -121,12 +143,12 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_split(KvArgs a, K
         for (int i = 0; i < 4; ++i) excl += i < wave ? sh_sum[i] : 0;
         const int64_t total = sh_sum[0] + sh_sum[1] + sh_sum[2] + sh_sum[3];
         if (tid == 0) sh_total = total;
+        const Ranges rg = ranges_of(total, sp.R);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const int64_t r = ((int64_t)blockIdx.x * 4 + w) / sp.hu;
-            const int32_t R = ranges_of(sp.R, total);
-            const int64_t s = R > 0 ? range_start(r, total, R) : 0;
-            if (r < R && mine > 0 && s >= excl && s < excl + mine) {   // one thread at most
+            const int32_t r = (blockIdx.x * 4 + w) / sp.hu;
+            const int64_t s = rg.start(r);
+            if (r < rg.R && mine > 0 && s >= excl && s < excl + mine) {   // one thread at most
                 int64_t at0 = excl;
                 int32_t b = b0;
                 for (; b < b1; ++b) {
@@ -140,13 +162,11 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_split(KvArgs a, K
         }
         __syncthreads();
     }
-    const int64_t job = (int64_t)blockIdx.x * 4 + wave;
-    const int32_t range = (int32_t)(job / sp.hu), hu = (int32_t)(job - (int64_t)range * sp.hu);
-    const int64_t total = sh_total;
-    const int32_t R = ranges_of(sp.R, total);
-    if (range >= R) return;
-    int64_t gtile = range_start(range, total, R);
-    const int32_t count = uniform((int32_t)(range_start(range + 1, total, R) - gtile));
+    const int32_t job = blockIdx.x * 4 + wave, range = job / sp.hu, hu = job - range * sp.hu;
+    const Ranges rg = ranges_of(sh_total, sp.R);
+    if (range >= rg.R) return;
+    int64_t gtile = rg.start(range);
+    const int32_t count = uniform((int32_t)(rg.start(range + 1) - gtile));
 
     const int32_t kvh = uniform(hu / sp.ncb), cb = uniform(hu - kvh * sp.ncb);
     const int32_t head = kvh * a.group + cb * 16 + col;
@@ -187,7 +207,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_split(KvArgs a, K
         return __ballot(ok);
     };
     const char *base = a.pages + head_bytes;
-    u32x4_t K[NS][KS], Vr[NV][VC];
+    u32x4_t K[NS][KS], V0[NV][VC], V1[NV][VC];   // V of this tile and of the next
     auto load_k = [&](uint32_t ku) {
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
@@ -198,7 +218,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_split(KvArgs a, K
         }
     };
     auto v_token = [&](int j) { return BF ? 32 * (j >> 3) + 16 * ((j >> 2) & 1) + 4 * g + (j & 3) : 16 * (j >> 2) + 4 * g + (j & 3); };
-    auto load_v = [&](uint32_t vu) {
+    auto load_v = [&](u32x4_t (&Vr)[NV][VC], uint32_t vu) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const uint32_t u = __shfl(vu, v_token(j), 64);
@@ -217,19 +237,18 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_split(KvArgs a, K
     u32x4_t Q[KS];
     f32x4_t acc[NA];
     float m = -INFINITY, l = 0.f;
-    auto begin = [&](int32_t b) {
+    // query rows of sequence b; lanes without a head take the first one's (their columns are never stored)
+    auto load_q = [&](int32_t b) {
         const char *p = (const char *)at.q + ((int64_t)b * at.ldq + (int64_t)(mine ? head : 0) * HD) * sizeof(E) + 16 * g;
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            Q[i] = load16(p + 64 * i);
-            if (!mine) Q[i] = u32x4_t{0, 0, 0, 0};
-        }
+        for (int i = 0; i < KS; ++i) Q[i] = load16(p + 64 * i);
+    };
+    auto reset = [&]() {
 #pragma unroll
         for (int i = 0; i < NA; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         m = -INFINITY;
         l = 0.f;
     };
-    // four values of consecutive dims at `d` in `o`: which accumulators hold them
     auto finish = [&](const Pos &p, bool whole, int slot) {
         float L = l + __shfl_xor(l, 16, 64);
         L += __shfl_xor(L, 32, 64);
@@ -262,23 +281,29 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_split(KvArgs a, K
             }
     };
 
-    // ---- the pipeline: page ids two tiles ahead, K one tile ahead, V behind the K of the same tile ----
+    // ---- the pipeline: page ids two tiles ahead, K and V one tile ahead ----
+    // The loads of the next tile are issued whether there is one or not (behind the last tile they read the
+    // pool's first page): a load under a condition would make every later wait a wait for all.
     Pos p0{uniform(sh_b[wave]), uniform(sh_j[wave]), 0};
     p0.n = len_of(p0.b);
     Pos p1 = p0, p2;
     int32_t kid, vid;
-    uint32_t ku, vu, vu1 = 0;
-    uint64_t there, there1 = 0;
+    uint32_t ku, vu;
+    uint64_t there, there1;
     load_ids(p0, &kid, &vid);
-    begin(p0.b);
+    load_q(p0.b);
+    reset();
     there = to_units(p0, kid, vid, &ku, &vu);
-    if (count > 1) { p1 = next(p0); load_ids(p1, &kid, &vid); }
+    if (count > 1) p1 = next(p0);
+    load_ids(p1, &kid, &vid);
     p2 = p1;
     load_k(ku);
-    load_v(vu);
+    load_v(V0, vu);
+    const int32_t hold = max(3840 / (sp.cols * TT), 1);
+    int32_t held = 0;
     int32_t first_j = p0.j;      // the tile this wave began the sequence at
     bool first_piece = true;
-    for (int32_t i = 0; i < count; ++i) {
+    auto step = [&](int32_t i, u32x4_t (&Vr)[NV][VC], u32x4_t (&Vn)[NV][VC]) {
         // logits: rows are tokens, columns heads
         f32x4_t S[NS];
 #pragma unroll
@@ -297,15 +322,17 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_split(KvArgs a, K
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (i + 1 < count) {
-            uint32_t ku1;
-            there1 = to_units(p1, kid, vid, &ku1, &vu1);
-            if (i + 2 < count) { p2 = next(p1); load_ids(p2, &kid, &vid); }
-            load_k(ku1);
-        }
+        const bool more = i + 1 < count;
+        if (more && p1.j == 0) load_q(p1.b);
+        uint32_t ku1, vu1;
+        there1 = to_units(p1, kid, vid, &ku1, &vu1);
+        if (i + 2 < count) p2 = next(p1);
+        load_ids(p2, &kid, &vid);
+        load_k(more ? ku1 : 0u);
+        load_v(Vn, more ? vu1 : 0u);
         __builtin_amdgcn_sched_barrier(0);
         // softmax statistics of this lane's head; the four lane groups hold different tokens
-        const bool full = (TT == 64 ? ~there : (~there & ((1ull << (TT & 63)) - 1))) == 0;
+        const bool full = (~there & ((1ull << TT) - 1)) == 0;
         float mt = -INFINITY;
 #pragma unroll
         for (int s = 0; s < NS; ++s)
@@ -316,10 +343,19 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_split(KvArgs a, K
                 S[s][r] = x;
                 mt = fmaxf(mt, x);
             }
-        if (SCORES && mine) {
-            float *lg = sp.logits + (gtile * a.n_heads + head) * TT + 4 * g;
+        if constexpr (SCORES) {
+            float *lg = sh_log[wave] + (held * sp.cols + col) * TT + 4 * g;
+            if (mine)
 #pragma unroll
-            for (int s = 0; s < NS; ++s) *(f32x4_t *)(lg + 16 * s) = S[s];
+                for (int s = 0; s < NS; ++s) *(f32x4_t *)(lg + 16 * s) = S[s];
+            if (++held == hold || !more) {                 // what is held, in one go
+                __builtin_amdgcn_wave_barrier();
+                float *dst = sp.logits + (hu * sp.tiles + gtile + 1 - held) * sp.cols * TT;
+                for (int32_t x = 4 * lane; x < held * sp.cols * TT; x += 256)
+                    *(f32x4_t *)(dst + x) = *(const f32x4_t *)(sh_log[wave] + x);
+                held = 0;
+                __builtin_amdgcn_wave_barrier();
+            }
         }
         mt = fmaxf(mt, __shfl_xor(mt, 16, 64));
         mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
@@ -389,18 +425,23 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_split(KvArgs a, K
                                                                                    acc[4 * cc + e], 0, 0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (i + 1 < count) load_v(vu1);
-        __builtin_amdgcn_sched_barrier(0);
         const bool ends = (p0.j + 1) * TT >= p0.n;
         if (ends || i + 1 == count) {
             finish(p0, ends && first_j == 0, first_piece ? 0 : 1);
             first_piece = false;
-            if (i + 1 < count) { begin(p1.b); first_j = 0; }
+            reset();
+            first_j = 0;
         }
         p0 = p1;
         p1 = p2;
         there = there1;
         ++gtile;
+    };
+    for (int32_t i = 0;;) {
+        step(i, V0, V1);
+        if (++i >= count) break;
+        step(i, V1, V0);
+        if (++i >= count) break;
     }
     if (bad) record(a, bad);
 }
@@ -425,24 +466,33 @@ __global__ __launch_bounds__(256) void k_kv_join(KvArgs a, KvAttend at, KvSplit 
             for (int d = tid; d < HD; d += 256) from_f32(o + d, 0.f);
             return;
         }
-        const Pieces p = pieces_of(t0, t0 + nt, total, ranges_of(sp.R, total));
+        const Pieces p = pieces_of(t0, t0 + nt, ranges_of(total, sp.R));
         if (p.r0 == p.r1) return;
         constexpr int PER = HD / 64;
         float m = -INFINITY, l = 0.f, acc[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-        for (int32_t r = p.r0 + wave; r <= p.r1; r += 4) {
-            const int64_t pl = ((int64_t)r * 2 + (r == p.r0 ? p.s0 : 0)) * a.n_heads + h;
-            const float2 ml = sp.part_ml[pl];
-            float v[PER];
+        for (int32_t r = p.r0 + wave; r <= p.r1; r += 16) {    // four pieces' loads at once
+            float2 ml[4];
+            float v[4][PER];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) v[i] = sp.part_o[pl * HD + 64 * i + lane];
-            const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
-            const float c = exp2_hw(m - ms), w = exp2_hw(ml.x - ms);
-            l = l * c + ml.y * w;
+            for (int u = 0; u < 4; ++u) {
+                const int32_t ru = min(r + 4 * u, p.r1);
+                const int64_t pl = ((int64_t)ru * 2 + (ru == p.r0 ? p.s0 : 0)) * a.n_heads + h;
+                ml[u] = sp.part_ml[pl];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) acc[i] = acc[i] * c + v[i] * w;
-            m = mn;
+                for (int i = 0; i < PER; ++i) v[u][i] = sp.part_o[pl * HD + 64 * i + lane];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (r + 4 * u > p.r1) break;
+                const float mn = fmaxf(m, ml[u].x), ms = mn == -INFINITY ? 0.f : mn;
+                const float c = exp2_hw(m - ms), w = exp2_hw(ml[u].x - ms);
+                l = l * c + ml[u].y * w;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) acc[i] = acc[i] * c + v[u][i] * w;
+                m = mn;
+            }
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) sh_o[wave][64 * i + lane] = acc[i];
@@ -464,58 +514,99 @@ __global__ __launch_bounds__(256) void k_kv_join(KvArgs a, KvAttend at, KvSplit 
         }
         return;
     }
-    const Pieces p = pieces_of(t0, t0 + nt, total, ranges_of(sp.R, total));
-    for (int32_t hh = tid; hh < a.n_heads; hh += 256) {    // each head's final maximum and 1 / sum
+    // The first heads' logits are on their way while the statistics are formed.
+    const int32_t t = first + tid;
+    const float *lg = sp.logits + (t0 + t / TT) * sp.cols * TT + (t & (TT - 1));
+    const int64_t plane = sp.tiles * sp.cols * TT;
+    int32_t cb = 0, col = 0;
+    constexpr int AHEAD = 32;
+    float x[AHEAD], sum = 0.f;
+    auto fetch = [&](int32_t heads) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (i >= heads) break;
+            x[i] = t < n ? lg[col * TT] : 0.f;
+            if (++col == min(16, a.group - 16 * cb)) {
+                col = 0;
+                cb = cb + 1 == sp.ncb ? 0 : cb + 1;
+                lg += plane;
+            }
+        }
+    };
+    fetch(a.n_heads);
+    const int64_t si = (int64_t)b * at.score_ld + t;
+    const float prior = at.prior && t < n ? at.prior[si] : 0.f;
+    // each head's final maximum and 1 / sum, by as many threads a head as there are
+    const Pieces p = pieces_of(t0, t0 + nt, ranges_of(total, sp.R));
+    const int32_t per = max(1, 256 / a.n_heads);
+    for (int32_t x = tid; x < a.n_heads * per; x += 256) {
+        const int32_t hh = per == 1 ? x : x % a.n_heads, k = per == 1 ? 0 : x / a.n_heads;
         float m = -INFINITY, l = 0.f;
         if (p.r0 == p.r1) {
-            const float2 ml = sp.done_ml[(int64_t)b * a.n_heads + hh];
-            m = ml.x;
-            l = ml.y;
+            if (k == 0) {
+                const float2 ml = sp.done_ml[(int64_t)b * a.n_heads + hh];
+                m = ml.x;
+                l = ml.y;
+            }
         } else {
-            for (int32_t r = p.r0; r <= p.r1; ++r) {
+#pragma unroll 4
+            for (int32_t r = p.r0 + k; r <= p.r1; r += per) {
                 const float2 ml = sp.part_ml[((int64_t)r * 2 + (r == p.r0 ? p.s0 : 0)) * a.n_heads + hh];
                 const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
                 l = l * exp2_hw(m - ms) + ml.y * exp2_hw(ml.x - ms);
                 m = mn;
             }
         }
-        sh_ml[hh] = make_float2(m == -INFINITY ? 0.f : m, l == 0.f ? 0.f : 1.f / l);
+        sh_ml[k * a.n_heads + hh] = make_float2(m, l);
     }
     __syncthreads();
-    const int32_t t = first + tid;
-    if (t >= n) return;
-    const float *lg = sp.logits + ((t0 + t / TT) * a.n_heads) * TT + (t & (TT - 1));
-    float sum = 0.f;
-    for (int32_t hh = 0; hh < a.n_heads; ++hh) {
-        const float2 ml = sh_ml[hh];
-        sum += exp2_hw(lg[(int64_t)hh * TT] - ml.x) * ml.y;
+    for (int32_t hh = tid; hh < a.n_heads; hh += 256) {
+        float m = -INFINITY, l = 0.f;
+        for (int32_t k = 0; k < per; ++k) {
+            const float2 ml = sh_ml[k * a.n_heads + hh];
+            const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+            l = l * exp2_hw(m - ms) + ml.y * exp2_hw(ml.x - ms);
+            m = mn;
+        }
+        sh_ml[hh] = make_float2(m == -INFINITY ? 0.f : m, l == 0.f ? 0.f : 1.f / l);   // this thread alone reads head hh
     }
-    const int64_t si = (int64_t)b * at.score_ld + t;
-    at.scores[si] = (at.prior ? at.prior[si] : 0.f) + sum;
+    __syncthreads();
+    for (int32_t hh = 0; hh < a.n_heads; hh += AHEAD) {
+        if (hh) fetch(a.n_heads - hh);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (i >= a.n_heads - hh) break;
+            const float2 ml = sh_ml[hh + i];
+            sum += exp2_hw(x[i] - ml.x) * ml.y;
+        }
+    }
+    if (t < n) at.scores[si] = prior + sum;
 }
 
 // ---- host ----------------------------------------------------------------------------------------
 namespace {
 
-int tile_tokens(int dtype, int hd) { return dtype == LORA_F32 ? (hd == 64 ? 32 : 16) : (hd == 64 ? 64 : 32); }
+int tile_tokens(int dtype, int hd) { return dtype == LORA_F32 && hd > 64 ? 16 : 32; }
 
 struct SplitPlan {
-    int32_t R, ncb, hu;
+    int32_t R, ncb, hu, cols;
+    int64_t tiles;
     size_t off_ml, off_done, off_logits, total;
 };
 SplitPlan split_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int64_t max_len, bool scores) {
     SplitPlan s;
     const int tt = tile_tokens(dtype, hd), group = n_heads / n_kv;
-    const int64_t tiles = (max_len + tt - 1) / tt * n_seq;    // at most
+    const int64_t tiles = s.tiles = (max_len + tt - 1) / tt * n_seq;
+    s.cols = std::min(group, 16);
     s.ncb = (group + 15) / 16;
     s.hu = n_kv * s.ncb;
-    // eight waves a CU; no more ranges than tiles
-    s.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, 2048 / s.hu));
+    // as many waves as the chip holds; no more ranges than tiles
+    s.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, 1024 * split_waves(dtype == LORA_F32 ? 4 : 2, hd) / s.hu));
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     s.off_ml = up((size_t)s.R * 2 * n_heads * hd * 4);
     s.off_done = s.off_ml + up((size_t)s.R * 2 * n_heads * 8);
     s.off_logits = s.off_done + up((size_t)n_seq * n_heads * 8);
-    s.total = s.off_logits + (scores ? up((size_t)tiles * tt * n_heads * 4) : 0);
+    s.total = s.off_logits + (scores ? up((size_t)s.hu * tiles * s.cols * tt * 4) : 0);
     return s;
 }
 
@@ -524,13 +615,13 @@ hipError_t run(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s) {
     const SplitPlan pl = split_plan(dtype, a.n_heads, a.n_kv, HD, a.n_seq, a.cap, at.scores != nullptr);
     char *ws = (char *)at.ws;
     const KvSplit sp{pl.R, pl.ncb, pl.hu, (float *)ws, (float2 *)(ws + pl.off_ml), (float2 *)(ws + pl.off_done),
-                     (float *)(ws + pl.off_logits)};
+                     pl.cols, pl.tiles, (float *)(ws + pl.off_logits)};
     const dim3 grid((unsigned)(((int64_t)pl.R * pl.hu + 3) / 4));
     if (at.scores) hipLaunchKernelGGL((k_kv_split<E, HD, true>), grid, dim3(256), 0, s, a, at, sp);
     else hipLaunchKernelGGL((k_kv_split<E, HD, false>), grid, dim3(256), 0, s, a, at, sp);
     const int32_t sb = at.scores ? (a.cap + 255) / 256 : 0;
     hipLaunchKernelGGL((k_kv_join<E, HD>), dim3(a.n_heads + sb, a.n_seq), dim3(256),
-                       at.scores ? a.n_heads * sizeof(float2) : 0, s, a, at, sp);
+                       at.scores ? std::max(a.n_heads, 256) * sizeof(float2) : 0, s, a, at, sp);
     return hipGetLastError();
 }
 
