@@ -104,10 +104,10 @@ __device__ __forceinline__ Pieces pieces_of(int64_t t0, int64_t t1, const Ranges
 }
 
 // waves a SIMD holds: what the registers of K, two V tiles, the accumulators and the queries leave room for
-constexpr int split_waves(int elem, int hd) { return hd == 256 ? 1 : hd == 64 && elem == 2 ? 3 : 2; }
+constexpr int split_waves(int hd) { return hd == 256 ? 1 : 2; }
 
 template <typename E, int HD, bool SCORES>
-__global__ __launch_bounds__(256, split_waves(sizeof(E), HD)) void k_kv_split(KvArgs a, KvAttend at, KvSplit sp) {
+__global__ __launch_bounds__(256, split_waves(HD)) void k_kv_split(KvArgs a, KvAttend at, KvSplit sp) {
     constexpr int TT = Tile<E, HD>::TT, NS = TT / 16;
     constexpr bool BF = sizeof(E) == 2;
     constexpr int KS = HD * (int)sizeof(E) / 64;           // 16-byte loads of a lane per token row of K
@@ -601,7 +601,7 @@ SplitPlan split_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, in
     s.ncb = (group + 15) / 16;
     s.hu = n_kv * s.ncb;
     // as many waves as the chip holds; no more ranges than tiles
-    s.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, 1024 * split_waves(dtype == LORA_F32 ? 4 : 2, hd) / s.hu));
+    s.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, 1024 * split_waves(hd) / s.hu));
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     s.off_ml = up((size_t)s.R * 2 * n_heads * hd * 4);
     s.off_done = s.off_ml + up((size_t)s.R * 2 * n_heads * 8);

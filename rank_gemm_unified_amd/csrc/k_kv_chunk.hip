@@ -1,0 +1,586 @@
+// Causal attention of many new tokens per sequence over the paged cache (a prompt, or its next part).
+//
+// Matrix products bound it: 4 * head_dim operations for every (query row, token) pair that the mask lets
+// through.  One workgroup takes 128 query rows of one K/V head -- 128 tokens of one head, or 64 or 32 of
+// two or four heads that share it -- and walks the sequence's tokens NT at a time with a running maximum
+// and sum.  K and V go from their pages straight to LDS (16 bytes a lane, gathered row by row, double
+// buffered); a wave's 32 rows stay in registers, as columns:
+//     S^T = K Q^T   (rows tokens, columns query rows)       out^T += V^T P^T   (rows dims)
+// so that a lane holds one query row's logits, and the products of the first are, after the softmax,
+// in place as the right operand of the second: the weights never leave their registers.  V^T comes out of
+// LDS through the transposing read.  Two workgroups a CU: one's softmax runs under the other's products.
+#include <algorithm>
+
+#include "kv_device.h"
+
+namespace lorapool {
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+
+struct KvChunk {
+    int32_t hpw;              // query heads of one K/V head a workgroup takes: 1, 2 or 4
+    int32_t slots;            // query tiles, at most
+    float2 *stats;            // [T][n_heads]: maximum (base-2 logits) and 1 / sum of each row, for the scores; or null
+    float *part;              // [n_seq][n_kv][cap_ld]: a K/V head's share of the scores
+    int64_t cap_ld;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ uint32_t pack2(float a, float b) {   // two floats to bfloat16, round to nearest even
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
+}
+
+template <typename E, int HD>
+struct Chunk {
+    static constexpr bool BF = sizeof(E) == 2;
+    static constexpr int NT = BF ? 64 : 32;                 // tokens of a step
+    static constexpr int RB = HD * (int)sizeof(E);          // bytes of a token's row
+    static constexpr int CH = RB / 16;                      // 16-byte pieces of it
+    static constexpr int BUF = NT * RB;
+    static constexpr int LDS = 4 * BUF;                     // K and V, two steps each
+    static constexpr int WAVES = LDS > 64 * 1024 ? 1 : 2;   // workgroups a CU
+    static constexpr int KQ = BF ? HD / 16 : HD / 8;        // 16-byte pieces of a query row a lane holds
+    static constexpr int NB = NT / 32;                      // blocks of 32 tokens
+    // Where piece c of row t lies in LDS.  What one cycle reads has to lie in different banks (256 bytes of them): of
+    // K one piece of 16 rows, of V (bfloat16, transposing read) two neighbouring pairs of pieces of four rows.
+    static __device__ __forceinline__ int k_swz(int t, int c) { return c ^ (CH == 8 ? t >> 1 & 7 : t & 15); }
+    static __device__ __forceinline__ int v_swz(int t, int c) { return !BF ? c : c ^ (CH == 8 ? (t >> 1 & 1) << 2 : (t & 3) << 2); }
+};
+
+// Page ids to addresses, in units of 128 bytes (every token row starts on one): token tok of a sequence of n,
+// one per lane; which tokens are there.
+__device__ __forceinline__ void lane_ids(const KvArgs &a, const int32_t *row, int32_t tok, int32_t n, int32_t *kid, int32_t *vid) {
+    int32_t e, slot;
+    page_of(a, tok, &e, &slot);
+    *kid = *vid = -1;
+    if (tok < n) { *kid = row[e]; *vid = row[a.max_pages + e]; }
+}
+__device__ __forceinline__ uint64_t lane_units(const KvArgs &a, int32_t tok, int32_t n, int32_t kid, int32_t vid, uint32_t *ku,
+                                               uint32_t *vu, int *bad) {
+    int32_t e, slot;
+    page_of(a, tok, &e, &slot);
+    const bool ok = kid >= 0 && vid >= 0 && kid < a.num_pages && vid < a.num_pages;
+    if (tok < n && !ok) *bad = DEV_ERR_PAGE;
+    const uint32_t pu = (uint32_t)(a.page_bytes >> 7), tu = (uint32_t)(a.tok_bytes >> 7);
+    *ku = ok ? (uint32_t)kid * pu + (uint32_t)slot * tu : 0u;
+    *vu = ok ? (uint32_t)vid * pu + (uint32_t)slot * tu : 0u;
+    return __ballot(ok);
+}
+
+// The query tile that a slot stands for: sequence and tile in it; -1 behind the last.  Slots count tiles of
+// all sequences from the end, so that the longest rows of a sequence start first.  All 256 threads call.
+__device__ __forceinline__ int32_t find_tile(const KvArgs &a, int32_t slot, int32_t tq, int32_t *tile, int32_t *sh) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int32_t per = (a.n_seq + 255) / 256, b0 = min(a.n_seq, tid * per), b1 = min(a.n_seq, b0 + per);
+    int32_t mine = 0;
+    for (int32_t b = b0; b < b1; ++b) mine += (seq_rows(a, b).m + tq - 1) / tq;
+    const int32_t incl = wave_incl_scan(mine, lane);
+    if (lane == 63) sh[wave] = incl;
+    if (tid == 0) sh[4] = -1;
+    __syncthreads();
+    int32_t excl = incl - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        excl += i < wave ? sh[i] : 0;
+        total += sh[i];
+    }
+    const int32_t want = total - 1 - slot;
+    if (want >= excl && want < excl + mine) {
+        int32_t at = excl;
+        for (int32_t b = b0; b < b1; ++b) {
+            const int32_t t = (seq_rows(a, b).m + tq - 1) / tq;
+            if (want < at + t) {
+                sh[4] = b;
+                sh[5] = want - at;
+                break;
+            }
+            at += t;
+        }
+    }
+    __syncthreads();
+    *tile = sh[5];
+    return sh[4];
+}
+
+template <typename E, int HD>
+__global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs a, KvAttend at, KvChunk ck) {
+    using C = Chunk<E, HD>;
+    constexpr int NT = C::NT, RB = C::RB, CH = C::CH, KQ = C::KQ, NB = C::NB, ND = HD / 32;
+    constexpr bool BF = C::BF;
+    extern __shared__ __align__(256) char smem[];
+    __shared__ int32_t sh[6];
+    __shared__ unsigned long long sh_flag;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, hh = lane >> 5;
+    const int32_t groups = a.n_heads / ck.hpw, hg = blockIdx.x % groups, slot = blockIdx.x / groups;
+    if (blockIdx.x == 0) check_seqs(a);
+    const int32_t tq = 128 / ck.hpw;
+    int32_t tile;
+    const int32_t b = find_tile(a, slot, tq, &tile, sh);
+    if (b < 0) return;
+    const SeqRows sq = seq_rows(a, b);
+    const int32_t head = hg * ck.hpw + (wave & (ck.hpw - 1)), q0 = tile * tq + (wave / ck.hpw) * 32;
+    const int32_t qi = q0 + col;
+    const bool row_ok = qi < sq.m;
+    const int64_t row = sq.first + (row_ok ? qi : sq.m - 1);
+    E *orow = (E *)at.out + row * at.ldo + (int64_t)head * HD;
+    if (sq.n == 0) {                                        // no tokens: zero rows
+        if (row_ok)
+            for (int d = hh * (HD / 2); d < (hh + 1) * (HD / 2); ++d) from_f32(orow + d, 0.f);
+        if (ck.stats && row_ok && hh == 0) ck.stats[row * a.n_heads + head] = make_float2(0.f, 0.f);
+        return;
+    }
+    const int32_t old = sq.n - sq.m;                        // tokens before the new ones
+    const int32_t pos = old + (row_ok ? qi : sq.m - 1);     // this lane's row sees tokens 0 .. pos
+    const int32_t wave_lo = old + min(q0, sq.m - 1), wave_hi = old + min(q0 + 31, sq.m - 1);
+    const int32_t wg_lo = old + tile * tq, wg_hi = old + min(tile * tq + tq, sq.m) - 1;
+    const int32_t steps = wg_hi / NT + 1;
+    const int32_t *trow = a.table + (int64_t)b * 2 * a.max_pages;
+    const char *base = a.pages + (int64_t)(head / a.group) * RB;
+    const float scale2 = at.scale * 1.4426950408889634f;
+
+    u32x4_t Q[KQ];
+    {
+        const char *p = (const char *)((const E *)at.q + row * at.ldq + (int64_t)head * HD) + 16 * hh;
+#pragma unroll
+        for (int i = 0; i < KQ; ++i) Q[i] = load16(p + 32 * i);
+    }
+    // K and V of one step into buffer `to`: every lane brings 16 bytes to where they are read from
+    int bad = 0;
+    auto fetch = [&](int to, uint32_t ku, uint32_t vu) {
+        constexpr int PER = C::BUF / 1024 / 4;              // 1 KiB pieces per wave
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int at0 = (wave * PER + j) * 1024, byte = at0 + lane * 16, t = byte / RB, c = (byte % RB) / 16;
+            const uint32_t uk = __shfl(ku, t, 64), uv = __shfl(vu, t, 64);
+            lds_gload16(base + ((uint64_t)uk << 7) + 16 * C::k_swz(t, c), (lds_void *)(smem + to * C::BUF + at0));
+            lds_gload16(base + ((uint64_t)uv << 7) + 16 * C::v_swz(t, c), (lds_void *)(smem + (2 + to) * C::BUF + at0));
+        }
+    };
+
+    f32x16_t acc[ND];
+    float m, l;
+    // Two passes at most.  The first lets tokens behind a row's own position into the products with weight 0, which
+    // is right unless their V holds an infinity or NaN; then a row comes out not finite, and the second
+    // pass takes such values out of the products and adds them to the rows that see them.
+    for (int careful = 0; careful < 2; ++careful) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
+        m = -INFINITY;
+        l = 0.f;
+        int32_t kid, vid;
+        uint32_t ku, vu;
+        const int32_t lt = lane & (NT - 1);
+        lane_ids(a, trow, lt, sq.n, &kid, &vid);
+        uint64_t there = lane_units(a, lt, sq.n, kid, vid, &ku, &vu, &bad), there1 = 0;
+        fetch(0, ku, vu);
+        lane_ids(a, trow, NT + lt, sq.n, &kid, &vid);
+        for (int32_t it = 0; it < steps; ++it) {
+            const int cur = it & 1;
+            const int32_t t0 = it * NT;
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this step's K and V, the next one's page ids
+            __syncthreads();
+            if (it + 1 < steps) {
+                there1 = lane_units(a, t0 + NT + lt, sq.n, kid, vid, &ku, &vu, &bad);
+                fetch(cur ^ 1, ku, vu);
+                lane_ids(a, trow, t0 + 2 * NT + lt, sq.n, &kid, &vid);
+            }
+            const char *kb = smem + cur * C::BUF;
+            char *vb = smem + (2 + cur) * C::BUF;
+            constexpr uint64_t FULL = NT == 64 ? ~0ull : (1ull << (NT & 63)) - 1;
+            const bool full = (there & FULL) == FULL;
+            if (!full) {                                    // rows of tokens that are not there must not reach the products
+                for (int x = tid; x < NT * CH; x += 256)
+                    if (!((there >> (x / CH)) & 1)) store16(vb + 16 * x, u32x4_t{0, 0, 0, 0});
+                __syncthreads();
+            }
+            if (careful && t0 + NT - 1 > wg_lo) {           // some row does not see all of these tokens
+                if (tid == 0) sh_flag = 0;
+                __syncthreads();
+                auto odd = [&](uint32_t w) {                // non-finite parts of a dword, the rest zero
+                    if constexpr (!BF) return (w & 0x7f800000u) == 0x7f800000u ? w : 0u;
+                    else return ((w & 0x7f80u) == 0x7f80u ? w & 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? w & 0xffff0000u : 0u);
+                };
+                for (int x = tid; x < NT * CH; x += 256) {
+                    const u32x4_t w = load16(vb + 16 * x);
+                    if (odd(w[0]) | odd(w[1]) | odd(w[2]) | odd(w[3])) atomicOr(&sh_flag, 1ull << (x / CH));
+                }
+                __syncthreads();
+                unsigned long long flags = sh_flag;
+                if (flags) {
+                    for (unsigned long long f = flags; f; f &= f - 1) {
+                        const int t = __ffsll((long long)f) - 1;
+                        if (t0 + t <= pos) {
+#pragma unroll
+                            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const int byte = (32 * d + 8 * (i / 4) + 4 * hh + (i & 3)) * (int)sizeof(E);
+                                    const E v = *(const E *)(vb + t * RB + 16 * C::v_swz(t, byte / 16) + byte % 16);
+                                    const float x = to_f32(v);
+                                    if (x - x != 0.f) acc[d][i] += x;
+                                }
+                        }
+                    }
+                    __syncthreads();
+                    for (int x = tid; x < NT * CH; x += 256) {
+                        u32x4_t w = load16(vb + 16 * x);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] ^= odd(w[i]);
+                        store16(vb + 16 * x, w);
+                    }
+                    __syncthreads();
+                }
+            }
+            if (t0 <= wave_hi) {
+                __builtin_amdgcn_sched_barrier(0);
+                f32x16_t S[NB];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) S[nb][i] = 0.f;
+#pragma unroll
+                for (int k = 0; k < KQ; ++k)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        const int t = 32 * nb + col;
+                        const u32x4_t f = load16(kb + t * RB + 16 * C::k_swz(t, 2 * k + hh));
+                        if constexpr (BF) {
+                            S[nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, f),
+                                                                            __builtin_bit_cast(bf16x8_t, Q[k]), S[nb], 0, 0, 0);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                S[nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(f[e]), __uint_as_float(Q[k][e]), S[nb], 0, 0, 0);
+                        }
+                    }
+                // K pieces come out of LDS three products ahead
+                __builtin_amdgcn_sched_group_barrier(0x100, 3 * NB, 0);
+#pragma unroll
+                for (int k = 0; k < KQ; ++k) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, NB * (BF ? 1 : 4), 0);
+                    if (k + 3 < KQ) __builtin_amdgcn_sched_group_barrier(0x100, NB, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                float mt = -INFINITY, sc = scale2;
+                if (!(scale2 > 0.f)) {                      // the largest logit need not be the largest product's
+                    sc = 1.f;
+                    float by = scale2;
+                    asm volatile("" : "+v"(by));            // keeps the products inside the branch
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) S[nb][i] *= by;
+                }
+                if (!full || t0 + NT - 1 > wave_lo) {       // tokens counted from this lane half's first
+                    const int32_t last = pos - t0 - 4 * hh;
+                    const uint64_t in = there >> (4 * hh);
+                    const uint32_t in0 = (uint32_t)in, in1 = (uint32_t)(in >> 32);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int t = 8 * (i / 4) + (i & 3);
+                            if (32 * nb + t > last || !((nb ? in1 : in0) & (1u << t))) S[nb][i] = -INFINITY;
+                        }
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) mt = fmaxf(mt, S[nb][i]);
+                mt *= sc;
+                mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
+                // The running maximum moves only when a logit passes it by 8: until then weights up to 2^8 do no
+                // harm, and the accumulators need no rescaling.
+                if (__any(mt > m + 8.f)) {
+                    const float mn = fmaxf(m, mt), ms = mn == -INFINITY ? 0.f : mn;
+                    const float c = exp2_fast(m - ms);
+                    m = mn;
+                    l *= c;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[d][i] *= c;
+                }
+                const float ms = m == -INFINITY ? 0.f : m;
+                float ps = 0.f;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        S[nb][i] = exp2_fast(S[nb][i] * sc - ms);
+                        ps += S[nb][i];
+                    }
+                l += ps;
+                if constexpr (BF) {
+#pragma unroll
+                    for (int s = 0; s < NT / 16; ++s) {
+                        u32x4_t p;                          // this lane's eight weights: tokens 16 s + 4 hh + 0..3 and 8 on
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int i = 8 * (s & 1) + 2 * x;
+                            p[x] = pack2(S[s / 2][i], S[s / 2][i + 1]);
+                        }
+                        const int i16 = lane & 15, t = 16 * s + 4 * hh + (i16 >> 2);
+#pragma unroll
+                        for (int d = 0; d < ND; ++d) {
+                            const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
+                            const char *ad = vb + t * RB + 16 * C::v_swz(t, c) + 8 * (i16 & 1);
+                            const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)ad);
+                            const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(ad + 8 * RB));
+                            typedef short s16x8_t __attribute__((ext_vector_type(8)));
+                            const s16x8_t v = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+                            acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v),
+                                                                             __builtin_bit_cast(bf16x8_t, p), acc[d], 0, 0, 0);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int t = 8 * (i / 4) + 4 * hh + (i & 3);
+#pragma unroll
+                        for (int d = 0; d < ND; ++d)
+                            acc[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(*(const float *)(vb + t * RB + 4 * (32 * d + col)), S[0][i],
+                                                                          acc[d], 0, 0, 0);
+                    }
+                }
+            }
+            there = there1;
+        }
+        __syncthreads();
+        if (careful) break;
+        float chk = 0.f;                                    // 0, or NaN where a sum is not finite
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) chk += acc[d][i] * 0.f;
+        if (!__syncthreads_or(chk != 0.f)) break;
+    }
+    if (bad) record(a, bad);
+    const float L = l + __shfl_xor(l, 32, 64), inv = L == 0.f ? 0.f : 1.f / L;
+    if (ck.stats && row_ok && hh == 0) ck.stats[row * a.n_heads + head] = make_float2(m == -INFINITY ? 0.f : m, inv);
+    if constexpr (BF) {
+        // rows through LDS, so that a row leaves in one piece
+        constexpr int OB = RB + 16;
+        char *o = smem + wave * 32 * OB;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint2 w = make_uint2(pack2(acc[d][4 * x] * inv, acc[d][4 * x + 1] * inv),
+                                     pack2(acc[d][4 * x + 2] * inv, acc[d][4 * x + 3] * inv));
+                *(uint2 *)(o + col * OB + (32 * d + 8 * x + 4 * hh) * 2) = w;
+            }
+        __builtin_amdgcn_wave_barrier();
+        E *out = (E *)at.out + (sq.first + (int64_t)q0) * at.ldo + (int64_t)head * HD;
+        for (int x = lane; x < 32 * CH; x += 64) {
+            const int r = x / CH, c = x % CH;
+            if (q0 + r < sq.m) store16(out + r * at.ldo + 8 * c, load16(o + r * OB + 16 * c));
+        }
+    } else if (row_ok) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                *(float4 *)(orow + 32 * d + 8 * x + 4 * hh) = make_float4(acc[d][4 * x] * inv, acc[d][4 * x + 1] * inv,
+                                                                        acc[d][4 * x + 2] * inv, acc[d][4 * x + 3] * inv);
+    }
+}
+
+// ---- scores: the weights once more, summed over the rows ---------------------------------------------
+// A token's weights can be summed only when its rows' maxima and sums are known.  One workgroup takes 4 * TB * 32
+// tokens of one K/V head, K in registers, and walks the query rows of the heads that share it; the logits are
+// multiplied again (half of the attention's products), and a lane sums its query rows' weights for each of its tokens.
+template <typename E, int HD>
+struct Scores {
+    static constexpr bool BF = sizeof(E) == 2;
+    static constexpr int RB = HD * (int)sizeof(E);
+    static constexpr int TB = !BF && HD == 256 ? 1 : 2;     // blocks of 32 tokens a wave holds
+    static constexpr int TOK = 4 * TB * 32;
+    static constexpr int NQ = 32;                           // query rows of a step
+    static constexpr int BUF = NQ * RB;
+    static constexpr int WAVES = RB > 256 ? 1 : 2;
+};
+
+template <typename E, int HD>
+__global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores(KvArgs a, KvAttend at, KvChunk ck) {
+    using P = Scores<E, HD>;
+    using C = Chunk<E, HD>;
+    constexpr int RB = P::RB, TB = P::TB, KQ = C::KQ, NQ = P::NQ;
+    constexpr bool BF = P::BF;
+    __shared__ __align__(256) char smem[2 * P::BUF];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, hh = lane >> 5;
+    const int32_t b = blockIdx.z, kvh = blockIdx.y, t0 = blockIdx.x * P::TOK;
+    const SeqRows sq = seq_rows(a, b);
+    if (t0 >= sq.n) return;
+    const int32_t old = sq.n - sq.m, tw = t0 + wave * TB * 32;
+    const float scale2 = at.scale * 1.4426950408889634f;
+    const int32_t *trow = a.table + (int64_t)b * 2 * a.max_pages;
+
+    u32x4_t K[TB][KQ];
+    uint32_t there = 0;                                     // one bit per block: the lane's token (row `col`)
+    int bad = 0;
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) {
+        int32_t kid, vid;
+        uint32_t ku, vu;
+        const int32_t tok = tw + 32 * tb + col;
+        lane_ids(a, trow, tok, sq.n, &kid, &vid);
+        const uint64_t ok = lane_units(a, tok, sq.n, kid, vid, &ku, &vu, &bad);
+        there |= (uint32_t)((ok >> lane) & 1) << tb;
+        const char *p = a.pages + ((uint64_t)ku << 7) + (int64_t)kvh * RB + 16 * hh;
+#pragma unroll
+        for (int k = 0; k < KQ; ++k) K[tb][k] = load16(p + 32 * k);
+    }
+    f32x16_t sum[TB];
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[tb][i] = 0.f;
+
+    // steps: for each head of the group, NQ query rows at a time from the first that sees token t0
+    const int32_t r0 = max(0, t0 - old) / NQ * NQ, per = sq.m > r0 ? (sq.m - r0 + NQ - 1) / NQ : 0;
+    const int32_t steps = per * a.group;
+    auto fetch = [&](int32_t it) {
+        const int32_t h = kvh * a.group + it / per, r = r0 + it % per * NQ;
+        constexpr int PER = (P::BUF / 1024 + 3) / 4;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int at0 = (wave * PER + j) * 1024, byte = at0 + lane * 16, q = byte / RB, c = (byte % RB) / 16;
+            if (at0 < P::BUF)
+                lds_gload16((const char *)((const E *)at.q + (sq.first + (int64_t)min(r + q, sq.m - 1)) * at.ldq + (int64_t)h * HD) +
+                                16 * C::k_swz(q, c),
+                            (lds_void *)(smem + (it & 1) * P::BUF + at0));
+        }
+    };
+    auto stat = [&](int32_t it) {
+        const int32_t h = kvh * a.group + it / per, r = r0 + it % per * NQ + col;
+        float2 s = ck.stats[(sq.first + (int64_t)min(r, sq.m - 1)) * a.n_heads + h];
+        if (r >= sq.m) s.y = 0.f;
+        return s;
+    };
+    float2 st = make_float2(0.f, 0.f), st1 = st;
+    if (steps) {
+        fetch(0);
+        st1 = stat(0);
+    }
+    for (int32_t it = 0; it < steps; ++it) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        st = st1;
+        if (it + 1 < steps) {
+            fetch(it + 1);
+            st1 = stat(it + 1);
+        }
+        const char *qb = smem + (it & 1) * P::BUF;
+        const int32_t r = r0 + it % per * NQ, hi = old + min(r + NQ, sq.m) - 1;   // the step's last position
+        if (tw > hi) continue;
+        f32x16_t S[TB];
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[tb][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KQ; ++k) {
+            const u32x4_t f = load16(qb + col * RB + 16 * C::k_swz(col, 2 * k + hh));
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb) {
+                if constexpr (BF) {
+                    S[tb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, K[tb][k]),
+                                                                    __builtin_bit_cast(bf16x8_t, f), S[tb], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        S[tb] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(K[tb][k][e]), __uint_as_float(f[e]), S[tb], 0, 0, 0);
+                }
+            }
+        }
+        const int32_t pos = old + r + col;
+        const bool edge = tw + TB * 32 - 1 > old + r;       // some row does not see all of the wave's tokens
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float w = exp2_fast(S[tb][i] * scale2 - st.x) * st.y;
+                if (edge && tw + 32 * tb + 8 * (i / 4) + 4 * hh + (i & 3) > pos) w = 0.f;
+                sum[tb][i] += w;
+            }
+    }
+    if (bad) record(a, bad);
+    float *out = ck.part + ((int64_t)b * a.n_kv + kvh) * ck.cap_ld;
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = sum[tb][i];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) v += __shfl_xor(v, o, 64);
+            const int t = 8 * (i / 4) + 4 * hh + (i & 3);
+            const bool ok = (__shfl(there, t, 64) >> tb) & 1;
+            const int32_t tok = tw + 32 * tb + t;
+            if (col == 0 && tok < sq.n) out[tok] = ok ? v : 0.f;
+        }
+}
+
+__global__ __launch_bounds__(256) void k_kv_chunk_sum(KvArgs a, KvAttend at, KvChunk ck) {
+    const int32_t b = blockIdx.y, t = blockIdx.x * 256 + threadIdx.x;
+    const SeqRows sq = seq_rows(a, b);
+    if (t >= sq.n) return;
+    float s = 0.f;
+    const float *p = ck.part + (int64_t)b * a.n_kv * ck.cap_ld + t;
+#pragma unroll 8
+    for (int32_t h = 0; h < a.n_kv; ++h) s += p[(int64_t)h * ck.cap_ld];
+    const int64_t i = (int64_t)b * at.score_ld + t;
+    at.scores[i] = (at.prior ? at.prior[i] : 0.f) + s;
+}
+
+// ---- host ------------------------------------------------------------------------------------------
+namespace {
+
+size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+template <typename E, int HD>
+hipError_t run(const KvArgs &a, const KvAttend &at, hipStream_t s) {
+    using C = Chunk<E, HD>;
+    KvChunk ck;
+    ck.hpw = a.group % 4 == 0 ? 4 : a.group % 2 == 0 ? 2 : 1;
+    const int32_t tq = 128 / ck.hpw;
+    ck.slots = a.T / tq + std::min(a.n_seq, a.T);
+    ck.cap_ld = ((int64_t)a.cap + 63) / 64 * 64;
+    ck.stats = at.scores ? (float2 *)at.ws : nullptr;
+    ck.part = (float *)((char *)at.ws + up256((size_t)a.T * a.n_heads * 8));
+    constexpr int OUT = C::BF ? 4 * 32 * (C::RB + 16) : 0, LDS = std::max(C::LDS, OUT);
+    static const hipError_t attr = hipFuncSetAttribute((const void *)k_kv_chunk<E, HD>, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+    if (attr != hipSuccess) return attr;
+    const int64_t grid = (int64_t)ck.slots * (a.n_heads / ck.hpw);
+    hipLaunchKernelGGL((k_kv_chunk<E, HD>), dim3((unsigned)grid), dim3(256), LDS, s, a, at, ck);
+    if (at.scores) {
+        constexpr int TOK = Scores<E, HD>::TOK;
+        hipLaunchKernelGGL((k_kv_chunk_scores<E, HD>), dim3((a.cap + TOK - 1) / TOK, a.n_kv, a.n_seq), dim3(256), 0, s, a, at, ck);
+        hipLaunchKernelGGL(k_kv_chunk_sum, dim3((a.cap + 255) / 256, a.n_seq), dim3(256), 0, s, a, at, ck);
+    }
+    return hipGetLastError();
+}
+
+template <typename E>
+hipError_t by_dim(const KvArgs &a, const KvAttend &at, hipStream_t s) {
+    return a.head_dim == 64 ? run<E, 64>(a, at, s) : a.head_dim == 128 ? run<E, 128>(a, at, s) : run<E, 256>(a, at, s);
+}
+
+}  // namespace
+
+size_t kv_chunk_ws_bytes(int, const lora_kv_layout_t &l, int32_t n_seq, int64_t T, int64_t max_len, bool scores) {
+    if (!scores) return 0;
+    return up256((size_t)T * l.n_heads * 8) + (size_t)n_seq * l.n_kv_heads * ((max_len + 63) / 64 * 64) * 4;
+}
+
+hipError_t launch_kv_chunk(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s) {
+    return dtype == LORA_F32 ? by_dim<float>(a, at, s) : by_dim<uint16_t>(a, at, s);
+}
+
+}  // namespace lorapool

@@ -159,6 +159,18 @@ def test_chunk_shapes(geo, dtype, lens, new):
     check(Case(geo, dtype, lens, new, seed=4, gap=1))
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+@pytest.mark.parametrize("new", [None, [50, 97, 1, 64]])
+def test_any_scale(new, scale):
+    """A scale of zero weighs all tokens alike; a negative one turns the order round."""
+    c = Case("gqa64", "bf16", [50, 129, 300, 64], new)
+    c.scale = scale
+    want, tol, sw, stol = c.ref()
+    sc = torch.zeros((c.n, c.cap), device="cuda")
+    close(c.run(scale=scale, scores=sc), want, tol, c.dt, "out")
+    close(sc, sw, stol, torch.float32, "scores")
+
+
 @pytest.mark.parametrize("new", [None, [50, 129, 1, 64]])
 def test_rows_of_a_wider_matrix(new):
     """q and out as column ranges of wider buffers: the columns beside them stay as they were."""
