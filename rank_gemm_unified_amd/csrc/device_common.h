@@ -24,6 +24,11 @@ __device__ __forceinline__ void lds_gload16(const void *src, lds_void *dst) {
     __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
 }
 
+// 4 bytes a lane: lane l's land at dst + 4 l.
+__device__ __forceinline__ void lds_gload4(const void *src, lds_void *dst) {
+    __builtin_amdgcn_global_load_lds(src, dst, 4, 0, 0);
+}
+
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
 
 // Round-to-nearest-even float32 -> bfloat16 bits; NaN stays NaN (quiet bit set).

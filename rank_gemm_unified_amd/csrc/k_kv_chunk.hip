@@ -10,6 +10,7 @@
 // in place as the right operand of the second: the weights never leave their registers.  V^T comes out of
 // LDS through the transposing read.  Two workgroups a CU: one's softmax runs under the other's products.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_device.h"
 
@@ -21,6 +22,10 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
+// The transposing read.  (Behind a restrict pointer: the compiler else takes it for a reader of the loads to LDS that
+// are in flight, and waits for them.  The waits that are needed are written out.)
+__device__ __forceinline__ s16x4_t read_tr(lds_s16x4 *__restrict__ p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p); }
+
 struct KvChunk {
     int32_t hpw;              // query heads of one K/V head a workgroup takes: 1, 2 or 4
     int32_t slots;            // query tiles, at most
@@ -29,6 +34,7 @@ struct KvChunk {
     int64_t cap_ld;
 };
 
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {   // two floats to bfloat16, round to nearest even
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
@@ -38,13 +44,14 @@ template <typename E, int HD>
 struct Chunk {
     static constexpr bool BF = sizeof(E) == 2;
     static constexpr int NT = BF ? 64 : 32;                 // tokens of a step
+    static constexpr int NB = NT / 32;
     static constexpr int RB = HD * (int)sizeof(E);          // bytes of a token's row
     static constexpr int CH = RB / 16;                      // 16-byte pieces of it
     static constexpr int BUF = NT * RB;
-    static constexpr int LDS = 4 * BUF;                     // K and V, two steps each
-    static constexpr int WAVES = LDS > 64 * 1024 ? 1 : 2;   // workgroups a CU
+    static constexpr int LDS = 4 * BUF + 6 * 1024 + 64;     // two steps of K and of V; addresses, page ids, a bit of 512 tokens
+    static constexpr int WAVES = HD == 256 ? 1 : 2;         // workgroups a CU (registers)
     static constexpr int KQ = BF ? HD / 16 : HD / 8;        // 16-byte pieces of a query row a lane holds
-    static constexpr int NB = NT / 32;                      // blocks of 32 tokens
+    static constexpr int PER = BUF / 4096;                  // 1 KiB pieces of a step's K a wave brings
     // Where piece c of row t lies in LDS.  What one cycle reads has to lie in different banks (256 bytes of them): of
     // K one piece of 16 rows, of V (bfloat16, transposing read) two neighbouring pairs of pieces of four rows.
     static __device__ __forceinline__ int k_swz(int t, int c) { return c ^ (CH == 8 ? t >> 1 & 7 : t & 15); }
@@ -109,19 +116,23 @@ __device__ __forceinline__ int32_t find_tile(const KvArgs &a, int32_t slot, int3
 template <typename E, int HD>
 __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs a, KvAttend at, KvChunk ck) {
     using C = Chunk<E, HD>;
-    constexpr int NT = C::NT, RB = C::RB, CH = C::CH, KQ = C::KQ, NB = C::NB, ND = HD / 32;
+    constexpr int NT = C::NT, NB = C::NB, RB = C::RB, CH = C::CH, KQ = C::KQ, ND = HD / 32;
     constexpr bool BF = C::BF;
     extern __shared__ __align__(256) char smem[];
     __shared__ int32_t sh[6];
     __shared__ unsigned long long sh_flag;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, hh = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 31, hh = lane >> 5;
     const int32_t groups = a.n_heads / ck.hpw, hg = blockIdx.x % groups, slot = blockIdx.x / groups;
     if (blockIdx.x == 0) check_seqs(a);
     const int32_t tq = 128 / ck.hpw;
     int32_t tile;
-    const int32_t b = find_tile(a, slot, tq, &tile, sh);
+    const int32_t b = uniform(find_tile(a, slot, tq, &tile, sh));
     if (b < 0) return;
-    const SeqRows sq = seq_rows(a, b);
+    tile = uniform(tile);
+    SeqRows sq = seq_rows(a, b);
+    sq.first = uniform(sq.first);
+    sq.m = uniform(sq.m);
+    sq.n = uniform(sq.n);
     const int32_t head = hg * ck.hpw + (wave & (ck.hpw - 1)), q0 = tile * tq + (wave / ck.hpw) * 32;
     const int32_t qi = q0 + col;
     const bool row_ok = qi < sq.m;
@@ -148,58 +159,110 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
 #pragma unroll
         for (int i = 0; i < KQ; ++i) Q[i] = load16(p + 32 * i);
     }
-    // K and V of one step into buffer `to`: every lane brings 16 bytes to where they are read from
+    // Where the tokens' rows lie, PH tokens at a time: a thread looks one token's pages up and leaves the addresses in
+    // LDS, in units of 128 bytes (every token row starts on one); tokens that are not there get the pool's first page.
+    constexpr int PH = 256, SP = PH / NT;                   // steps they last for
+    uint32_t *units = (uint32_t *)(smem + 4 * C::BUF);           // [2][K, V][PH]
+    int32_t *raw = (int32_t *)(units + 4 * PH) + 64 * wave;             // [K, V][PH]: page ids, this wave's 64 tokens
+    uint64_t *masks = (uint64_t *)((uint32_t *)(smem + 4 * C::BUF) + 6 * PH);   // [2][PH / 64]: which tokens are there
     int bad = 0;
-    auto fetch = [&](int to, uint32_t ku, uint32_t vu) {
-        constexpr int PER = C::BUF / 1024 / 4;              // 1 KiB pieces per wave
+    auto look_up = [&](int32_t ph) {                        // page ids on their way to LDS (from the table's first entry
+        const int32_t tok = ph * PH + tid;                  // where no token is)
+        int32_t e, slot;
+        page_of(a, tok, &e, &slot);
+        const int32_t *p = trow + (tok < sq.n ? e : 0);
+        lds_gload4(p, (lds_void *)raw);
+        lds_gload4(p + a.max_pages, (lds_void *)(raw + PH));
+    };
+    auto place = [&](int32_t ph) {
+        const int32_t tok = ph * PH + tid, kid = raw[lane], vid = raw[PH + lane];
+        int32_t e, slot;
+        page_of(a, tok, &e, &slot);
+        const bool token = tok < sq.n && tok < steps * NT;
+        const bool ok = token && kid >= 0 && vid >= 0 && kid < a.num_pages && vid < a.num_pages;
+        if (token && !ok) bad = DEV_ERR_PAGE;
+        const uint32_t pu = (uint32_t)(a.page_bytes >> 7), at0 = (uint32_t)slot * (uint32_t)(a.tok_bytes >> 7);
+        uint32_t *u = units + (ph & 1) * 2 * PH + tid;
+        u[0] = ok ? (uint32_t)kid * pu + at0 : 0u;
+        u[PH] = ok ? (uint32_t)vid * pu + at0 : 0u;
+        const uint64_t there = __ballot(ok);
+        if (lane == 0) masks[(ph & 1) * (PH / 64) + wave] = there;
+    };
+    // K and V of step j to LDS: every lane brings 16 bytes to where they are read from.
+    auto fetch = [&](int32_t j) {
+        const uint32_t *uk = units + (j / SP & 1) * 2 * PH + j % SP * NT, *uv = uk + PH;
+        char *kb = smem + (j & 1) * C::BUF, *vb = smem + (2 + (j & 1)) * C::BUF;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int at0 = (wave * PER + j) * 1024, byte = at0 + lane * 16, t = byte / RB, c = (byte % RB) / 16;
-            const uint32_t uk = __shfl(ku, t, 64), uv = __shfl(vu, t, 64);
-            lds_gload16(base + ((uint64_t)uk << 7) + 16 * C::k_swz(t, c), (lds_void *)(smem + to * C::BUF + at0));
-            lds_gload16(base + ((uint64_t)uv << 7) + 16 * C::v_swz(t, c), (lds_void *)(smem + (2 + to) * C::BUF + at0));
+        for (int x = 0; x < C::PER; ++x) {
+            const int at0 = (wave * C::PER + x) * 1024, byte = at0 + lane * 16, t = byte / RB, c = (byte % RB) / 16;
+            lds_gload16(base + ((uint64_t)uk[t] << 7) + 16 * C::k_swz(t, c), (lds_void *)(kb + at0));
+            lds_gload16(base + ((uint64_t)uv[t] << 7) + 16 * C::v_swz(t, c), (lds_void *)(vb + at0));
         }
     };
+    auto other_half = [](float x) {                          // the value of the lane 32 further, or before
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        return __uint_as_float(threadIdx.x & 32 ? r[0] : r[1]);
+    };
 
-    f32x16_t acc[ND];
+    f32x16_t acc[ND], S[NB];
     float m, l;
+    // S^T = K Q^T of one step
+    auto logits = [&](const char *kb, f32x16_t (&x)[NB]) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[nb][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KQ; ++k)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const u32x4_t f = load16(kb + (32 * nb + col) * RB + 16 * C::k_swz(col, 2 * k + hh));
+                if constexpr (BF) {
+                    x[nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, f), __builtin_bit_cast(bf16x8_t, Q[k]), x[nb], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(f[e]), __uint_as_float(Q[k][e]), x[nb], 0, 0, 0);
+                }
+            }
+    };
     // Two passes at most.  The first lets tokens behind a row's own position into the products with weight 0, which
     // is right unless their V holds an infinity or NaN; then a row comes out not finite, and the second
     // pass takes such values out of the products and adds them to the rows that see them.
-    for (int careful = 0; careful < 2; ++careful) {
+    auto pass = [&](auto careful) {
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
         m = -INFINITY;
         l = 0.f;
-        int32_t kid, vid;
-        uint32_t ku, vu;
-        const int32_t lt = lane & (NT - 1);
-        lane_ids(a, trow, lt, sq.n, &kid, &vid);
-        uint64_t there = lane_units(a, lt, sq.n, kid, vid, &ku, &vu, &bad), there1 = 0;
-        fetch(0, ku, vu);
-        lane_ids(a, trow, NT + lt, sq.n, &kid, &vid);
-        for (int32_t it = 0; it < steps; ++it) {
-            const int cur = it & 1;
-            const int32_t t0 = it * NT;
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this step's K and V, the next one's page ids
-            __syncthreads();
-            if (it + 1 < steps) {
-                there1 = lane_units(a, t0 + NT + lt, sq.n, kid, vid, &ku, &vu, &bad);
-                fetch(cur ^ 1, ku, vu);
-                lane_ids(a, trow, t0 + 2 * NT + lt, sq.n, &kid, &vid);
-            }
-            const char *kb = smem + cur * C::BUF;
-            char *vb = smem + (2 + cur) * C::BUF;
-            constexpr uint64_t FULL = NT == 64 ? ~0ull : (1ull << (NT & 63)) - 1;
-            const bool full = (there & FULL) == FULL;
-            if (!full) {                                    // rows of tokens that are not there must not reach the products
+        look_up(0);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        place(0);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        look_up(1);
+        __builtin_amdgcn_s_barrier();
+        fetch(0);
+        for (int32_t j = 0; j < steps; ++j) {
+            const int32_t t0 = j * NT;
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // this step's K and V are in
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            fetch(j + 1);
+            if ((j + 2) % SP == 0) place((j + 2) / SP);     // before the first fetch from there, at the next step
+            if ((j + 3) % SP == 0) look_up((j + 3) / SP);
+            const int32_t at64 = t0 % (2 * PH) / 64;
+            const uint64_t word = (uint64_t)(uint32_t)uniform((int32_t)(masks[at64] >> 32)) << 32 | (uint32_t)uniform((int32_t)masks[at64]);
+            const uint64_t there = NT == 64 ? word : word >> (t0 & 32) & 0xffffffffu;
+            constexpr uint64_t ALL = NT == 64 ? ~0ull : 0xffffffffu;
+            char *vb = smem + (2 + (j & 1)) * C::BUF;
+            if (there != ALL) {                             // rows of tokens that are not there must not reach the products
                 for (int x = tid; x < NT * CH; x += 256)
                     if (!((there >> (x / CH)) & 1)) store16(vb + 16 * x, u32x4_t{0, 0, 0, 0});
-                __syncthreads();
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
             }
-            if (careful && t0 + NT - 1 > wg_lo) {           // some row does not see all of these tokens
+            if (careful.value && t0 + NT - 1 > wg_lo) {     // some row does not see all of these tokens
                 if (tid == 0) sh_flag = 0;
                 __syncthreads();
                 auto odd = [&](uint32_t w) {                // non-finite parts of a dword, the rest zero
@@ -211,8 +274,7 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
                     if (odd(w[0]) | odd(w[1]) | odd(w[2]) | odd(w[3])) atomicOr(&sh_flag, 1ull << (x / CH));
                 }
                 __syncthreads();
-                unsigned long long flags = sh_flag;
-                if (flags) {
+                if (const unsigned long long flags = sh_flag) {
                     for (unsigned long long f = flags; f; f &= f - 1) {
                         const int t = __ffsll((long long)f) - 1;
                         if (t0 + t <= pos) {
@@ -221,8 +283,7 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) {
                                     const int byte = (32 * d + 8 * (i / 4) + 4 * hh + (i & 3)) * (int)sizeof(E);
-                                    const E v = *(const E *)(vb + t * RB + 16 * C::v_swz(t, byte / 16) + byte % 16);
-                                    const float x = to_f32(v);
+                                    const float x = to_f32(*(const E *)(vb + t * RB + 16 * C::v_swz(t, byte / 16) + byte % 16));
                                     if (x - x != 0.f) acc[d][i] += x;
                                 }
                         }
@@ -237,132 +298,111 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
                     __syncthreads();
                 }
             }
-            if (t0 <= wave_hi) {
-                __builtin_amdgcn_sched_barrier(0);
-                f32x16_t S[NB];
+            if (t0 > wave_hi) continue;
+            __builtin_amdgcn_sched_barrier(0);
+            logits(smem + (j & 1) * C::BUF, S);
+            // K pieces come out of LDS three products ahead
+            __builtin_amdgcn_sched_group_barrier(0x100, 3 * NB, 0);
+#pragma unroll
+            for (int k = 0; k < KQ; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, NB * (BF ? 1 : 4), 0);
+                if (k + 3 < KQ) __builtin_amdgcn_sched_group_barrier(0x100, NB, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            float sc = scale2;
+            if (!(scale2 > 0.f)) {                          // the largest logit need not be the largest product's
+                sc = 1.f;
+                float by = scale2;
+                asm volatile("" : "+v"(by));                // keeps the products inside the branch
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) S[nb][i] = 0.f;
+                    for (int i = 0; i < 16; ++i) S[nb][i] *= by;
+            }
+            if (there != ALL || t0 + NT - 1 > wave_lo) {    // tokens counted from this lane half's first
+                const int32_t last = pos - t0 - 4 * hh;
+                const uint64_t in = there >> (4 * hh);
+                const uint32_t in0 = (uint32_t)in, in1 = (uint32_t)(in >> 32);
 #pragma unroll
-                for (int k = 0; k < KQ; ++k)
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        const int t = 32 * nb + col;
-                        const u32x4_t f = load16(kb + t * RB + 16 * C::k_swz(t, 2 * k + hh));
-                        if constexpr (BF) {
-                            S[nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, f),
-                                                                            __builtin_bit_cast(bf16x8_t, Q[k]), S[nb], 0, 0, 0);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                S[nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(f[e]), __uint_as_float(Q[k][e]), S[nb], 0, 0, 0);
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        const int t = 8 * (i / 4) + (i & 3);
+                        if (32 * nb + t > last || !((nb ? in1 : in0) & (1u << t))) S[nb][i] = -INFINITY;
                     }
-                // K pieces come out of LDS three products ahead
-                __builtin_amdgcn_sched_group_barrier(0x100, 3 * NB, 0);
+            }
+            float mt = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < KQ; ++k) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, NB * (BF ? 1 : 4), 0);
-                    if (k + 3 < KQ) __builtin_amdgcn_sched_group_barrier(0x100, NB, 0);
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) mt = fmaxf(mt, S[nb][i]);
+            mt = fmaxf(mt, other_half(mt)) * sc;
+            // The running maximum moves only when a logit passes it by 8: until then weights up to 2^8 do no
+            // harm, and the accumulators need no rescaling.
+            if (__any(mt > m + 8.f)) {
+                const float mn = fmaxf(m, mt), ms = mn == -INFINITY ? 0.f : mn;
+                const float c = exp2_fast(m - ms);
+                m = mn;
+                l *= c;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[d][i] *= c;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const float ms = m == -INFINITY ? 0.f : m;
+            float ps = 0.f;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    S[nb][i] = exp2_fast(S[nb][i] * sc - ms);
+                    ps += S[nb][i];
                 }
-                __builtin_amdgcn_sched_barrier(0);
-                float mt = -INFINITY, sc = scale2;
-                if (!(scale2 > 0.f)) {                      // the largest logit need not be the largest product's
-                    sc = 1.f;
-                    float by = scale2;
-                    asm volatile("" : "+v"(by));            // keeps the products inside the branch
+            l += ps;
+            if constexpr (BF) {
+                const int i16 = lane & 15;
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
+                for (int s = 0; s < NT / 16; ++s) {
+                    u32x4_t p;                              // this lane's eight weights: tokens 16 s + 4 hh + 0..3 and 8 on
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) S[nb][i] *= by;
+                    for (int x = 0; x < 4; ++x) p[x] = pack2(S[s / 2][8 * (s & 1) + 2 * x], S[s / 2][8 * (s & 1) + 2 * x + 1]);
+                    const int t = 16 * s + 4 * hh + (i16 >> 2);
+#pragma unroll
+                    for (int d = 0; d < ND; ++d) {
+                        const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
+                        const char *ad = vb + t * RB + 16 * C::v_swz(t, c) + 8 * (i16 & 1);
+                        const s16x4_t v0 = read_tr((lds_s16x4 *)ad);
+                        const s16x4_t v1 = read_tr((lds_s16x4 *)(ad + 8 * RB));
+                        typedef short s16x8_t __attribute__((ext_vector_type(8)));
+                        const s16x8_t v = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+                        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v),
+                                                                         __builtin_bit_cast(bf16x8_t, p), acc[d], 0, 0, 0);
+                    }
                 }
-                if (!full || t0 + NT - 1 > wave_lo) {       // tokens counted from this lane half's first
-                    const int32_t last = pos - t0 - 4 * hh;
-                    const uint64_t in = there >> (4 * hh);
-                    const uint32_t in0 = (uint32_t)in, in1 = (uint32_t)(in >> 32);
+            } else {
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int t = 8 * (i / 4) + (i & 3);
-                            if (32 * nb + t > last || !((nb ? in1 : in0) & (1u << t))) S[nb][i] = -INFINITY;
-                        }
-                }
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) mt = fmaxf(mt, S[nb][i]);
-                mt *= sc;
-                mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
-                // The running maximum moves only when a logit passes it by 8: until then weights up to 2^8 do no
-                // harm, and the accumulators need no rescaling.
-                if (__any(mt > m + 8.f)) {
-                    const float mn = fmaxf(m, mt), ms = mn == -INFINITY ? 0.f : mn;
-                    const float c = exp2_fast(m - ms);
-                    m = mn;
-                    l *= c;
+                for (int i = 0; i < 16; ++i) {
+                    const int t = 8 * (i / 4) + 4 * hh + (i & 3);
 #pragma unroll
                     for (int d = 0; d < ND; ++d)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[d][i] *= c;
-                }
-                const float ms = m == -INFINITY ? 0.f : m;
-                float ps = 0.f;
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        S[nb][i] = exp2_fast(S[nb][i] * sc - ms);
-                        ps += S[nb][i];
-                    }
-                l += ps;
-                if constexpr (BF) {
-#pragma unroll
-                    for (int s = 0; s < NT / 16; ++s) {
-                        u32x4_t p;                          // this lane's eight weights: tokens 16 s + 4 hh + 0..3 and 8 on
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int i = 8 * (s & 1) + 2 * x;
-                            p[x] = pack2(S[s / 2][i], S[s / 2][i + 1]);
-                        }
-                        const int i16 = lane & 15, t = 16 * s + 4 * hh + (i16 >> 2);
-#pragma unroll
-                        for (int d = 0; d < ND; ++d) {
-                            const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
-                            const char *ad = vb + t * RB + 16 * C::v_swz(t, c) + 8 * (i16 & 1);
-                            const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)ad);
-                            const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(ad + 8 * RB));
-                            typedef short s16x8_t __attribute__((ext_vector_type(8)));
-                            const s16x8_t v = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
-                            acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v),
-                                                                             __builtin_bit_cast(bf16x8_t, p), acc[d], 0, 0, 0);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int t = 8 * (i / 4) + 4 * hh + (i & 3);
-#pragma unroll
-                        for (int d = 0; d < ND; ++d)
-                            acc[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(*(const float *)(vb + t * RB + 4 * (32 * d + col)), S[0][i],
-                                                                          acc[d], 0, 0, 0);
-                    }
+                        acc[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(*(const float *)(vb + t * RB + 4 * (32 * d + col)), S[0][i], acc[d], 0, 0, 0);
                 }
             }
-            there = there1;
+            __builtin_amdgcn_sched_barrier(0);
         }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // no load is on its way to LDS any more
         __syncthreads();
-        if (careful) break;
-        float chk = 0.f;                                    // 0, or NaN where a sum is not finite
+    };
+    pass(std::false_type{});
+    float chk = 0.f;                                        // 0, or NaN where a sum is not finite
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
+    for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) chk += acc[d][i] * 0.f;
-        if (!__syncthreads_or(chk != 0.f)) break;
-    }
+        for (int i = 0; i < 16; ++i) chk += acc[d][i] * 0.f;
+    if (__syncthreads_or(chk != 0.f)) pass(std::true_type{});
     if (bad) record(a, bad);
-    const float L = l + __shfl_xor(l, 32, 64), inv = L == 0.f ? 0.f : 1.f / L;
+    const float L = l + other_half(l), inv = L == 0.f ? 0.f : 1.f / L;
     if (ck.stats && row_ok && hh == 0) ck.stats[row * a.n_heads + head] = make_float2(m == -INFINITY ? 0.f : m, inv);
     if constexpr (BF) {
         // rows through LDS, so that a row leaves in one piece
