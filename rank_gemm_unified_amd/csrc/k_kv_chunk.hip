@@ -442,7 +442,7 @@ struct Scores {
     static constexpr int RB = HD * (int)sizeof(E);
     static constexpr int TB = !BF && HD == 256 ? 1 : 2;     // blocks of 32 tokens a wave holds
     static constexpr int TOK = 4 * TB * 32;
-    static constexpr int NQ = 32;                           // query rows of a step
+    static constexpr int NQ = RB > 256 ? 32 : 64;           // query rows of a step
     static constexpr int BUF = NQ * RB;
     static constexpr int WAVES = RB > 256 ? 1 : 2;
 };
@@ -498,73 +498,95 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
                             (lds_void *)(smem + (it & 1) * P::BUF + at0));
         }
     };
+    float2 st[NQ / 32], st1[NQ / 32];
     auto stat = [&](int32_t it) {
-        const int32_t h = kvh * a.group + it / per, r = r0 + it % per * NQ + col;
-        float2 s = ck.stats[(sq.first + (int64_t)min(r, sq.m - 1)) * a.n_heads + h];
-        if (r >= sq.m) s.y = 0.f;
-        return s;
+        const int32_t h = kvh * a.group + it / per;
+#pragma unroll
+        for (int qb = 0; qb < NQ / 32; ++qb) {
+            const int32_t r = r0 + it % per * NQ + 32 * qb + col;
+            st1[qb] = ck.stats[(sq.first + (int64_t)min(r, sq.m - 1)) * a.n_heads + h];
+            if (r >= sq.m) st1[qb].y = 0.f;
+        }
     };
-    float2 st = make_float2(0.f, 0.f), st1 = st;
+    auto qb_at = [&](int32_t it) { return smem + (it & 1) * P::BUF; };
     if (steps) {
         fetch(0);
-        st1 = stat(0);
+        stat(0);
     }
     for (int32_t it = 0; it < steps; ++it) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        st = st1;
+#pragma unroll
+        for (int qb = 0; qb < NQ / 32; ++qb) st[qb] = st1[qb];
         if (it + 1 < steps) {
             fetch(it + 1);
-            st1 = stat(it + 1);
+            stat(it + 1);
         }
-        const char *qb = smem + (it & 1) * P::BUF;
-        const int32_t r = r0 + it % per * NQ, hi = old + min(r + NQ, sq.m) - 1;   // the step's last position
-        if (tw > hi) continue;
-        f32x16_t S[TB];
+        const int32_t r = r0 + it % per * NQ;
 #pragma unroll
-        for (int tb = 0; tb < TB; ++tb)
+        for (int qb = 0; qb < NQ / 32; ++qb) {
+            const int32_t rq = r + 32 * qb;
+            if (rq >= sq.m || tw > old + min(rq + 32, sq.m) - 1) continue;   // no row, or none that sees the wave's tokens
+            f32x16_t S[TB];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) S[tb][i] = 0.f;
+            for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-        for (int k = 0; k < KQ; ++k) {
-            const u32x4_t f = load16(qb + col * RB + 16 * C::k_swz(col, 2 * k + hh));
+                for (int i = 0; i < 16; ++i) S[tb][i] = 0.f;
 #pragma unroll
-            for (int tb = 0; tb < TB; ++tb) {
-                if constexpr (BF) {
-                    S[tb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, K[tb][k]),
-                                                                    __builtin_bit_cast(bf16x8_t, f), S[tb], 0, 0, 0);
-                } else {
+            for (int k = 0; k < KQ; ++k) {
+                const u32x4_t f = load16(qb_at(it) + (32 * qb + col) * RB + 16 * C::k_swz(col, 2 * k + hh));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        S[tb] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(K[tb][k][e]), __uint_as_float(f[e]), S[tb], 0, 0, 0);
+                for (int tb = 0; tb < TB; ++tb) {
+                    if constexpr (BF) {
+                        S[tb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, K[tb][k]),
+                                                                        __builtin_bit_cast(bf16x8_t, f), S[tb], 0, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            S[tb] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(K[tb][k][e]), __uint_as_float(f[e]), S[tb], 0, 0, 0);
+                    }
                 }
             }
-        }
-        const int32_t pos = old + r + col;
-        const bool edge = tw + TB * 32 - 1 > old + r;       // some row does not see all of the wave's tokens
+            const int32_t pos = old + rq + col;
+            if (tw + TB * 32 - 1 > old + rq) {              // some row does not see all of the wave's tokens
 #pragma unroll
-        for (int tb = 0; tb < TB; ++tb)
+                for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float w = exp2_fast(S[tb][i] * scale2 - st.x) * st.y;
-                if (edge && tw + 32 * tb + 8 * (i / 4) + 4 * hh + (i & 3) > pos) w = 0.f;
-                sum[tb][i] += w;
+                    for (int i = 0; i < 16; ++i) {
+                        const float w = exp2_fast(S[tb][i] * scale2 - st[qb].x) * st[qb].y;
+                        sum[tb][i] += tw + 32 * tb + 8 * (i / 4) + 4 * hh + (i & 3) > pos ? 0.f : w;
+                    }
+            } else {
+#pragma unroll
+                for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[tb][i] += exp2_fast(S[tb][i] * scale2 - st[qb].x) * st[qb].y;
             }
+        }
     }
     if (bad) record(a, bad);
-    float *out = ck.part + ((int64_t)b * a.n_kv + kvh) * ck.cap_ld;
+    // Sum over the 32 query rows, which are the lanes: at each exchange a lane hands half of its tokens over and keeps
+    // the other half's sums, until one token is left to it.
+    float v[16 * TB];
 #pragma unroll
-    for (int tb = 0; tb < TB; ++tb)
+    for (int x = 0; x < 16 * TB; ++x) v[x] = sum[x / 16][x % 16];
+    int left = 16 * TB;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float v = sum[tb][i];
+    for (int o = 16; o > 0; o >>= 1) {
+        if (left > 1) {
+            left /= 2;
+            const bool up = col & o;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) v += __shfl_xor(v, o, 64);
-            const int t = 8 * (i / 4) + 4 * hh + (i & 3);
-            const bool ok = (__shfl(there, t, 64) >> tb) & 1;
-            const int32_t tok = tw + 32 * tb + t;
-            if (col == 0 && tok < sq.n) out[tok] = ok ? v : 0.f;
+            for (int x = 0; x < 16 * TB; ++x)
+                if (x < left) v[x] = (up ? v[x + left] : v[x]) + __shfl_xor(up ? v[x] : v[x + left], o, 64);
+        } else {
+            v[0] += __shfl_xor(v[0], o, 64);
         }
+    }
+    const int x = TB == 2 ? col : col >> 1, tb = x / 16, t = 8 * (x % 16 / 4) + 4 * hh + (x & 3);
+    const bool ok = (__shfl(there, t, 64) >> tb) & 1;
+    const int32_t tok = tw + 32 * tb + t;
+    if ((TB == 2 || !(col & 1)) && tok < sq.n) ck.part[((int64_t)b * a.n_kv + kvh) * ck.cap_ld + tok] = ok ? v[0] : 0.f;
 }
 
 __global__ __launch_bounds__(256) void k_kv_chunk_sum(KvArgs a, KvAttend at, KvChunk ck) {
