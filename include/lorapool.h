@@ -376,7 +376,7 @@ int lora_project_noalloc(lora_pool *pool, const void *x, const void *W, const in
  * LORA_MAX_KV_TOKENS.  n_seq == 0 or no rows: nothing is done.
  */
 #define LORA_MAX_SEQS 65535
-#define LORA_MAX_KV_TOKENS (1 << 24)
+#define LORA_MAX_KV_TOKENS (1 << 22)
 #define LORA_MAX_TOKENS_PER_PAGE 256
 #define LORA_MAX_HEADS 1024
 

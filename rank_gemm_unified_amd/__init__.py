@@ -24,7 +24,7 @@ LORA_MAX_RANK, LORA_MAX_ADAPTERS, LORA_MAX_TOKENS = 64, 8192, 1 << 22
 LORA_VICTIM_LOAD_ORDER, LORA_VICTIM_LRU, LORA_VICTIM_FARTHEST = 0, 1, 2
 LORA_MAX_CALL_SLOTS = 4
 LORA_NOALLOC_SCRATCH_MB = 32
-LORA_MAX_SEQS, LORA_MAX_KV_TOKENS, LORA_MAX_TOKENS_PER_PAGE, LORA_MAX_HEADS = 65535, 1 << 24, 256, 1024
+LORA_MAX_SEQS, LORA_MAX_KV_TOKENS, LORA_MAX_TOKENS_PER_PAGE, LORA_MAX_HEADS = 65535, 1 << 22, 256, 1024
 STATUS_NAMES = {0: "ok", -1: "einval", -2: "enomem", -3: "enoent", -4: "erank", -5: "ebusy",
                 -6: "eexist", -7: "ehip", -8: "edevice"}
 

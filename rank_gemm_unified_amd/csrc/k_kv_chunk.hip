@@ -433,55 +433,51 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
 }
 
 // ---- scores: the weights once more, summed over the rows ---------------------------------------------
-// A token's weights can be summed only when its rows' maxima and sums are known.  One workgroup takes 4 * TB * 32
+// A token's weights can be summed only when its rows' maxima and sums are known.  One workgroup takes 128
 // tokens of one K/V head, K in registers, and walks the query rows of the heads that share it; the logits are
 // multiplied again (half of the attention's products), and a lane sums its query rows' weights for each of its tokens.
 template <typename E, int HD>
 struct Scores {
     static constexpr bool BF = sizeof(E) == 2;
     static constexpr int RB = HD * (int)sizeof(E);
-    static constexpr int TB = !BF && HD == 256 ? 1 : 2;     // blocks of 32 tokens a wave holds
-    static constexpr int TOK = 4 * TB * 32;
+    static constexpr int TOK = 4 * 32;
     static constexpr int NQ = RB > 256 ? 32 : 64;           // query rows of a step
     static constexpr int BUF = NQ * RB;
-    static constexpr int WAVES = RB > 256 ? 1 : 2;
+    static constexpr int WAVES = RB > 512 ? 1 : RB > 256 ? 2 : 4;
 };
 
 template <typename E, int HD>
 __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores(KvArgs a, KvAttend at, KvChunk ck) {
     using P = Scores<E, HD>;
     using C = Chunk<E, HD>;
-    constexpr int RB = P::RB, TB = P::TB, KQ = C::KQ, NQ = P::NQ;
+    constexpr int RB = P::RB, KQ = C::KQ, NQ = P::NQ;
     constexpr bool BF = P::BF;
     __shared__ __align__(256) char smem[2 * P::BUF];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, hh = lane >> 5;
-    const int32_t b = blockIdx.z, kvh = blockIdx.y, t0 = blockIdx.x * P::TOK;
+    const int32_t b = blockIdx.z, kvh = blockIdx.x, t0 = blockIdx.y * P::TOK;
     const SeqRows sq = seq_rows(a, b);
     if (t0 >= sq.n) return;
-    const int32_t old = sq.n - sq.m, tw = t0 + wave * TB * 32;
+    const int32_t old = sq.n - sq.m, tw = t0 + wave * 32;
     const float scale2 = at.scale * 1.4426950408889634f;
     const int32_t *trow = a.table + (int64_t)b * 2 * a.max_pages;
 
-    u32x4_t K[TB][KQ];
-    uint32_t there = 0;                                     // one bit per block: the lane's token (row `col`)
+    u32x4_t K[KQ];
+    int32_t kid, vid;
+    uint32_t ku, vu;
     int bad = 0;
-#pragma unroll
-    for (int tb = 0; tb < TB; ++tb) {
-        int32_t kid, vid;
-        uint32_t ku, vu;
-        const int32_t tok = tw + 32 * tb + col;
-        lane_ids(a, trow, tok, sq.n, &kid, &vid);
-        const uint64_t ok = lane_units(a, tok, sq.n, kid, vid, &ku, &vu, &bad);
-        there |= (uint32_t)((ok >> lane) & 1) << tb;
+    lane_ids(a, trow, tw + col, sq.n, &kid, &vid);
+    const uint32_t there = (uint32_t)lane_units(a, tw + col, sq.n, kid, vid, &ku, &vu, &bad);
+    {
         const char *p = a.pages + ((uint64_t)ku << 7) + (int64_t)kvh * RB + 16 * hh;
 #pragma unroll
-        for (int k = 0; k < KQ; ++k) K[tb][k] = load16(p + 32 * k);
+        for (int k = 0; k < KQ; ++k) K[k] = load16(p + 32 * k);
     }
-    f32x16_t sum[TB];
+    // K is waited for here: the compiler would put the wait into the loop, where it would also wait for the rows ahead
 #pragma unroll
-    for (int tb = 0; tb < TB; ++tb)
+    for (int k = 0; k < KQ; ++k) asm volatile("" : "+v"(K[k]));
+    f32x16_t sum;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum[tb][i] = 0.f;
+    for (int i = 0; i < 16; ++i) sum[i] = 0.f;
 
     // steps: for each head of the group, NQ query rows at a time from the first that sees token t0
     const int32_t r0 = max(0, t0 - old) / NQ * NQ, per = sq.m > r0 ? (sq.m - r0 + NQ - 1) / NQ : 0;
@@ -527,66 +523,49 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
         for (int qb = 0; qb < NQ / 32; ++qb) {
             const int32_t rq = r + 32 * qb;
             if (rq >= sq.m || tw > old + min(rq + 32, sq.m) - 1) continue;   // no row, or none that sees the wave's tokens
-            f32x16_t S[TB];
+            f32x16_t S;
 #pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) S[tb][i] = 0.f;
+            for (int i = 0; i < 16; ++i) S[i] = 0.f;
 #pragma unroll
             for (int k = 0; k < KQ; ++k) {
                 const u32x4_t f = load16(qb_at(it) + (32 * qb + col) * RB + 16 * C::k_swz(col, 2 * k + hh));
+                if constexpr (BF) {
+                    S = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, K[k]), __builtin_bit_cast(bf16x8_t, f), S, 0, 0, 0);
+                } else {
 #pragma unroll
-                for (int tb = 0; tb < TB; ++tb) {
-                    if constexpr (BF) {
-                        S[tb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, K[tb][k]),
-                                                                        __builtin_bit_cast(bf16x8_t, f), S[tb], 0, 0, 0);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            S[tb] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(K[tb][k][e]), __uint_as_float(f[e]), S[tb], 0, 0, 0);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        S = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(K[k][e]), __uint_as_float(f[e]), S, 0, 0, 0);
                 }
             }
-            const int32_t pos = old + rq + col;
-            if (tw + TB * 32 - 1 > old + rq) {              // some row does not see all of the wave's tokens
+            if (tw + 31 > old + rq) {                       // some row does not see all of the wave's tokens
+                const int32_t last = old + rq + col - tw - 4 * hh;
 #pragma unroll
-                for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float w = exp2_fast(S[tb][i] * scale2 - st[qb].x) * st[qb].y;
-                        sum[tb][i] += tw + 32 * tb + 8 * (i / 4) + 4 * hh + (i & 3) > pos ? 0.f : w;
-                    }
+                for (int i = 0; i < 16; ++i) {
+                    const float w = exp2_fast(S[i] * scale2 - st[qb].x) * st[qb].y;
+                    sum[i] += 8 * (i / 4) + (i & 3) > last ? 0.f : w;
+                }
             } else {
 #pragma unroll
-                for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) sum[tb][i] += exp2_fast(S[tb][i] * scale2 - st[qb].x) * st[qb].y;
+                for (int i = 0; i < 16; ++i) sum[i] += exp2_fast(S[i] * scale2 - st[qb].x) * st[qb].y;
             }
         }
     }
     if (bad) record(a, bad);
     // Sum over the 32 query rows, which are the lanes: at each exchange a lane hands half of its tokens over and keeps
     // the other half's sums, until one token is left to it.
-    float v[16 * TB];
+    float v[16];
 #pragma unroll
-    for (int x = 0; x < 16 * TB; ++x) v[x] = sum[x / 16][x % 16];
-    int left = 16 * TB;
+    for (int x = 0; x < 16; ++x) v[x] = sum[x];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        if (left > 1) {
-            left /= 2;
+    for (int o = 16; o > 1; o >>= 1)
+#pragma unroll
+        for (int x = 0; x < o / 2; ++x) {
             const bool up = col & o;
-#pragma unroll
-            for (int x = 0; x < 16 * TB; ++x)
-                if (x < left) v[x] = (up ? v[x + left] : v[x]) + __shfl_xor(up ? v[x] : v[x + left], o, 64);
-        } else {
-            v[0] += __shfl_xor(v[0], o, 64);
+            v[x] = (up ? v[x + o / 2] : v[x]) + __shfl_xor(up ? v[x] : v[x + o / 2], o, 64);
         }
-    }
-    const int x = TB == 2 ? col : col >> 1, tb = x / 16, t = 8 * (x % 16 / 4) + 4 * hh + (x & 3);
-    const bool ok = (__shfl(there, t, 64) >> tb) & 1;
-    const int32_t tok = tw + 32 * tb + t;
-    if ((TB == 2 || !(col & 1)) && tok < sq.n) ck.part[((int64_t)b * a.n_kv + kvh) * ck.cap_ld + tok] = ok ? v[0] : 0.f;
+    v[0] += __shfl_xor(v[0], 1, 64);
+    const int x = col >> 1, t = 8 * (x / 4) + 4 * hh + (x & 3);
+    if (!(col & 1) && tw + t < sq.n) ck.part[((int64_t)b * a.n_kv + kvh) * ck.cap_ld + tw + t] = (there >> t) & 1 ? v[0] : 0.f;
 }
 
 __global__ __launch_bounds__(256) void k_kv_chunk_sum(KvArgs a, KvAttend at, KvChunk ck) {
@@ -623,7 +602,7 @@ hipError_t run(const KvArgs &a, const KvAttend &at, hipStream_t s) {
     hipLaunchKernelGGL((k_kv_chunk<E, HD>), dim3((unsigned)grid), dim3(256), LDS, s, a, at, ck);
     if (at.scores) {
         constexpr int TOK = Scores<E, HD>::TOK;
-        hipLaunchKernelGGL((k_kv_chunk_scores<E, HD>), dim3((a.cap + TOK - 1) / TOK, a.n_kv, a.n_seq), dim3(256), 0, s, a, at, ck);
+        hipLaunchKernelGGL((k_kv_chunk_scores<E, HD>), dim3(a.n_kv, (a.cap + TOK - 1) / TOK, a.n_seq), dim3(256), 0, s, a, at, ck);
         hipLaunchKernelGGL(k_kv_chunk_sum, dim3((a.cap + 255) / 256, a.n_seq), dim3(256), 0, s, a, at, ck);
     }
     return hipGetLastError();

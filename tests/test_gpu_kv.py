@@ -371,6 +371,10 @@ def _evict_case(tpp, layers, lens, seed, kind):
     (256, 1, [3000], 300, 1, 1, None),
     (1, 1, [100, 200], 300, 4, 4, None),
     (2, 1, [100], 0, 60, 60, None),
+    (1, 2, [511, 512, 3, 505], 100, 2, 2, None),
+    (1, 1, [2040, 1999], 1000, 2, 2, None),
+    (1, 1, [9001, 20], 4000, 4, 8, None),                   # rows that do not fit the registers of a workgroup
+    (2, 1, [17003, 500], 301, 5, 9, 7000),
 ])
 def test_evict(tpp, layers, lens, budget, first, last, max_drop, kind, in_place):
     pool = rg.Pool(4, 64 * 256, rg.LORA_BF16, max_rank=1)

@@ -51,7 +51,7 @@ def test_layouts_refused(which, layout):
 REFUSED = [
     ("write", dict(k=None)), ("write", dict(v=None)), ("write", dict(table=None)), ("write", dict(lens=None)),
     ("write", dict(k=A + 8)), ("write", dict(ldk=127)), ("write", dict(ldk=132)), ("write", dict(ldv=-128)), ("write", dict(ldv=1 << 40)),
-    ("write", dict(max_pages=0)), ("write", dict(max_pages=(1 << 23) + 1)), ("write", dict(n_seq=-1)),
+    ("write", dict(max_pages=0)), ("write", dict(max_pages=(1 << 21) + 1)), ("write", dict(n_seq=-1)),
     ("write", dict(n_seq=(1 << 16) + 1)), ("write", dict(T=-1)), ("write", dict(T=(1 << 22) + 1)),
     ("write", dict(q_start=None)), ("write", dict(q_start=A + 2)), ("write", dict(table=A + 2)), ("write", dict(lens=A + 1)),
     ("token", dict(q=None)), ("token", dict(out=None)), ("token", dict(table=None)), ("token", dict(lens=None)),
@@ -92,7 +92,7 @@ def test_workspace_sizes():
     p = _pool()
     for f in (lambda n, m, s: rg.lora_kv_attend_workspace_size(p.handle, L, n, m, s),
               lambda n, m, s: rg.lora_kv_attend_chunk_workspace_size(p.handle, L, 4, n, m, s)):
-        assert f(0, 8, True) == 0 and f(1, 0, True) == 0 and f(1, (1 << 24) + 1, True) == 0 and f((1 << 22) + 1, 8, True) == 0
+        assert f(0, 8, True) == 0 and f(1, 0, True) == 0 and f(1, (1 << 22) + 1, True) == 0 and f((1 << 22) + 1, 8, True) == 0
         assert 0 < f(1, 8, True) <= f(64, 8, True) <= f(64, 4096, True)
         assert f(64, 4096, False) <= f(64, 4096, True)
     assert rg.lora_kv_attend_workspace_size(p.handle, rg.lora_kv_layout_t(8, 3, 64, 1), 4, 8, True) == 0
