@@ -139,8 +139,8 @@ def _check(rc: int, where: str) -> int:
 
 def _ptr(t) -> int | None:
     """Device/host address of a tensor or array (None stays NULL)."""
-    if t is None:
-        return None
+    if t is None or type(t) is int:
+        return t
     if isinstance(t, int):
         return t
     if isinstance(t, np.ndarray):
@@ -155,6 +155,12 @@ def _stream(s) -> int | None:
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+# The current stream's handle of a device.  torch's own short way to it where there is one: a stream object costs
+# two microseconds, as much as the rest of a call's checks.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 # ---- C-ABI, one wrapper per entry point ----------------------------------------------------------
@@ -518,41 +524,43 @@ class Pool:
     # several streams, and calls captured into several graphs, share none.
 
     def _where(self, stream):
-        """(stream handle, whether the call runs on the current stream of the current device)."""
-        torch, dev = self.torch, self.pages.device
+        """(stream handle, whether the call runs on the current stream)."""
         if stream is None:
-            return torch.cuda.current_stream(dev).cuda_stream, True
+            return _current_stream(self.pages.get_device()), True
         return (stream if isinstance(stream, int) else stream.cuda_stream), False
 
     def _empty(self, here, stream, shape, dtype):
         """Memory that belongs to the call's stream, as its allocator sees it."""
-        torch, dev = self.torch, self.pages.device
         if here:
-            return torch.empty(shape, dtype=dtype, device=dev)
+            return self.pages.new_empty(shape, dtype=dtype)
+        torch, dev = self.torch, self.pages.device
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=dev)
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=dev)
 
     def _kv_rows(self, what, t, width):
-        if t.dim() != 2 or t.shape[1] != width or t.dtype != self.tdtype or t.device != self.pages.device \
-                or (t.stride(1) != 1 and t.numel()):
+        """Rows of `width` elements of the pool's type: how far they lie apart."""
+        shape, stride = t.shape, t.stride()
+        if len(shape) != 2 or shape[1] != width or t.dtype is not self.tdtype or not t.is_cuda \
+                or t.get_device() != self.pages.get_device() or (stride[1] != 1 and shape[0]):
             raise ValueError(f"{what}: rows of {width} {self.tdtype} elements on {self.pages.device} are wanted, not "
-                             f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
-        return t.stride(0)
+                             f"{tuple(shape)} {t.dtype} on {t.device}, strides {stride}")
+        return stride[0]
 
-    def _kv_ints(self, what, t, shape, dtype=None):
-        dtype = self.torch.int32 if dtype is None else dtype
-        if tuple(t.shape) != shape or t.dtype != dtype or t.device != self.pages.device or not t.is_contiguous():
+    def _kv_ints(self, what, t, shape, dtype):
+        if t.shape != shape or t.dtype is not dtype or not t.is_cuda or t.get_device() != self.pages.get_device() \
+                or not t.is_contiguous():
             raise ValueError(f"{what}: contiguous {dtype} {shape} on {self.pages.device} is wanted, not {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
 
     def _kv_table(self, table, lens, q_start):
+        i32 = torch.int32
         n, mp = table.shape[0], table.shape[-1]
-        self._kv_ints("table", table, (n, 2, mp))
-        self._kv_ints("lens", lens, (n,))
+        self._kv_ints("table", table, (n, 2, mp), i32)
+        self._kv_ints("lens", lens, (n,), i32)
         if q_start is not None:
-            self._kv_ints("q_start", q_start, (n + 1,))
+            self._kv_ints("q_start", q_start, (n + 1,), i32)
         return n, mp
 
     def kv_write(self, layout, k, v, table, lens, q_start=None, stream=None):
@@ -562,7 +570,8 @@ class Pool:
         ldk, ldv = self._kv_rows("k", k, width), self._kv_rows("v", v, width)
         if k.shape[0] != v.shape[0]:
             raise ValueError(f"k has {k.shape[0]} rows and v {v.shape[0]}")
-        lora_kv_write(self.handle, layout, k, ldk, v, ldv, table, mp, q_start, lens, n, k.shape[0],
+        lora_kv_write(self.handle, layout, k.data_ptr(), ldk, v.data_ptr(), ldv, table.data_ptr(), mp,
+                      None if q_start is None else q_start.data_ptr(), lens.data_ptr(), n, k.shape[0],
                       stream=self._where(stream)[0])
 
     def _kv_attend(self, layout, q, table, lens, q_start, scale, max_len, out, scores, prior, workspace, stream):
@@ -571,28 +580,33 @@ class Pool:
         ldq = self._kv_rows("q", q, width)
         if q_start is None and T != n:
             raise ValueError(f"q has {T} rows for {n} sequences")
-        for what, t in (("scores", scores), ("prior", prior)):
-            if t is not None:
-                self._kv_ints(what, t, (n, cap), self.torch.float32)
+        if scores is not None:
+            self._kv_ints("scores", scores, (n, cap), torch.float32)
+        if prior is not None:
+            self._kv_ints("prior", prior, (n, cap), torch.float32)
         handle, here = self._where(stream)
         if out is None:
-            out = self._empty(here, stream, (T, width), self.tdtype)
-        ldo = self._kv_rows("out", out, width)
-        if out.shape[0] != T:
-            raise ValueError(f"out has {out.shape[0]} rows and q {T}")
+            out, ldo = self._empty(here, stream, (T, width), self.tdtype), width
+        else:
+            ldo = self._kv_rows("out", out, width)
+            if out.shape[0] != T:
+                raise ValueError(f"out has {out.shape[0]} rows and q {T}")
         scale = layout.head_dim ** -0.5 if scale is None else scale
         max_len = cap if max_len is None else max_len
         if workspace is None:
             need = lora_kv_attend_workspace_size(self.handle, layout, n, max_len, scores is not None) \
                 if q_start is None else \
                 lora_kv_attend_chunk_workspace_size(self.handle, layout, n, T, max_len, scores is not None)
-            workspace = self._empty(here, stream, need, self.torch.uint8) if need else None
+            workspace = self._empty(here, stream, (need,), torch.uint8) if need else None
+        args = (None if prior is None else prior.data_ptr(), None if scores is None else scores.data_ptr(),
+                None if workspace is None else workspace.data_ptr(),
+                0 if workspace is None else workspace.numel() * workspace.element_size())
         if q_start is None:
-            lora_kv_attend(self.handle, layout, q, ldq, table, mp, lens, n, max_len, scale, out, ldo, prior, scores,
-                           workspace, stream=handle)
+            lora_kv_attend(self.handle, layout, q.data_ptr(), ldq, table.data_ptr(), mp, lens.data_ptr(), n, max_len,
+                           scale, out.data_ptr(), ldo, *args, stream=handle)
         else:
-            lora_kv_attend_chunk(self.handle, layout, q, ldq, table, mp, q_start, lens, n, T, max_len, scale, out, ldo,
-                                 prior, scores, workspace, stream=handle)
+            lora_kv_attend_chunk(self.handle, layout, q.data_ptr(), ldq, table.data_ptr(), mp, q_start.data_ptr(),
+                                 lens.data_ptr(), n, T, max_len, scale, out.data_ptr(), ldo, *args, stream=handle)
         return out
 
     def kv_attend(self, layout, q, table, lens, scale=None, max_len=None, out=None, scores=None, prior=None,
@@ -612,11 +626,10 @@ class Pool:
         """Thin the caches out by accumulated attention (lora_kv_evict).  table: int32 [layers, n_seq, 2,
         max_pages]; scores: float32 [layers, n_seq, max_pages * tokens_per_page].  Returns (table, scores, lens,
         dropped, n_dropped), the first two the tensors passed in if in_place."""
-        torch = self.torch
         layers, n, mp = table.shape[0], table.shape[1], table.shape[-1]
-        self._kv_ints("table", table, (layers, n, 2, mp))
+        self._kv_ints("table", table, (layers, n, 2, mp), torch.int32)
         self._kv_ints("scores", scores, (layers, n, mp * layout.tokens_per_page), torch.float32)
-        self._kv_ints("lens", lens, (n,))
+        self._kv_ints("lens", lens, (n,), torch.int32)
         max_drop = mp if max_drop is None else max_drop
         handle, here = self._where(stream)
         table_out = table if in_place else self._empty(here, stream, table.shape, torch.int32)
@@ -624,8 +637,9 @@ class Pool:
         lens_out = self._empty(here, stream, (n,), torch.int32)
         dropped = self._empty(here, stream, (layers, n, 2, max_drop), torch.int32)
         n_dropped = self._empty(here, stream, (n,), torch.int32)
-        lora_kv_evict(self.handle, layout, layers, n, table, table_out, mp, scores, scores_out, lens, lens_out, budget,
-                      keep_first, keep_last, dropped, max_drop, n_dropped, stream=handle)
+        lora_kv_evict(self.handle, layout, layers, n, table.data_ptr(), table_out.data_ptr(), mp, scores.data_ptr(),
+                      scores_out.data_ptr(), lens.data_ptr(), lens_out.data_ptr(), budget, keep_first, keep_last,
+                      dropped.data_ptr(), max_drop, n_dropped.data_ptr(), stream=handle)
         return table_out, scores_out, lens_out, dropped, n_dropped
 
 

@@ -80,7 +80,7 @@ __device__ __forceinline__ uint64_t lane_units(const KvArgs &a, int32_t tok, int
 
 // The query tile that a slot stands for: sequence and tile in it; -1 behind the last.  Slots count tiles of
 // all sequences from the end, so that the longest rows of a sequence start first.  All 256 threads call.
-__device__ __forceinline__ int32_t find_tile(const KvArgs &a, int32_t slot, int32_t tq, int32_t *tile, int32_t *sh) {
+__device__ __forceinline__ int32_t find_tile(const KvArgs &a, int32_t slot, int32_t tq, int32_t *tile, SeqRows *rows, int32_t *sh) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int32_t per = (a.n_seq + 255) / 256, b0 = min(a.n_seq, tid * per), b1 = min(a.n_seq, b0 + per);
     int32_t mine = 0;
@@ -101,16 +101,23 @@ __device__ __forceinline__ int32_t find_tile(const KvArgs &a, int32_t slot, int3
         for (int32_t b = b0; b < b1; ++b) {
             const int32_t t = (seq_rows(a, b).m + tq - 1) / tq;
             if (want < at + t) {
+                const SeqRows q = seq_rows(a, b);
                 sh[4] = b;
                 sh[5] = want - at;
+                sh[6] = q.first;
+                sh[7] = q.m;
+                sh[8] = q.n;
                 break;
             }
             at += t;
         }
     }
     __syncthreads();
-    *tile = sh[5];
-    return sh[4];
+    *tile = uniform(sh[5]);
+    rows->first = uniform(sh[6]);
+    rows->m = uniform(sh[7]);
+    rows->n = uniform(sh[8]);
+    return uniform(sh[4]);
 }
 
 template <typename E, int HD>
@@ -119,20 +126,16 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
     constexpr int NT = C::NT, NB = C::NB, RB = C::RB, CH = C::CH, KQ = C::KQ, ND = HD / 32;
     constexpr bool BF = C::BF;
     extern __shared__ __align__(256) char smem[];
-    __shared__ int32_t sh[6];
+    __shared__ int32_t sh[9];
     __shared__ unsigned long long sh_flag;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 31, hh = lane >> 5;
     const int32_t groups = a.n_heads / ck.hpw, hg = blockIdx.x % groups, slot = blockIdx.x / groups;
     if (blockIdx.x == 0) check_seqs(a);
     const int32_t tq = 128 / ck.hpw;
     int32_t tile;
-    const int32_t b = uniform(find_tile(a, slot, tq, &tile, sh));
+    SeqRows sq;
+    const int32_t b = find_tile(a, slot, tq, &tile, &sq, sh);
     if (b < 0) return;
-    tile = uniform(tile);
-    SeqRows sq = seq_rows(a, b);
-    sq.first = uniform(sq.first);
-    sq.m = uniform(sq.m);
-    sq.n = uniform(sq.n);
     const int32_t head = hg * ck.hpw + (wave & (ck.hpw - 1)), q0 = tile * tq + (wave / ck.hpw) * 32;
     const int32_t qi = q0 + col;
     const bool row_ok = qi < sq.m;
@@ -453,7 +456,7 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
     constexpr int RB = P::RB, KQ = C::KQ, NQ = P::NQ;
     constexpr bool BF = P::BF;
     __shared__ __align__(256) char smem[2 * P::BUF];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, hh = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 31, hh = lane >> 5;
     const int32_t b = blockIdx.z, kvh = blockIdx.x, t0 = blockIdx.y * P::TOK;
     const SeqRows sq = seq_rows(a, b);
     if (t0 >= sq.n) return;
@@ -472,53 +475,60 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
 #pragma unroll
         for (int k = 0; k < KQ; ++k) K[k] = load16(p + 32 * k);
     }
-    // K is waited for here: the compiler would put the wait into the loop, where it would also wait for the rows ahead
-#pragma unroll
-    for (int k = 0; k < KQ; ++k) asm volatile("" : "+v"(K[k]));
     f32x16_t sum;
 #pragma unroll
     for (int i = 0; i < 16; ++i) sum[i] = 0.f;
 
-    // steps: for each head of the group, NQ query rows at a time from the first that sees token t0
+    // steps: for each head of the group, NQ query rows at a time from the first that sees token t0.  (fh, fr): the
+    // next step to fetch, off: its distance in bytes from the first one's rows, where this lane's pieces lie.
     const int32_t r0 = max(0, t0 - old) / NQ * NQ, per = sq.m > r0 ? (sq.m - r0 + NQ - 1) / NQ : 0;
-    const int32_t steps = per * a.group;
-    auto fetch = [&](int32_t it) {
-        const int32_t h = kvh * a.group + it / per, r = r0 + it % per * NQ;
-        constexpr int PER = (P::BUF / 1024 + 3) / 4;
+    const int32_t steps = per * a.group, h0 = kvh * a.group;
+    constexpr int PER = P::BUF / 4096;
+    const int64_t row_bytes = at.ldq * (int64_t)sizeof(E);
+    const char *piece[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int byte = (wave * PER + j) * 1024 + lane * 16, x = byte / RB, c = (byte % RB) / 16;
+        piece[j] = (const char *)at.q + (sq.first + r0 + x) * row_bytes + (int64_t)h0 * RB + 16 * C::k_swz(x, c);
+    }
+    int32_t fh = 0, fr = r0;
+    int64_t off = 0;
+    float2 st[NQ / 32], st1[NQ / 32];
+    auto fetch = [&](char *to) {
+        const int32_t over = fr + NQ - sq.m;                // rows of the step behind the last one: it comes again
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int at0 = (wave * PER + j) * 1024, byte = at0 + lane * 16, q = byte / RB, c = (byte % RB) / 16;
-            if (at0 < P::BUF)
-                lds_gload16((const char *)((const E *)at.q + (sq.first + (int64_t)min(r + q, sq.m - 1)) * at.ldq + (int64_t)h * HD) +
-                                16 * C::k_swz(q, c),
-                            (lds_void *)(smem + (it & 1) * P::BUF + at0));
+            const int at0 = (wave * PER + j) * 1024, x = (at0 + lane * 16) / RB;
+            const char *p = piece[j] + off;
+            if (over > 0) p -= max(0, x + over - NQ + 1) * row_bytes;
+            lds_gload16(p, (lds_void *)(to + at0));
         }
-    };
-    float2 st[NQ / 32], st1[NQ / 32];
-    auto stat = [&](int32_t it) {
-        const int32_t h = kvh * a.group + it / per;
 #pragma unroll
         for (int qb = 0; qb < NQ / 32; ++qb) {
-            const int32_t r = r0 + it % per * NQ + 32 * qb + col;
-            st1[qb] = ck.stats[(sq.first + (int64_t)min(r, sq.m - 1)) * a.n_heads + h];
+            const int32_t r = fr + 32 * qb + col;
+            st1[qb] = ck.stats[(sq.first + (int64_t)min(r, sq.m - 1)) * a.n_heads + h0 + fh];
             if (r >= sq.m) st1[qb].y = 0.f;
         }
+        fr += NQ;
+        off += NQ * row_bytes;
+        if (fr >= sq.m) {
+            fr = r0;
+            ++fh;
+            off = (int64_t)fh * RB;
+        }
     };
-    auto qb_at = [&](int32_t it) { return smem + (it & 1) * P::BUF; };
-    if (steps) {
-        fetch(0);
-        stat(0);
-    }
+    if (steps) fetch(smem);
+    // K is waited for here: the compiler would put the wait into the loop, where it would also wait for the rows ahead
+#pragma unroll
+    for (int k = 0; k < KQ; ++k) asm volatile("" : "+v"(K[k]));
+    int32_t r = r0;
     for (int32_t it = 0; it < steps; ++it) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
 #pragma unroll
         for (int qb = 0; qb < NQ / 32; ++qb) st[qb] = st1[qb];
-        if (it + 1 < steps) {
-            fetch(it + 1);
-            stat(it + 1);
-        }
-        const int32_t r = r0 + it % per * NQ;
+        if (it + 1 < steps) fetch(smem + (~it & 1) * P::BUF);
+        const char *q = smem + (it & 1) * P::BUF;
 #pragma unroll
         for (int qb = 0; qb < NQ / 32; ++qb) {
             const int32_t rq = r + 32 * qb;
@@ -528,7 +538,7 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
             for (int i = 0; i < 16; ++i) S[i] = 0.f;
 #pragma unroll
             for (int k = 0; k < KQ; ++k) {
-                const u32x4_t f = load16(qb_at(it) + (32 * qb + col) * RB + 16 * C::k_swz(col, 2 * k + hh));
+                const u32x4_t f = load16(q + (32 * qb + col) * RB + 16 * C::k_swz(col, 2 * k + hh));
                 if constexpr (BF) {
                     S = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, K[k]), __builtin_bit_cast(bf16x8_t, f), S, 0, 0, 0);
                 } else {
@@ -549,6 +559,8 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
                 for (int i = 0; i < 16; ++i) sum[i] += exp2_fast(S[i] * scale2 - st[qb].x) * st[qb].y;
             }
         }
+        r += NQ;
+        if (r >= sq.m) r = r0;
     }
     if (bad) record(a, bad);
     // Sum over the 32 query rows, which are the lanes: at each exchange a lane hands half of its tokens over and keeps
