@@ -29,7 +29,7 @@ __device__ __forceinline__ s16x4_t read_tr(lds_s16x4 *__restrict__ p) { return _
 struct KvChunk {
     int32_t hpw;              // query heads of one K/V head a workgroup takes: 1, 2 or 4
     int32_t slots;            // query tiles, at most
-    float2 *stats;            // [T][n_heads]: maximum (base-2 logits) and 1 / sum of each row, for the scores; or null
+    float2 *stats;            // [n_heads][T]: maximum (base-2 logits) and 1 / sum of each row, for the scores; or null
     float *part;              // [n_seq][n_kv][cap_ld]: a K/V head's share of the scores
     int64_t cap_ld;
 };
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
     if (sq.n == 0) {                                        // no tokens: zero rows
         if (row_ok)
             for (int d = hh * (HD / 2); d < (hh + 1) * (HD / 2); ++d) from_f32(orow + d, 0.f);
-        if (ck.stats && row_ok && hh == 0) ck.stats[row * a.n_heads + head] = make_float2(0.f, 0.f);
+        if (ck.stats && row_ok && hh == 0) ck.stats[(int64_t)head * a.T + row] = make_float2(0.f, 0.f);
         return;
     }
     const int32_t old = sq.n - sq.m;                        // tokens before the new ones
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
     if (__syncthreads_or(chk != 0.f)) pass(std::true_type{});
     if (bad) record(a, bad);
     const float L = l + other_half(l), inv = L == 0.f ? 0.f : 1.f / L;
-    if (ck.stats && row_ok && hh == 0) ck.stats[row * a.n_heads + head] = make_float2(m == -INFINITY ? 0.f : m, inv);
+    if (ck.stats && row_ok && hh == 0) ck.stats[(int64_t)head * a.T + row] = make_float2(m == -INFINITY ? 0.f : m, inv);
     if constexpr (BF) {
         // rows through LDS, so that a row leaves in one piece
         constexpr int OB = RB + 16;
@@ -506,7 +506,7 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
 #pragma unroll
         for (int qb = 0; qb < NQ / 32; ++qb) {
             const int32_t r = fr + 32 * qb + col;
-            st1[qb] = ck.stats[(sq.first + (int64_t)min(r, sq.m - 1)) * a.n_heads + h0 + fh];
+            st1[qb] = ck.stats[(int64_t)(h0 + fh) * a.T + sq.first + min(r, sq.m - 1)];
             if (r >= sq.m) st1[qb].y = 0.f;
         }
         fr += NQ;
@@ -529,34 +529,50 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
         for (int qb = 0; qb < NQ / 32; ++qb) st[qb] = st1[qb];
         if (it + 1 < steps) fetch(smem + (~it & 1) * P::BUF);
         const char *q = smem + (it & 1) * P::BUF;
+        if (tw <= old + min(r + NQ, sq.m) - 1) {            // else no row of the step sees the wave's tokens
+            constexpr int NB = NQ / 32;
+            f32x16_t S[NB];
 #pragma unroll
-        for (int qb = 0; qb < NQ / 32; ++qb) {
-            const int32_t rq = r + 32 * qb;
-            if (rq >= sq.m || tw > old + min(rq + 32, sq.m) - 1) continue;   // no row, or none that sees the wave's tokens
-            f32x16_t S;
+            for (int qb = 0; qb < NB; ++qb)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) S[i] = 0.f;
+                for (int i = 0; i < 16; ++i) S[qb][i] = 0.f;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = 0; k < KQ; ++k)
+#pragma unroll
+                for (int qb = 0; qb < NB; ++qb) {
+                    const u32x4_t f = load16(q + (32 * qb + col) * RB + 16 * C::k_swz(col, 2 * k + hh));
+                    if constexpr (BF) {
+                        S[qb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, K[k]), __builtin_bit_cast(bf16x8_t, f), S[qb], 0, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            S[qb] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(K[k][e]), __uint_as_float(f[e]), S[qb], 0, 0, 0);
+                    }
+                }
+            // the rows come out of LDS three products ahead
+            __builtin_amdgcn_sched_group_barrier(0x100, 3 * NB, 0);
 #pragma unroll
             for (int k = 0; k < KQ; ++k) {
-                const u32x4_t f = load16(q + (32 * qb + col) * RB + 16 * C::k_swz(col, 2 * k + hh));
-                if constexpr (BF) {
-                    S = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, K[k]), __builtin_bit_cast(bf16x8_t, f), S, 0, 0, 0);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        S = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(K[k][e]), __uint_as_float(f[e]), S, 0, 0, 0);
-                }
+                __builtin_amdgcn_sched_group_barrier(0x008, NB * (BF ? 1 : 4), 0);
+                if (k + 3 < KQ) __builtin_amdgcn_sched_group_barrier(0x100, NB, 0);
             }
-            if (tw + 31 > old + rq) {                       // some row does not see all of the wave's tokens
-                const int32_t last = old + rq + col - tw - 4 * hh;
+            __builtin_amdgcn_sched_barrier(0);
+            if (tw + 31 > old + r || r + NQ > sq.m) {       // some row does not see all of the wave's tokens, or is none
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float w = exp2_fast(S[i] * scale2 - st[qb].x) * st[qb].y;
-                    sum[i] += 8 * (i / 4) + (i & 3) > last ? 0.f : w;
+                for (int qb = 0; qb < NB; ++qb) {
+                    const int32_t last = old + r + 32 * qb + col - tw - 4 * hh;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float w = exp2_fast(S[qb][i] * scale2 - st[qb].x) * st[qb].y;
+                        sum[i] += 8 * (i / 4) + (i & 3) > last ? 0.f : w;
+                    }
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sum[i] += exp2_fast(S[i] * scale2 - st[qb].x) * st[qb].y;
+                for (int qb = 0; qb < NB; ++qb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[i] += exp2_fast(S[qb][i] * scale2 - st[qb].x) * st[qb].y;
             }
         }
         r += NQ;
