@@ -372,8 +372,8 @@ int lora_project_noalloc(lora_pool *pool, const void *x, const void *W, const in
  * Pool dtype throughout (k, v, q, out); products are summed, and softmax statistics and scores held,
  * in float32.  Rows are `ld` elements apart (a column range of a wider matrix, such as the output of
  * one projection for q, k and v, is fine); every row starts on a 16-byte boundary.
- * Row counts up to LORA_MAX_TOKENS, n_seq up to LORA_MAX_SEQS, and max_pages * tokens_per_page up to
- * LORA_MAX_KV_TOKENS.  n_seq == 0 or no rows: nothing is done.
+ * Row counts up to LORA_MAX_TOKENS, n_seq up to LORA_MAX_SEQS, max_pages * tokens_per_page up to
+ * LORA_MAX_KV_TOKENS, and n_seq times the longest length up to 2^34.  n_seq == 0 or no rows: nothing is done.
  */
 #define LORA_MAX_SEQS 65535
 #define LORA_MAX_KV_TOKENS (1 << 22)

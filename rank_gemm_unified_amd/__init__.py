@@ -555,6 +555,8 @@ class Pool:
                              f"{tuple(t.shape)} on {t.device}")
 
     def _kv_table(self, table, lens, q_start):
+        if self.pages is None:
+            raise ValueError("a bookkeeping-only pool holds no KV vectors")
         i32 = torch.int32
         n, mp = table.shape[0], table.shape[-1]
         self._kv_ints("table", table, (n, 2, mp), i32)

@@ -28,7 +28,7 @@ __device__ __forceinline__ s16x4_t read_tr(lds_s16x4 *__restrict__ p) { return _
 
 struct KvChunk {
     int32_t hpw;              // query heads of one K/V head a workgroup takes: 1, 2 or 4
-    int32_t slots;            // query tiles, at most
+    int32_t slots_x;          // query tiles of one row of the grid
     float2 *stats;            // [n_heads][T]: maximum (base-2 logits) and 1 / sum of each row, for the scores; or null
     float *part;              // [n_seq][n_kv][cap_ld]: a K/V head's share of the scores
     int64_t cap_ld;
@@ -129,13 +129,13 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
     __shared__ int32_t sh[9];
     __shared__ unsigned long long sh_flag;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 31, hh = lane >> 5;
-    const int32_t groups = a.n_heads / ck.hpw, hg = blockIdx.x % groups, slot = blockIdx.x / groups;
-    if (blockIdx.x == 0) check_seqs(a);
+    const int32_t groups = a.n_heads / ck.hpw, hg = blockIdx.x % groups, slot = blockIdx.y * ck.slots_x + blockIdx.x / groups;
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(a);
     const int32_t tq = 128 / ck.hpw;
     int32_t tile;
     SeqRows sq;
     const int32_t b = find_tile(a, slot, tq, &tile, &sq, sh);
-    if (b < 0) return;
+    if (b < 0 || tile < 0 || tile >= (sq.m + tq - 1) / tq) return;   // (ranges that overlap can have more tiles than counted)
     const int32_t head = hg * ck.hpw + (wave & (ck.hpw - 1)), q0 = tile * tq + (wave / ck.hpw) * 32;
     const int32_t qi = q0 + col;
     const bool row_ok = qi < sq.m;
@@ -243,7 +243,6 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         place(0);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        look_up(1);
         __builtin_amdgcn_s_barrier();
         fetch(0);
         for (int32_t j = 0; j < steps; ++j) {
@@ -613,21 +612,27 @@ namespace {
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
+// More than 64 KiB of LDS has to be asked for, on each device.
+hipError_t big_lds(const void *kernel, int bytes) {
+    return bytes <= 64 * 1024 ? hipSuccess : hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <typename E, int HD>
 hipError_t run(const KvArgs &a, const KvAttend &at, hipStream_t s) {
     using C = Chunk<E, HD>;
     KvChunk ck;
     ck.hpw = a.group % 4 == 0 ? 4 : a.group % 2 == 0 ? 2 : 1;
     const int32_t tq = 128 / ck.hpw;
-    ck.slots = a.T / tq + std::min(a.n_seq, a.T);
+    const int32_t groups = a.n_heads / ck.hpw, slots = a.T / tq + std::min(a.n_seq, a.T);   // tiles, at most
+    ck.slots_x = std::min(slots, (1 << 22) / groups);       // a row of the grid has less than 2^32 threads
     ck.cap_ld = ((int64_t)a.cap + 63) / 64 * 64;
     ck.stats = at.scores ? (float2 *)at.ws : nullptr;
     ck.part = (float *)((char *)at.ws + up256((size_t)a.T * a.n_heads * 8));
     constexpr int OUT = C::BF ? 4 * 32 * (C::RB + 16) : 0, LDS = std::max(C::LDS, OUT);
-    static const hipError_t attr = hipFuncSetAttribute((const void *)k_kv_chunk<E, HD>, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
-    if (attr != hipSuccess) return attr;
-    const int64_t grid = (int64_t)ck.slots * (a.n_heads / ck.hpw);
-    hipLaunchKernelGGL((k_kv_chunk<E, HD>), dim3((unsigned)grid), dim3(256), LDS, s, a, at, ck);
+    hipError_t e = big_lds((const void *)k_kv_chunk<E, HD>, LDS);
+    if (e != hipSuccess) return e;
+    const dim3 grid((unsigned)(groups * ck.slots_x), (unsigned)((slots + ck.slots_x - 1) / ck.slots_x));
+    hipLaunchKernelGGL((k_kv_chunk<E, HD>), grid, dim3(256), LDS, s, a, at, ck);
     if (at.scores) {
         constexpr int TOK = Scores<E, HD>::TOK;
         hipLaunchKernelGGL((k_kv_chunk_scores<E, HD>), dim3(a.n_kv, (a.cap + TOK - 1) / TOK, a.n_seq), dim3(256), 0, s, a, at, ck);

@@ -47,6 +47,8 @@ int common(lora_pool *p, const char *fn, const lora_kv_layout_t *l, const int32_
                          LORA_MAX_KV_TOKENS);
     if (max_len < 1 || max_len > cap)
         return set_error(LORA_EINVAL, "%s: max_len %lld not in [1, %lld]", fn, (long long)max_len, (long long)cap);
+    if (n_seq * max_len > (int64_t(1) << 34))
+        return set_error(LORA_EINVAL, "%s: %d sequences of up to %lld tokens: more than 2^34", fn, n_seq, (long long)max_len);
     if (!table || !lens) return set_error(LORA_EINVAL, "%s: NULL pointer argument", fn);
     if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(q_start, 4))
         return set_error(LORA_EINVAL, "%s: misaligned pointer (table, q_start, lens: 4 B)", fn);
@@ -158,7 +160,7 @@ extern "C" int lora_kv_write(lora_pool *p, const lora_kv_layout_t *l, const void
 
 static bool sizes_ok(const lora_pool *p, const lora_kv_layout_t *l, int32_t n_seq, int64_t T, int64_t max_len) {
     return p && layout_ok(p, l) && n_seq >= 1 && n_seq <= LORA_MAX_SEQS && T >= 1 && T <= LORA_MAX_TOKENS &&
-           max_len >= 1 && max_len <= LORA_MAX_KV_TOKENS;
+           max_len >= 1 && max_len <= LORA_MAX_KV_TOKENS && n_seq * max_len <= (int64_t(1) << 34);
 }
 
 extern "C" size_t lora_kv_attend_workspace_size(const lora_pool *p, const lora_kv_layout_t *l, int32_t n_seq,

@@ -62,6 +62,7 @@ REFUSED = [
     ("token", dict(workspace=None)), ("token", dict(workspace=A + 6 * GAP + 16)), ("token", dict(workspace_bytes=8)),
     ("chunk", dict(q_start=None)), ("chunk", dict(q_start=A + 1)), ("chunk", dict(T=(1 << 22) + 1)), ("chunk", dict(out=A + 2048)),
     ("chunk", dict(workspace_bytes=8)), ("chunk", dict(n_seq=-3)), ("chunk", dict(max_len=1 << 40)),
+    ("token", dict(n_seq=65535, max_pages=1 << 21, max_len=1 << 20)), ("chunk", dict(n_seq=8192, max_pages=1 << 21, max_len=(1 << 21) + 1)),
     ("evict", dict(layers=0)), ("evict", dict(layers=65536)), ("evict", dict(n_seq=-1)), ("evict", dict(max_pages=0)), ("evict", dict(budget=-1)),
     ("evict", dict(keep_first=-1)), ("evict", dict(keep_last=-1)), ("evict", dict(max_drop=0)), ("evict", dict(max_drop=5)),
     ("evict", dict(keep_last=1 << 30)), ("evict", dict(lens_out=A + 2 * GAP)), ("evict", dict(table_out=A + 4)), ("evict", dict(scores_out=A + GAP + 32)),
@@ -149,8 +150,13 @@ def test_dropped_pages_serve_adapters():
 
 
 def test_cache_needs_device_pages():
+    import torch
     with pytest.raises(ValueError):
         rg.KvCache(_pool(), 2, L, 4, 100)
+    z = torch.zeros((1, 2, 4), dtype=torch.int32)
+    for call in (lambda: POOL.kv_write(L, z, z, z, z), lambda: POOL.kv_attend(L, z, z, z), lambda: POOL.kv_attend_chunk(L, z, z, z, z)):
+        with pytest.raises(ValueError):
+            call()
 
 
 def test_reference_forms_agree_with_loops():
