@@ -106,8 +106,10 @@ __device__ __forceinline__ Pieces pieces_of(int64_t t0, int64_t t1, const Ranges
 // waves a SIMD holds: what the registers of K, two V tiles, the accumulators and the queries leave room for
 constexpr int split_waves(int hd) { return hd == 256 ? 1 : 2; }
 
-template <typename E, int HD, bool SCORES>
-__global__ __launch_bounds__(256, split_waves(HD)) void k_kv_split(KvArgs a, KvAttend at, KvSplit sp) {
+// LOCAL: one workgroup per (sequence, K/V head), its waves sharing the sequence's tiles, joined in LDS: no second
+// launch.  For short caches of few sequences, where launches and round trips are the time.
+template <typename E, int HD, bool SCORES, bool LOCAL>
+__global__ __launch_bounds__(LOCAL ? 256 * split_waves(HD) : 256, split_waves(HD)) void k_kv_split(KvArgs a, KvAttend at, KvSplit sp) {
     constexpr int TT = Tile<E, HD>::TT, NS = TT / 16;
     constexpr bool BF = sizeof(E) == 2;
     constexpr int KS = HD * (int)sizeof(E) / 64;           // 16-byte loads of a lane per token row of K
@@ -123,9 +125,9 @@ __global__ __launch_bounds__(256, split_waves(HD)) void k_kv_split(KvArgs a, KvA
     __shared__ __align__(16) float sh_log[4][SCORES ? 3840 : 4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
 
-    if (blockIdx.x == 0) check_seqs(a);
+    if (blockIdx.x == 0 && (!LOCAL || blockIdx.y == 0)) check_seqs(a);
     // ---- where this workgroup's waves begin ----
-    {
+    if constexpr (!LOCAL) {
         if (tid < 4) sh_b[tid] = sh_j[tid] = 0;
         const int32_t per = (a.n_seq + 255) / 256, b0 = tid * per, b1 = min(a.n_seq, b0 + per);
         int64_t mine = 0;
@@ -162,11 +164,27 @@ __global__ __launch_bounds__(256, split_waves(HD)) void k_kv_split(KvArgs a, KvA
         }
         __syncthreads();
     }
-    const int32_t job = blockIdx.x * 4 + wave, range = job / sp.hu, hu = job - range * sp.hu;
-    const Ranges rg = ranges_of(sh_total, sp.R);
-    if (range >= rg.R) return;
-    int64_t gtile = rg.start(range);
-    const int32_t count = uniform((int32_t)(rg.start(range + 1) - gtile));
+    int32_t range, hu, count, b0, j0;
+    int64_t gtile = 0;
+    if constexpr (LOCAL) {
+        constexpr int NW = 4 * split_waves(HD);
+        hu = blockIdx.x;
+        b0 = blockIdx.y;
+        range = 0;
+        const int32_t nt = seq_tiles<TT>(a, b0);
+        j0 = uniform(wave * nt / NW);
+        count = uniform((wave + 1) * nt / NW) - j0;
+    } else {
+        const int32_t job = blockIdx.x * 4 + wave;
+        range = job / sp.hu;
+        hu = job - range * sp.hu;
+        const Ranges rg = ranges_of(sh_total, sp.R);
+        if (range >= rg.R) return;
+        gtile = rg.start(range);
+        count = uniform((int32_t)(rg.start(range + 1) - gtile));
+        b0 = uniform(sh_b[wave]);
+        j0 = uniform(sh_j[wave]);
+    }
 
     const int32_t kvh = uniform(hu / sp.ncb), cb = uniform(hu - kvh * sp.ncb);
     const int32_t head = kvh * a.group + cb * 16 + col;
@@ -284,8 +302,7 @@ __global__ __launch_bounds__(256, split_waves(HD)) void k_kv_split(KvArgs a, KvA
     // ---- the pipeline: page ids two tiles ahead, K and V one tile ahead ----
     // The loads of the next tile are issued whether there is one or not (behind the last tile they read the
     // pool's first page): a load under a condition would make every later wait a wait for all.
-    Pos p0{uniform(sh_b[wave]), uniform(sh_j[wave]), 0};
-    p0.n = len_of(p0.b);
+    Pos p0{b0, j0, len_of(b0)};
     Pos p1 = p0, p2;
     int32_t kid, vid;
     uint32_t ku, vu;
@@ -426,7 +443,7 @@ __global__ __launch_bounds__(256, split_waves(HD)) void k_kv_split(KvArgs a, KvA
         }
         __builtin_amdgcn_sched_barrier(0);
         const bool ends = (p0.j + 1) * TT >= p0.n;
-        if (ends || i + 1 == count) {
+        if (!LOCAL && (ends || i + 1 == count)) {
             finish(p0, ends && first_j == 0, first_piece ? 0 : 1);
             first_piece = false;
             reset();
@@ -437,13 +454,47 @@ __global__ __launch_bounds__(256, split_waves(HD)) void k_kv_split(KvArgs a, KvA
         there = there1;
         ++gtile;
     };
-    for (int32_t i = 0;;) {
+    for (int32_t i = 0; i < count;) {
         step(i, V0, V1);
         if (++i >= count) break;
         step(i, V1, V0);
-        if (++i >= count) break;
+        ++i;
     }
     if (bad) record(a, bad);
+    if constexpr (LOCAL) {
+        constexpr int NW = 4 * split_waves(HD), W = BF && HD >= 128 ? 8 : 4;
+        extern __shared__ __align__(16) float sh_o[];       // [NW][cols][HD], then maxima and sums [NW][cols]
+        float2 *sh_s = (float2 *)(sh_o + NW * sp.cols * HD);
+        float L = l + __shfl_xor(l, 16, 64);
+        L += __shfl_xor(L, 32, 64);
+        if (mine) {
+            float *o = sh_o + (wave * sp.cols + col) * HD;
+#pragma unroll
+            for (int c = 0; c < NA / W; ++c)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int i = 0; i < W; ++i) o[16 * W * c + W * (4 * g + r) + i] = acc[W * c + i][r];
+            if (g == 0) sh_s[wave * sp.cols + col] = make_float2(m, L);
+        }
+        __syncthreads();
+        const int32_t nc = min(16, a.group - 16 * cb);
+        for (int32_t x = tid; x < nc * HD; x += 64 * NW) {
+            const int32_t c = x / HD, d = x % HD;
+            float M = -INFINITY, sum = 0.f, v = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) M = fmaxf(M, sh_s[w * sp.cols + c].x);
+            const float Ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float2 ml = sh_s[w * sp.cols + c];
+                const float f = exp2_hw(ml.x - Ms);
+                sum += ml.y * f;
+                v += sh_o[(w * sp.cols + c) * HD + d] * f;
+            }
+            from_f32((E *)at.out + (int64_t)b0 * at.ldo + (int64_t)(kvh * a.group + cb * 16 + c) * HD + d, sum == 0.f ? 0.f : v / sum);
+        }
+    }
 }
 
 // Put the pieces of a sequence (blockIdx.y) together, and form its scores.  Workgroups below n_heads take a
@@ -591,6 +642,7 @@ int tile_tokens(int dtype, int hd) { return dtype == LORA_F32 && hd > 64 ? 16 : 
 struct SplitPlan {
     int32_t R, ncb, hu, cols;
     int64_t tiles;
+    bool local;
     size_t off_ml, off_done, off_logits, total;
 };
 SplitPlan split_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int64_t max_len, bool scores) {
@@ -600,13 +652,16 @@ SplitPlan split_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, in
     s.cols = std::min(group, 16);
     s.ncb = (group + 15) / 16;
     s.hu = n_kv * s.ncb;
+    // One workgroup per (sequence, head) where the chip holds them all at once and none of their waves gets more than
+    // four tiles; scores need every head's sums, so they keep the second launch.
+    s.local = !scores && (int64_t)n_seq * s.hu <= 256 && (max_len + tt - 1) / tt <= 4 * 4 * split_waves(hd);
     // as many waves as the chip holds; no more ranges than tiles
     s.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, 1024 * split_waves(hd) / s.hu));
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     s.off_ml = up((size_t)s.R * 2 * n_heads * hd * 4);
     s.off_done = s.off_ml + up((size_t)s.R * 2 * n_heads * 8);
     s.off_logits = s.off_done + up((size_t)n_seq * n_heads * 8);
-    s.total = s.off_logits + (scores ? up((size_t)s.hu * tiles * s.cols * tt * 4) : 0);
+    s.total = s.local ? 0 : s.off_logits + (scores ? up((size_t)s.hu * tiles * s.cols * tt * 4) : 0);
     return s;
 }
 
@@ -616,9 +671,20 @@ hipError_t run(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s) {
     char *ws = (char *)at.ws;
     const KvSplit sp{pl.R, pl.ncb, pl.hu, (float *)ws, (float2 *)(ws + pl.off_ml), (float2 *)(ws + pl.off_done),
                      pl.cols, pl.tiles, (float *)(ws + pl.off_logits)};
+    if (pl.local) {
+        constexpr int NW = 4 * split_waves(HD);
+        const int lds = NW * pl.cols * (HD * 4 + 8);
+        if (lds > 64 * 1024) {                              // asked for on each device
+            const hipError_t e = hipFuncSetAttribute((const void *)k_kv_split<E, HD, false, true>,
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+            if (e != hipSuccess) return e;
+        }
+        hipLaunchKernelGGL((k_kv_split<E, HD, false, true>), dim3(pl.hu, a.n_seq), dim3(64 * NW), lds, s, a, at, sp);
+        return hipGetLastError();
+    }
     const dim3 grid((unsigned)(((int64_t)pl.R * pl.hu + 3) / 4));
-    if (at.scores) hipLaunchKernelGGL((k_kv_split<E, HD, true>), grid, dim3(256), 0, s, a, at, sp);
-    else hipLaunchKernelGGL((k_kv_split<E, HD, false>), grid, dim3(256), 0, s, a, at, sp);
+    if (at.scores) hipLaunchKernelGGL((k_kv_split<E, HD, true, false>), grid, dim3(256), 0, s, a, at, sp);
+    else hipLaunchKernelGGL((k_kv_split<E, HD, false, false>), grid, dim3(256), 0, s, a, at, sp);
     const int32_t sb = at.scores ? (a.cap + 255) / 256 : 0;
     hipLaunchKernelGGL((k_kv_join<E, HD>), dim3(a.n_heads + sb, a.n_seq), dim3(256),
                        at.scores ? std::max(a.n_heads, 256) * sizeof(float2) : 0, s, a, at, sp);
