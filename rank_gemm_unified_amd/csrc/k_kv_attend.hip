@@ -17,6 +17,7 @@ struct KvSplit {
     int32_t R;                // ranges
     int32_t ncb;              // blocks of 16 query heads of one K/V head
     int32_t hu;               // K/V heads * ncb
+    int32_t jh;               // heads a workgroup of the join takes: 4, or 1
     float *part_o;            // [R][2][n_heads][head_dim]: slot 0 a range's first piece, 1 its last
     float2 *part_ml;          // [R][2][n_heads]: maximum (base-2 logits), sum
     float2 *done_ml;          // [n_seq][n_heads]: of the sequences one range saw whole
@@ -29,15 +30,8 @@ template <typename E, int HD> struct Tile;   // tokens per step
 template <int HD> struct Tile<uint16_t, HD> { static constexpr int TT = 32; };
 template <int HD> struct Tile<float, HD> { static constexpr int TT = HD == 64 ? 32 : 16; };
 
-__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// The tiles of all sequences: their number, and where each of up to four places (one per wave of the
-// workgroup) lies.  All 256 threads call.
-struct Places {
-    int64_t total;
-    int32_t b[4], j[4];
-};
+// Tiles of sequence b.
 template <int TT>
 __device__ __forceinline__ int32_t seq_tiles(const KvArgs &a, int32_t b) {
     const int32_t n = a.lens[b];
@@ -289,10 +283,9 @@ __global__ __launch_bounds__(LOCAL ? 256 * split_waves(HD) : 256, split_waves(HD
 #pragma unroll
                     for (int i = 0; i < W; i += 4) *(float4 *)(po + d + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 } else if constexpr (BF && W == 8) {
-                    store16(o + d, pack_bf16x8(v));
+                    store16(o + d, u32x4_t{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])});
                 } else if constexpr (BF) {
-                    *(uint2 *)(o + d) = make_uint2(f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
-                                                   f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16);
+                    *(uint2 *)(o + d) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
                 } else {
                     *(float4 *)(o + d) = make_float4(v[0], v[1], v[2], v[3]);
                 }
@@ -410,8 +403,7 @@ __global__ __launch_bounds__(LOCAL ? 256 * split_waves(HD) : 256, split_waves(HD
                     const float a0 = S[2 * q + x / 2][2 * (x & 1)], a1 = S[2 * q + x / 2][2 * (x & 1) + 1];
                     const uint32_t h0 = __float_as_uint(a0) & 0xffff0000u, h1 = __float_as_uint(a1) & 0xffff0000u;
                     hi[x] = h0 >> 16 | h1;
-                    lo[x] = f32_to_bf16_bits(fmaxf(a0 - __uint_as_float(h0), 0x1p-100f)) |
-                            f32_to_bf16_bits(fmaxf(a1 - __uint_as_float(h1), 0x1p-100f)) << 16;
+                    lo[x] = pack2(fmaxf(a0 - __uint_as_float(h0), 0x1p-100f), fmaxf(a1 - __uint_as_float(h1), 0x1p-100f));
                 }
                 constexpr int W = HD == 64 ? 4 : 8;
 #pragma unroll
@@ -497,8 +489,9 @@ __global__ __launch_bounds__(LOCAL ? 256 * split_waves(HD) : 256, split_waves(HD
     }
 }
 
-// Put the pieces of a sequence (blockIdx.y) together, and form its scores.  Workgroups below n_heads take a
-// head: each of the four waves a part of the pieces, joined in LDS.  The others take 256 tokens' scores.
+// Put the pieces of a sequence (blockIdx.y) together, and form its scores.  The first workgroups take jh heads
+// each: a wave to a head where the pieces are few, else all four waves a part of the pieces of one head after the
+// other, joined in LDS.  The others take 256 tokens' scores.
 template <typename E, int HD>
 __global__ __launch_bounds__(256) void k_kv_join(KvArgs a, KvAttend at, KvSplit sp) {
     constexpr int TT = Tile<E, HD>::TT;
@@ -506,62 +499,83 @@ __global__ __launch_bounds__(256) void k_kv_join(KvArgs a, KvAttend at, KvSplit 
     __shared__ int64_t sh[8];
     __shared__ float sh_o[4][HD], sh_m[4], sh_l[4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int32_t b = blockIdx.y, h = blockIdx.x, first = (h - a.n_heads) * 256;
+    const int32_t join_wgs = (a.n_heads + sp.jh - 1) / sp.jh, b = blockIdx.y, first = ((int32_t)blockIdx.x - join_wgs) * 256;
     const int32_t n = a.lens[b], nt = seq_tiles<TT>(a, b);
     if (first >= 0 && (nt == 0 || first >= n)) return;
     int64_t total;
     const int64_t t0 = tiles_before<TT>(a, b, sh, &total);
     if (first < 0) {
-        E *o = (E *)at.out + (int64_t)b * at.ldo + (int64_t)h * HD;
+        const int32_t h0 = blockIdx.x * sp.jh;
+        constexpr int PER = HD / 64;
+        E *out = (E *)at.out + (int64_t)b * at.ldo;
         if (nt == 0) {
-            for (int d = tid; d < HD; d += 256) from_f32(o + d, 0.f);
+            if (wave < sp.jh && h0 + wave < a.n_heads)
+#pragma unroll
+                for (int i = 0; i < PER; ++i) from_f32(out + (int64_t)(h0 + wave) * HD + 64 * i + lane, 0.f);
             return;
         }
         const Pieces p = pieces_of(t0, t0 + nt, ranges_of(total, sp.R));
         if (p.r0 == p.r1) return;
-        constexpr int PER = HD / 64;
-        float m = -INFINITY, l = 0.f, acc[PER];
+        // pieces r, r + by, ... of head h: a lane's dims, and the maximum and sum they go by; four loads at once
+        float m, l, acc[PER];
+        auto gather = [&](int32_t h, int32_t r, int32_t by) {
+            m = -INFINITY;
+            l = 0.f;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-        for (int32_t r = p.r0 + wave; r <= p.r1; r += 16) {    // four pieces' loads at once
-            float2 ml[4];
-            float v[4][PER];
+            for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+            for (; r <= p.r1; r += 4 * by) {
+                float2 ml[4];
+                float v[4][PER];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int32_t ru = min(r + 4 * u, p.r1);
-                const int64_t pl = ((int64_t)ru * 2 + (ru == p.r0 ? p.s0 : 0)) * a.n_heads + h;
-                ml[u] = sp.part_ml[pl];
+                for (int u = 0; u < 4; ++u) {
+                    const int32_t ru = min(r + by * u, p.r1);
+                    const int64_t pl = ((int64_t)ru * 2 + (ru == p.r0 ? p.s0 : 0)) * a.n_heads + h;
+                    ml[u] = sp.part_ml[pl];
 #pragma unroll
-                for (int i = 0; i < PER; ++i) v[u][i] = sp.part_o[pl * HD + 64 * i + lane];
+                    for (int i = 0; i < PER; ++i) v[u][i] = sp.part_o[pl * HD + 64 * i + lane];
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (r + by * u > p.r1) break;
+                    const float mn = fmaxf(m, ml[u].x), ms = mn == -INFINITY ? 0.f : mn;
+                    const float c = exp2_hw(m - ms), w = exp2_hw(ml[u].x - ms);
+                    l = l * c + ml[u].y * w;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) acc[i] = acc[i] * c + v[u][i] * w;
+                    m = mn;
+                }
             }
+        };
+        if (sp.jh == 4 && p.r1 - p.r0 < 8) {                // few pieces: a wave to a head
+            if (h0 + wave < a.n_heads) {
+                gather(h0 + wave, p.r0, 1);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (r + 4 * u > p.r1) break;
-                const float mn = fmaxf(m, ml[u].x), ms = mn == -INFINITY ? 0.f : mn;
-                const float c = exp2_hw(m - ms), w = exp2_hw(ml[u].x - ms);
-                l = l * c + ml[u].y * w;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) acc[i] = acc[i] * c + v[u][i] * w;
-                m = mn;
+                for (int i = 0; i < PER; ++i) from_f32(out + (int64_t)(h0 + wave) * HD + 64 * i + lane, acc[i] * inv);
             }
+            return;
         }
+        for (int32_t h = h0; h < min(h0 + sp.jh, a.n_heads); ++h) {
+            gather(h, p.r0 + wave, 4);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) sh_o[wave][64 * i + lane] = acc[i];
-        if (lane == 0) { sh_m[wave] = m; sh_l[wave] = l; }
-        __syncthreads();
-        const float M = fmaxf(fmaxf(sh_m[0], sh_m[1]), fmaxf(sh_m[2], sh_m[3])), Ms = M == -INFINITY ? 0.f : M;
-        float L = 0.f, w[4];
+            for (int i = 0; i < PER; ++i) sh_o[wave][64 * i + lane] = acc[i];
+            if (lane == 0) { sh_m[wave] = m; sh_l[wave] = l; }
+            __syncthreads();
+            const float M = fmaxf(fmaxf(sh_m[0], sh_m[1]), fmaxf(sh_m[2], sh_m[3])), Ms = M == -INFINITY ? 0.f : M;
+            float L = 0.f, w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[i] = exp2_hw(sh_m[i] - Ms);
-            L += sh_l[i] * w[i];
-        }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        for (int d = tid; d < HD; d += 256) {
-            float v = 0.f;
+            for (int i = 0; i < 4; ++i) {
+                w[i] = exp2_hw(sh_m[i] - Ms);
+                L += sh_l[i] * w[i];
+            }
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            for (int d = tid; d < HD; d += 256) {
+                float v = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v += sh_o[i][d] * w[i];
-            from_f32(o + d, v * inv);
+                for (int i = 0; i < 4; ++i) v += sh_o[i][d] * w[i];
+                from_f32(out + (int64_t)h * HD + d, v * inv);
+            }
+            __syncthreads();
         }
         return;
     }
@@ -652,9 +666,12 @@ SplitPlan split_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, in
     s.cols = std::min(group, 16);
     s.ncb = (group + 15) / 16;
     s.hu = n_kv * s.ncb;
-    // One workgroup per (sequence, head) where the chip holds them all at once and none of their waves gets more than
-    // four tiles; scores need every head's sums, so they keep the second launch.
-    s.local = !scores && (int64_t)n_seq * s.hu <= 256 && (max_len + tt - 1) / tt <= 4 * 4 * split_waves(hd);
+    // One workgroup per (sequence, head), all of them on the chip at once, where none of their waves gets more than a few
+    // tiles: 32 heads of 128, one sequence of 203 tokens 6.3 us (ranges and join: 11.2), of 768 12.2 (12.9), of 1024
+    // 14.7 (13.8); eight of 1024 23.6 (29.6).  Behind that the ranges are as fast, and lengths that differ leave
+    // none of their waves idle.  Scores need every head's sums, so they keep the second launch.
+    const int64_t wgs = (int64_t)n_seq * s.hu;
+    s.local = !scores && wgs <= 256 && (max_len + tt - 1) / tt <= (wgs < 64 ? 3 : 4) * 4 * split_waves(hd);
     // as many waves as the chip holds; no more ranges than tiles
     s.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, 1024 * split_waves(hd) / s.hu));
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
@@ -669,7 +686,10 @@ template <typename E, int HD>
 hipError_t run(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s) {
     const SplitPlan pl = split_plan(dtype, a.n_heads, a.n_kv, HD, a.n_seq, a.cap, at.scores != nullptr);
     char *ws = (char *)at.ws;
-    const KvSplit sp{pl.R, pl.ncb, pl.hu, (float *)ws, (float2 *)(ws + pl.off_ml), (float2 *)(ws + pl.off_done),
+    // a wave to a head where a sequence has a few pieces on average (64 sequences, 64 ranges: 14.3 -> 11.6 us with
+    // scores); all four waves to one where it has many (8 sequences, 256 ranges: 15.5 us, one wave 26.8)
+    const int32_t jh = pl.R <= 4 * a.n_seq ? 4 : 1;
+    const KvSplit sp{pl.R, pl.ncb, pl.hu, jh, (float *)ws, (float2 *)(ws + pl.off_ml), (float2 *)(ws + pl.off_done),
                      pl.cols, pl.tiles, (float *)(ws + pl.off_logits)};
     if (pl.local) {
         constexpr int NW = 4 * split_waves(HD);
@@ -686,7 +706,7 @@ hipError_t run(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s) {
     if (at.scores) hipLaunchKernelGGL((k_kv_split<E, HD, true, false>), grid, dim3(256), 0, s, a, at, sp);
     else hipLaunchKernelGGL((k_kv_split<E, HD, false, false>), grid, dim3(256), 0, s, a, at, sp);
     const int32_t sb = at.scores ? (a.cap + 255) / 256 : 0;
-    hipLaunchKernelGGL((k_kv_join<E, HD>), dim3(a.n_heads + sb, a.n_seq), dim3(256),
+    hipLaunchKernelGGL((k_kv_join<E, HD>), dim3((a.n_heads + sp.jh - 1) / sp.jh + sb, a.n_seq), dim3(256),
                        at.scores ? std::max(a.n_heads, 256) * sizeof(float2) : 0, s, a, at, sp);
     return hipGetLastError();
 }

@@ -17,8 +17,6 @@
 namespace lorapool {
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
@@ -33,12 +31,6 @@ struct KvChunk {
     float *part;              // [n_seq][n_kv][cap_ld]: a K/V head's share of the scores
     int64_t cap_ld;
 };
-
-__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {   // two floats to bfloat16, round to nearest even
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
-}
 
 template <typename E, int HD>
 struct Chunk {
@@ -343,7 +335,7 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
             // harm, and the accumulators need no rescaling.
             if (__any(mt > m + 8.f)) {
                 const float mn = fmaxf(m, mt), ms = mn == -INFINITY ? 0.f : mn;
-                const float c = exp2_fast(m - ms);
+                const float c = exp2_hw(m - ms);
                 m = mn;
                 l *= c;
 #pragma unroll
@@ -358,7 +350,7 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    S[nb][i] = exp2_fast(S[nb][i] * sc - ms);
+                    S[nb][i] = exp2_hw(S[nb][i] * sc - ms);
                     ps += S[nb][i];
                 }
             l += ps;
@@ -563,7 +555,7 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
                     const int32_t last = old + r + 32 * qb + col - tw - 4 * hh;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float w = exp2_fast(S[qb][i] * scale2 - st[qb].x) * st[qb].y;
+                        const float w = exp2_hw(S[qb][i] * scale2 - st[qb].x) * st[qb].y;
                         sum[i] += 8 * (i / 4) + (i & 3) > last ? 0.f : w;
                     }
                 }
@@ -571,7 +563,7 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
 #pragma unroll
                 for (int qb = 0; qb < NB; ++qb)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) sum[i] += exp2_fast(S[qb][i] * scale2 - st[qb].x) * st[qb].y;
+                    for (int i = 0; i < 16; ++i) sum[i] += exp2_hw(S[qb][i] * scale2 - st[qb].x) * st[qb].y;
             }
         }
         r += NQ;

@@ -63,21 +63,14 @@ __device__ __forceinline__ void check_seqs(const KvArgs &a) {
     record(a, bits);
 }
 
-// The sequence that row t belongs to, found by the whole workgroup (-1: none); all threads must call.
-// A range that seq_rows() would not accept owns no row.  `sh` is one int of LDS.
-__device__ __forceinline__ int32_t find_seq(const KvArgs &a, int32_t t, int32_t *sh) {
-    if (!a.q_start) return t < a.n_seq ? t : -1;
-    if (threadIdx.x == 0) *sh = -1;
-    __syncthreads();
-    for (int32_t b = threadIdx.x; b < a.n_seq; b += blockDim.x) {
-        const int32_t s0 = a.q_start[b], s1 = a.q_start[b + 1];
-        if (s0 >= 0 && s1 <= a.T && s0 <= t && t < s1) atomicMax(sh, b);
-    }
-    __syncthreads();
-    const int32_t b = *sh;
-    __syncthreads();
-    return b;
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack2(float a, float b) {   // two floats to bfloat16, round to nearest even
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
 }
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+// A value that is the same in every lane of the wave, as a scalar.
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(uint16_t v) { return bf16_bits_to_f32(v); }
