@@ -539,6 +539,10 @@ class Pool:
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=dev)
 
+    def _like(self, here, stream, t):
+        """As _empty, for a contiguous tensor of t's kind (the quickest of torch's calls that allocate)."""
+        return self.torch.empty_like(t) if here else self._empty(here, stream, t.shape, t.dtype)
+
     def _kv_rows(self, what, t, width):
         """Rows of `width` elements of the pool's type: how far they lie apart."""
         shape, stride = t.shape, t.stride()
@@ -554,9 +558,12 @@ class Pool:
             raise ValueError(f"{what}: contiguous {dtype} {shape} on {self.pages.device} is wanted, not {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
 
-    def _kv_table(self, table, lens, q_start):
+    def _kv_pages(self):
         if self.pages is None:
             raise ValueError("a bookkeeping-only pool holds no KV vectors")
+
+    def _kv_table(self, table, lens, q_start):
+        self._kv_pages()
         i32 = torch.int32
         n, mp = table.shape[0], table.shape[-1]
         self._kv_ints("table", table, (n, 2, mp), i32)
@@ -628,17 +635,20 @@ class Pool:
         """Thin the caches out by accumulated attention (lora_kv_evict).  table: int32 [layers, n_seq, 2,
         max_pages]; scores: float32 [layers, n_seq, max_pages * tokens_per_page].  Returns (table, scores, lens,
         dropped, n_dropped), the first two the tensors passed in if in_place."""
+        self._kv_pages()
         layers, n, mp = table.shape[0], table.shape[1], table.shape[-1]
         self._kv_ints("table", table, (layers, n, 2, mp), torch.int32)
         self._kv_ints("scores", scores, (layers, n, mp * layout.tokens_per_page), torch.float32)
         self._kv_ints("lens", lens, (n,), torch.int32)
         max_drop = mp if max_drop is None else max_drop
         handle, here = self._where(stream)
-        table_out = table if in_place else self._empty(here, stream, table.shape, torch.int32)
-        scores_out = scores if in_place else self._empty(here, stream, scores.shape, torch.float32)
-        lens_out = self._empty(here, stream, (n,), torch.int32)
-        dropped = self._empty(here, stream, (layers, n, 2, max_drop), torch.int32)
-        n_dropped = self._empty(here, stream, (n,), torch.int32)
+        table_out = table if in_place else self._like(here, stream, table)
+        scores_out = scores if in_place else self._like(here, stream, scores)
+        lens_out, n_dropped = self._like(here, stream, lens), self._like(here, stream, lens)
+        if max_drop == mp:
+            dropped = self._like(here, stream, table)
+        else:
+            dropped = self._empty(here, stream, (layers, n, 2, max_drop), torch.int32)
         lora_kv_evict(self.handle, layout, layers, n, table.data_ptr(), table_out.data_ptr(), mp, scores.data_ptr(),
                       scores_out.data_ptr(), lens.data_ptr(), lens_out.data_ptr(), budget, keep_first, keep_last,
                       dropped.data_ptr(), max_drop, n_dropped.data_ptr(), stream=handle)

@@ -181,3 +181,17 @@ def test_reference_forms_agree_with_loops():
             want_sc[: len(p)] += p
             assert np.allclose(out[r, h * 64:(h + 1) * 64], sum(a * b for a, b in zip(p, v)), atol=1e-12)
     assert np.allclose(sc[0, :n], want_sc, atol=1e-12) and (sc[0, n:] == 0).all()
+
+
+def test_methods_refuse_a_bookkeeping_pool():
+    import torch
+
+    i32 = dict(dtype=torch.int32)
+    table, lens, q = torch.zeros((3, 2, 4), **i32), torch.ones(3, **i32), torch.zeros((3, 512), dtype=torch.bfloat16)
+    scores = torch.zeros((1, 3, 8))
+    for call in (lambda: POOL.kv_write(L, q[:, :128], q[:, :128], table, lens),
+                 lambda: POOL.kv_attend(L, q, table, lens),
+                 lambda: POOL.kv_attend_chunk(L, q, table, lens, torch.arange(4, **i32)),
+                 lambda: POOL.kv_evict(L, table[None], scores, lens, 4)):
+        with pytest.raises(ValueError, match="bookkeeping-only"):
+            call()
