@@ -422,7 +422,8 @@ size_t lora_kv_attend_workspace_size(const lora_pool *pool, const lora_kv_layout
  *   prior        the same shape; NULL: zeros.  May be `scores` itself (accumulate in place); must not
  *                overlap it otherwise
  *   workspace    as lora_project's
- * The out element is rounded once from float32.  Where every weight is zero (no token, or each
+ * The out element is rounded once from float32; bfloat16 pools: the weights enter the product with V
+ * as the sum of two bfloat16 numbers, off by at most 2^-15 of themselves.  Where every weight is zero (no token, or each
  * product is -inf) the output is zero.  Results do not change from call to call of the same shape.
  * Errors: LORA_EINVAL, LORA_EHIP.
  */

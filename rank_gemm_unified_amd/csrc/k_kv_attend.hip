@@ -7,6 +7,13 @@
 // heads of the same pages.  A range ends inside a sequence as a rule: what a wave has of a sequence it
 // did not see whole goes to the workspace with its maximum and sum, and k_kv_join puts the pieces
 // together (split and joined, no atomics: results do not change from call to call).
+//
+// The logits go through the matrix units although a decode step leaves most of their columns empty (16 query heads of a
+// K/V head, one where none is shared): a first kernel on the vector units, whose sums cross lanes, took 680 us for the
+// 64 sequences below.  bfloat16, head_dim 128, 32 heads, with scores: 64 sequences of up to 1031 tokens (637 MB of K, V
+// and scores): 116 - 121 us (5.3 - 5.5 TB/s), and 11.6 us for the join, which reads the logits; 8 of up to 32768 on
+// 8 K/V heads (748 MB): 138 - 146 us (5.1 - 5.4 TB/s), and 15.7.  float32, 16 sequences of up to 777 tokens, 16 heads
+// of 64, in one launch: 18.7 us (3.6 TB/s: few tiles a wave).  A copy of 1 GiB reaches 5.5 TB/s.
 #include <algorithm>
 
 #include "kv_device.h"

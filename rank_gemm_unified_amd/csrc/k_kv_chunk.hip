@@ -9,6 +9,12 @@
 // so that a lane holds one query row's logits, and the products of the first are, after the softmax,
 // in place as the right operand of the second: the weights never leave their registers.  V^T comes out of
 // LDS through the transposing read.  Two workgroups a CU: one's softmax runs under the other's products.
+//
+// bfloat16, head_dim 128, 32 heads: the last 2048 of 16384 tokens on 8 K/V heads (515 GFLOP) 542 us, 950 TFLOP/s, where a
+// large matrix product reaches 1220; one prompt of 4096 tokens (137 GFLOP) 194 us; eight of 512 (17 GFLOP, 134 MB)
+// 48.7 us.  A long cache is bound by one wave's chain of LDS reads, products and softmax with two waves a SIMD; short prompts
+// by what a workgroup does around its steps (8 us: its sequence, its page ids, the first K, the rows' way out;
+// 2 us a step).  float32, head_dim 64, 5 x 201 tokens behind 130: 30.4 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -430,6 +436,8 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
 // A token's weights can be summed only when its rows' maxima and sums are known.  One workgroup takes 128
 // tokens of one K/V head, K in registers, and walks the query rows of the heads that share it; the logits are
 // multiplied again (half of the attention's products), and a lane sums its query rows' weights for each of its tokens.
+// 8 x 512 tokens, 32 heads of 128: 28.0 us (two blocks of rows at a time; one: 36; 64 tokens a workgroup and rows
+// summed one exchange a token: 44), and 4.1 for the sum over the K/V heads.
 template <typename E, int HD>
 struct Scores {
     static constexpr bool BF = sizeof(E) == 2;

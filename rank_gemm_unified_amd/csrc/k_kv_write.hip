@@ -1,5 +1,7 @@
 // New tokens' K and V rows into their pages.  A copy: bound by the bytes moved, each row read and
-// written once, 16 bytes per lane.
+// written once, 16 bytes per lane; for few tokens by the two look-ups before it (sequence and length, then page).
+// 8 x 512 tokens of 8 KiB rows (134 MB moved): 25.3 - 26.8 us, 5.0 - 5.3 TB/s, a plain copy of 1 GiB reaches 5.5;
+// 64 tokens (2 MB): 4.4 us.
 #include <algorithm>
 
 #include "kv_device.h"
