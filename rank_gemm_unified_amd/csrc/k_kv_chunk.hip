@@ -341,7 +341,8 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
             // harm, and the accumulators need no rescaling.
             if (__any(mt > m + 8.f)) {
                 const float mn = fmaxf(m, mt), ms = mn == -INFINITY ? 0.f : mn;
-                const float c = exp2_hw(m - ms);
+                // (before a row's first weight the accumulators hold zeros, or infinities that the second pass added)
+                const float c = careful.value && m == -INFINITY ? 1.f : exp2_hw(m - ms);
                 m = mn;
                 l *= c;
 #pragma unroll

@@ -225,6 +225,23 @@ def test_a_bad_token_reaches_no_row_before_it(which, value, dtype):
         assert torch.isfinite(rows[:, group:, :3]).all() and torch.isfinite(rows[:, group:, 4:]).all()
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("at", [0, 5, 31, 40, 63, 64])
+def test_an_infinite_value_stays_infinite(at, dtype):
+    """In the rows from its own on, also where it lies in the first tokens that a row weighs."""
+    c = Case("gqa64", dtype, [150], [150])
+    want, tol, _, _ = c.ref()
+    tpp, dim = c.layout.tokens_per_page, c.layout.head_dim
+    c.pool.pages[int(c.table[0, 1, at // tpp]), (at % tpp) * 2 * dim + 3] = float("inf")   # first K/V head, element 3
+    out = c.run().cpu().to(torch.float64).numpy()
+    hit = np.zeros(want.shape, bool)
+    for h in range(4):
+        hit[at:, h * dim + 3] = True
+    assert (out[hit] == np.inf).all()
+    want[hit] = out[hit] = 0
+    close(torch.as_tensor(out), want, tol, c.dt, "out")
+
+
 def test_attend_values_pass_through():
     """Infinities and NaN of a token that is seen come through as the formula has them."""
     c = Case("mha64", "bf16", [90, 90, 90, 64])
