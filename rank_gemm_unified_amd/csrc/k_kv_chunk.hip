@@ -32,7 +32,7 @@ __device__ __forceinline__ s16x4_t read_tr(lds_s16x4 *__restrict__ p) { return _
 
 struct KvChunk {
     int32_t hpw;              // query heads of one K/V head a workgroup takes: 1, 2 or 4
-    int32_t slots_x;          // query tiles of one row of the grid
+    int32_t slots_x;          // query tiles (pairs of them) of one row of the grid
     float2 *stats;            // [n_heads][T]: maximum (base-2 logits) and 1 / sum of each row, for the scores; or null
     float *part;              // [n_seq][n_kv][cap_ld]: a K/V head's share of the scores
     int64_t cap_ld;
@@ -76,13 +76,16 @@ __device__ __forceinline__ uint64_t lane_units(const KvArgs &a, int32_t tok, int
     return __ballot(ok);
 }
 
-// The query tile that a slot stands for: sequence and tile in it; -1 behind the last.  Slots count tiles of
-// all sequences from the end, so that the longest rows of a sequence start first.  All 256 threads call.
+// What a slot stands for: sequence and tile, or pair of tiles, in it; -1 behind the last.  Slots count those of all
+// sequences from the end, so that the longest rows of a sequence start first.  All 256 threads call.
+template <bool PAIR>
+__device__ __forceinline__ int32_t slots_of(int32_t m, int32_t tq) { return ((m + tq - 1) / tq + PAIR) / (1 + PAIR); }
+template <bool PAIR>
 __device__ __forceinline__ int32_t find_tile(const KvArgs &a, int32_t slot, int32_t tq, int32_t *tile, SeqRows *rows, int32_t *sh) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int32_t per = (a.n_seq + 255) / 256, b0 = min(a.n_seq, tid * per), b1 = min(a.n_seq, b0 + per);
     int32_t mine = 0;
-    for (int32_t b = b0; b < b1; ++b) mine += (seq_rows(a, b).m + tq - 1) / tq;
+    for (int32_t b = b0; b < b1; ++b) mine += slots_of<PAIR>(seq_rows(a, b).m, tq);
     const int32_t incl = wave_incl_scan(mine, lane);
     if (lane == 63) sh[wave] = incl;
     if (tid == 0) sh[4] = -1;
@@ -97,7 +100,7 @@ __device__ __forceinline__ int32_t find_tile(const KvArgs &a, int32_t slot, int3
     if (want >= excl && want < excl + mine) {
         int32_t at = excl;
         for (int32_t b = b0; b < b1; ++b) {
-            const int32_t t = (seq_rows(a, b).m + tq - 1) / tq;
+            const int32_t t = slots_of<PAIR>(seq_rows(a, b).m, tq);
             if (want < at + t) {
                 const SeqRows q = seq_rows(a, b);
                 sh[4] = b;
@@ -118,7 +121,9 @@ __device__ __forceinline__ int32_t find_tile(const KvArgs &a, int32_t slot, int3
     return uniform(sh[4]);
 }
 
-template <typename E, int HD>
+// PAIR: a workgroup takes two tiles of a sequence, one from each end, one after the other: as much work for every pair,
+// and its start is paid once.
+template <typename E, int HD, bool PAIR>
 __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs a, KvAttend at, KvChunk ck) {
     using C = Chunk<E, HD>;
     constexpr int NT = C::NT, NB = C::NB, RB = C::RB, CH = C::CH, KQ = C::KQ, ND = HD / 32;
@@ -126,15 +131,31 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
     extern __shared__ __align__(256) char smem[];
     __shared__ int32_t sh[9];
     __shared__ unsigned long long sh_flag;
-    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 31, hh = lane >> 5;
+    const int wave = uniform((int)threadIdx.x >> 6);
     const int32_t groups = a.n_heads / ck.hpw, hg = blockIdx.x % groups, slot = blockIdx.y * ck.slots_x + blockIdx.x / groups;
     if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(a);
     const int32_t tq = 128 / ck.hpw;
     int32_t tile;
     SeqRows sq;
-    const int32_t b = find_tile(a, slot, tq, &tile, &sq, sh);
-    if (b < 0 || tile < 0 || tile >= (sq.m + tq - 1) / tq) return;   // (ranges that overlap can have more tiles than counted)
-    const int32_t head = hg * ck.hpw + (wave & (ck.hpw - 1)), q0 = tile * tq + (wave / ck.hpw) * 32;
+    const int32_t b = find_tile<PAIR>(a, slot, tq, &tile, &sq, sh), tiles = (sq.m + tq - 1) / tq;
+    if (b < 0 || tile < 0 || tile >= slots_of<PAIR>(sq.m, tq)) return;   // (ranges that overlap can have more than counted)
+    int32_t second = -1;
+    if constexpr (PAIR) {
+        const int32_t first = tiles - 1 - tile;
+        if (tile < first) second = tile;
+        tile = first;
+    }
+    const int32_t head = hg * ck.hpw + (wave & (ck.hpw - 1)), in_tile = (wave / ck.hpw) * 32;
+    const int32_t old = sq.n - sq.m;                        // tokens before the new ones
+    const int32_t *trow = a.table + (int64_t)b * 2 * a.max_pages;
+    const char *base = a.pages + (int64_t)(head / a.group) * RB;
+    const float scale2 = at.scale * 1.4426950408889634f;
+    bool placed = false;                                    // the addresses of the first tokens are in LDS
+    for (;;) {
+    int tid = threadIdx.x;
+    if constexpr (PAIR) asm volatile("" : "+v"(tid));       // what hangs on it is worked out for each tile, not kept over both
+    const int lane = tid & 63, col = lane & 31, hh = lane >> 5;
+    const int32_t q0 = tile * tq + in_tile;
     const int32_t qi = q0 + col;
     const bool row_ok = qi < sq.m;
     const int64_t row = sq.first + (row_ok ? qi : sq.m - 1);
@@ -143,17 +164,15 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
         if (row_ok)
             for (int d = hh * (HD / 2); d < (hh + 1) * (HD / 2); ++d) from_f32(orow + d, 0.f);
         if (ck.stats && row_ok && hh == 0) ck.stats[(int64_t)head * a.T + row] = make_float2(0.f, 0.f);
-        return;
+        if (!PAIR || second < 0) return;
+        tile = second;
+        second = -1;
+        continue;
     }
-    const int32_t old = sq.n - sq.m;                        // tokens before the new ones
     const int32_t pos = old + (row_ok ? qi : sq.m - 1);     // this lane's row sees tokens 0 .. pos
     const int32_t wave_lo = old + min(q0, sq.m - 1), wave_hi = old + min(q0 + 31, sq.m - 1);
     const int32_t wg_lo = old + tile * tq, wg_hi = old + min(tile * tq + tq, sq.m) - 1;
     const int32_t steps = wg_hi / NT + 1;
-    const int32_t *trow = a.table + (int64_t)b * 2 * a.max_pages;
-    const char *base = a.pages + (int64_t)(head / a.group) * RB;
-    const float scale2 = at.scale * 1.4426950408889634f;
-
     u32x4_t Q[KQ];
     {
         const char *p = (const char *)((const E *)at.q + row * at.ldq + (int64_t)head * HD) + 16 * hh;
@@ -237,9 +256,11 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
             for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
         m = -INFINITY;
         l = 0.f;
-        look_up(0);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        place(0);
+        if (!PAIR || !placed) {
+            look_up(0);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            place(0);
+        }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         fetch(0);
@@ -430,6 +451,11 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
             for (int x = 0; x < 4; ++x)
                 *(float4 *)(orow + 32 * d + 8 * x + 4 * hh) = make_float4(acc[d][4 * x] * inv, acc[d][4 * x + 1] * inv,
                                                                         acc[d][4 * x + 2] * inv, acc[d][4 * x + 3] * inv);
+    }
+    if (!PAIR || second < 0) return;
+    placed = steps <= 2 * SP - 2;                           // nothing has been put over them
+    tile = second;
+    second = -1;
     }
 }
 
@@ -624,16 +650,27 @@ hipError_t run(const KvArgs &a, const KvAttend &at, hipStream_t s) {
     KvChunk ck;
     ck.hpw = a.group % 4 == 0 ? 4 : a.group % 2 == 0 ? 2 : 1;
     const int32_t tq = 128 / ck.hpw;
-    const int32_t groups = a.n_heads / ck.hpw, slots = a.T / tq + std::min(a.n_seq, a.T);   // tiles, at most
-    ck.slots_x = std::min(slots, (1 << 22) / groups);       // a row of the grid has less than 2^32 threads
+    const int32_t groups = a.n_heads / ck.hpw;
     ck.cap_ld = ((int64_t)a.cap + 63) / 64 * 64;
     ck.stats = at.scores ? (float2 *)at.ws : nullptr;
     ck.part = (float *)((char *)at.ws + up256((size_t)a.T * a.n_heads * 8));
     constexpr int OUT = C::BF ? 4 * 32 * (C::RB + 16) : 0, LDS = std::max(C::LDS, OUT);
-    hipError_t e = big_lds((const void *)k_kv_chunk<E, HD>, LDS);
+    auto launch = [&](auto kernel, int32_t slots) {
+        const hipError_t e = big_lds((const void *)kernel, LDS);
+        if (e != hipSuccess) return e;
+        ck.slots_x = std::min(slots, (1 << 22) / groups);   // a row of the grid has less than 2^32 threads
+        const dim3 grid((unsigned)(groups * ck.slots_x), (unsigned)((slots + ck.slots_x - 1) / ck.slots_x));
+        hipLaunchKernelGGL(kernel, grid, dim3(256), LDS, s, a, at, ck);
+        return hipSuccess;
+    };
+    const int32_t seqs = std::min(a.n_seq, a.T), tiles = a.T / tq + seqs;   // at most
+    // Pairs where they fill the GPU, two workgroups a CU, and sequences are so short that starts count (32 heads of 128:
+    // 8 x 512 tokens 49.0 us one by one, 46.5 in pairs, 4 x 1024 68.4 and 65.8, 2 x 2048 104.9 and 108.7).  Not for
+    // float32 and head_dim 256, which products and registers bind.
+    constexpr bool CAN = C::BF && HD <= 128;
+    const hipError_t e = CAN && (int64_t)groups * (a.T / tq) >= 2 * 512 && a.cap <= 1024 ? launch(k_kv_chunk<E, HD, CAN>, (tiles + seqs + 1) / 2)
+                                                                        : launch(k_kv_chunk<E, HD, false>, tiles);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)(groups * ck.slots_x), (unsigned)((slots + ck.slots_x - 1) / ck.slots_x));
-    hipLaunchKernelGGL((k_kv_chunk<E, HD>), grid, dim3(256), LDS, s, a, at, ck);
     if (at.scores) {
         constexpr int TOK = Scores<E, HD>::TOK;
         hipLaunchKernelGGL((k_kv_chunk_scores<E, HD>), dim3(a.n_kv, (a.cap + TOK - 1) / TOK, a.n_seq), dim3(256), 0, s, a, at, ck);

@@ -23,6 +23,14 @@ GEO = {
     "dim256": (4, 2, 256, 2048, 4),
     "mha128": (32, 32, 128, 4096, 1),
 }
+# so many heads that a prompt's query tiles are taken in pairs
+WIDE = {
+    "wide64": (256, 256, 64, 16384, 1),
+    "wide64_kv64": (256, 64, 64, 4096, 1),
+    "wide64_kv128": (256, 128, 64, 16384, 2),
+    "wide128": (128, 128, 128, 16384, 1),
+    "wide128_kv32": (128, 32, 128, 4096, 1),
+}
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 
@@ -36,7 +44,7 @@ class Case:
     """A pool full of random vectors (every page, used or not), sequences with pages in random order."""
 
     def __init__(self, geo, dtype, lens, new=None, seed=1, extra_pages=3, gap=0):
-        nh, nkv, dim, H, tpp = GEO[geo]
+        nh, nkv, dim, H, tpp = {**GEO, **WIDE}[geo]
         self.layout, self.dt = rg.lora_kv_layout_t(nh, nkv, dim, tpp), DT[dtype]
         self.lens, self.n = list(lens), len(lens)
         self.mp = max(1, max(-(-n // tpp) for n in lens)) + extra_pages
@@ -157,6 +165,37 @@ def test_chunk_lengths(geo, dtype):
 ])
 def test_chunk_shapes(geo, dtype, lens, new):
     check(Case(geo, dtype, lens, new, seed=4, gap=1))
+
+
+@pytest.mark.parametrize("geo,lens,new", [
+    ("wide64", [300, 1, 0, 257, 128], [300, 1, 0, 129, 128]), ("wide64", [613, 5], [513, 5]),       # longer than the addresses kept
+    ("wide64_kv64", [200, 97, 290], [200, 33, 290]), ("wide64_kv128", [401, 129], [384, 129]),
+    ("wide128", [260, 384, 385], [260, 384, 385]), ("wide128_kv32", [390, 0, 7, 400, 300], [390, 0, 7, 400, 300]),
+    ("wide64", [513], [513]), ("wide64", [64] * 9, [64] * 9),
+])
+def test_chunk_pairs(geo, lens, new):
+    """Query tiles taken two a workgroup: odd and even numbers of them, sequences of one, none, and long ones."""
+    c = Case(geo, "bf16", lens, new, seed=6, gap=1)
+    group = c.layout.n_heads // c.layout.n_kv_heads
+    hpw = 4 if group % 4 == 0 else 2 if group % 2 == 0 else 1
+    assert c.layout.n_heads // hpw * (c.T // (128 // hpw)) >= 1024
+    check(c)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("at", [40, 130, 300])
+def test_chunk_pairs_hide_what_comes_later(at, value):
+    """A value that is not finite reaches the rows from its own position on, in either tile of a pair, and no other."""
+    c = Case("wide64", "bf16", [384, 140], [384, 140], seed=7)
+    want, tol, _, _ = c.ref()
+    c.pool.pages[int(c.table[0, 1, at]), 64 * 9 + 3] = value
+    out = c.run()
+    hit = np.zeros(want.shape, bool)
+    hit[at:384, 64 * 9 + 3] = True
+    got = out.cpu().to(torch.float64).numpy()
+    assert (np.isnan(got[hit]) if value != value else got[hit] == value).all()
+    want[hit] = 0
+    close(torch.as_tensor(np.where(hit, 0, got)), want, np.where(hit, 1, tol), c.dt, "out")
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
