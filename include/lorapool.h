@@ -432,7 +432,8 @@ int lora_kv_attend(lora_pool *pool, const lora_kv_layout_t *layout, const void *
                    int64_t max_len, float scale, void *out, int64_t ldo, const float *prior,
                    float *scores, void *workspace, size_t workspace_bytes, void *stream);
 
-/* As lora_kv_attend_workspace_size, for lora_kv_attend_chunk with T rows. */
+/* As lora_kv_attend_workspace_size, for lora_kv_attend_chunk with T rows.  Never less for more rows,
+ * sequences or tokens: a workspace of the largest call serves them all. */
 size_t lora_kv_attend_chunk_workspace_size(const lora_pool *pool, const lora_kv_layout_t *layout,
                                            int32_t n_seq, int64_t T, int64_t max_len,
                                            int32_t with_scores);

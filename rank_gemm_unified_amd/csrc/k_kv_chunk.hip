@@ -33,6 +33,9 @@ __device__ __forceinline__ s16x4_t read_tr(lds_s16x4 *__restrict__ p) { return _
 struct KvChunk {
     int32_t hpw;              // query heads of one K/V head a workgroup takes: 1, 2 or 4
     int32_t slots_x;          // query tiles (pairs of them) of one row of the grid
+    int32_t ranges;           // ranges of tokens a tile's are cut into, at most; 1: not cut
+    float *piece_o;           // [ranges][T][n_heads][head_dim]: sums of a range, not divided
+    float2 *piece_ml;         // [ranges][T][n_heads]: its maximum (base-2 logits) and sum
     float2 *stats;            // [n_heads][T]: maximum (base-2 logits) and 1 / sum of each row, for the scores; or null
     float *part;              // [n_seq][n_kv][cap_ld]: a K/V head's share of the scores
     int64_t cap_ld;
@@ -121,9 +124,16 @@ __device__ __forceinline__ int32_t find_tile(const KvArgs &a, int32_t slot, int3
     return uniform(sh[4]);
 }
 
+// Steps of one of a tile's ranges: whole runs of the tokens whose addresses are looked up together.
+constexpr int PH = 256;
+__device__ __forceinline__ int32_t range_steps(int32_t steps, int32_t ranges, int32_t run) {
+    return ((steps + ranges - 1) / ranges + run - 1) / run * run;
+}
+
 // PAIR: a workgroup takes two tiles of a sequence, one from each end, one after the other: as much work for every pair,
-// and its start is paid once.
-template <typename E, int HD, bool PAIR>
+// and its start is paid once.  SPLIT: it takes one range (blockIdx.z) of the tile's tokens, and k_kv_chunk_join puts the
+// ranges together.
+template <typename E, int HD, bool PAIR, bool SPLIT>
 __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs a, KvAttend at, KvChunk ck) {
     using C = Chunk<E, HD>;
     constexpr int NT = C::NT, NB = C::NB, RB = C::RB, CH = C::CH, KQ = C::KQ, ND = HD / 32;
@@ -133,7 +143,7 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
     __shared__ unsigned long long sh_flag;
     const int wave = uniform((int)threadIdx.x >> 6);
     const int32_t groups = a.n_heads / ck.hpw, hg = blockIdx.x % groups, slot = blockIdx.y * ck.slots_x + blockIdx.x / groups;
-    if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(a);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && (!SPLIT || blockIdx.z == 0)) check_seqs(a);
     const int32_t tq = 128 / ck.hpw;
     int32_t tile;
     SeqRows sq;
@@ -160,6 +170,7 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
     const bool row_ok = qi < sq.m;
     const int64_t row = sq.first + (row_ok ? qi : sq.m - 1);
     E *orow = (E *)at.out + row * at.ldo + (int64_t)head * HD;
+    if (SPLIT && sq.n == 0) return;
     if (sq.n == 0) {                                        // no tokens: zero rows
         if (row_ok)
             for (int d = hh * (HD / 2); d < (hh + 1) * (HD / 2); ++d) from_f32(orow + d, 0.f);
@@ -172,7 +183,14 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
     const int32_t pos = old + (row_ok ? qi : sq.m - 1);     // this lane's row sees tokens 0 .. pos
     const int32_t wave_lo = old + min(q0, sq.m - 1), wave_hi = old + min(q0 + 31, sq.m - 1);
     const int32_t wg_lo = old + tile * tq, wg_hi = old + min(tile * tq + tq, sq.m) - 1;
-    const int32_t steps = wg_hi / NT + 1;
+    constexpr int SP = PH / NT;                             // steps that one look-up of addresses lasts for
+    int32_t begin = 0, steps = wg_hi / NT + 1;              // the first step, and the one behind the last
+    if constexpr (SPLIT) {
+        const int32_t per = range_steps(steps, ck.ranges, SP);
+        begin = (int32_t)blockIdx.z * per;
+        if (begin >= steps) return;
+        steps = min(steps, begin + per);
+    }
     u32x4_t Q[KQ];
     {
         const char *p = (const char *)((const E *)at.q + row * at.ldq + (int64_t)head * HD) + 16 * hh;
@@ -181,7 +199,6 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
     }
     // Where the tokens' rows lie, PH tokens at a time: a thread looks one token's pages up and leaves the addresses in
     // LDS, in units of 128 bytes (every token row starts on one); tokens that are not there get the pool's first page.
-    constexpr int PH = 256, SP = PH / NT;                   // steps they last for
     uint32_t *units = (uint32_t *)(smem + 4 * C::BUF);           // [2][K, V][PH]
     int32_t *raw = (int32_t *)(units + 4 * PH) + 64 * wave;             // [K, V][PH]: page ids, this wave's 64 tokens
     uint64_t *masks = (uint64_t *)((uint32_t *)(smem + 4 * C::BUF) + 6 * PH);   // [2][PH / 64]: which tokens are there
@@ -257,14 +274,14 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
         m = -INFINITY;
         l = 0.f;
         if (!PAIR || !placed) {
-            look_up(0);
+            look_up(begin / SP);
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            place(0);
+            place(begin / SP);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
-        fetch(0);
-        for (int32_t j = 0; j < steps; ++j) {
+        fetch(begin);
+        for (int32_t j = begin; j < steps; ++j) {
             const int32_t t0 = j * NT;
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // this step's K and V are in
             __builtin_amdgcn_s_barrier();
@@ -424,6 +441,20 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
         for (int i = 0; i < 16; ++i) chk += acc[d][i] * 0.f;
     if (__syncthreads_or(chk != 0.f)) pass(std::true_type{});
     if (bad) record(a, bad);
+    if constexpr (SPLIT) {
+        const float sum = l + other_half(l);
+        if (row_ok) {
+            const int64_t at_piece = ((int64_t)blockIdx.z * a.T + row) * a.n_heads + head;
+            if (hh == 0) ck.piece_ml[at_piece] = make_float2(m, sum);
+            float *o = ck.piece_o + at_piece * HD;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    *(float4 *)(o + 32 * d + 8 * x + 4 * hh) = make_float4(acc[d][4 * x], acc[d][4 * x + 1], acc[d][4 * x + 2], acc[d][4 * x + 3]);
+        }
+        return;
+    }
     const float L = l + other_half(l), inv = L == 0.f ? 0.f : 1.f / L;
     if (ck.stats && row_ok && hh == 0) ck.stats[(int64_t)head * a.T + row] = make_float2(m == -INFINITY ? 0.f : m, inv);
     if constexpr (BF) {
@@ -457,6 +488,59 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
     tile = second;
     second = -1;
     }
+}
+
+// Put the ranges of a row (blockIdx.x) together: a wave to a head.
+constexpr int RANGES = 512;
+template <typename E, int HD>
+__global__ __launch_bounds__(256) void k_kv_chunk_join(KvArgs a, KvAttend at, KvChunk ck) {
+    __shared__ int32_t seq;
+    __shared__ float weight[4][RANGES];
+    const int32_t t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, head = blockIdx.y * 4 + wave;
+    if (tid == 0) seq = -1;
+    __syncthreads();
+    for (int32_t b = tid; b < a.n_seq; b += 256) {
+        const SeqRows q = seq_rows(a, b);
+        if (t >= q.first && t < q.first + q.m) atomicMax(&seq, b);
+    }
+    __syncthreads();
+    if (seq < 0 || head >= a.n_heads) return;
+    const SeqRows sq = seq_rows(a, seq);
+    constexpr int W = HD / 64;                              // dims of a lane
+    E *out = (E *)at.out + (int64_t)t * at.ldo + (int64_t)head * HD + W * lane;
+    const int32_t tq = 128 / ck.hpw, tile = (t - sq.first) / tq, last = sq.n - sq.m + min(tile * tq + tq, sq.m) - 1;
+    constexpr int NT = Chunk<E, HD>::NT;
+    const int32_t steps = last / NT + 1, per = range_steps(steps, ck.ranges, PH / NT);
+    const int32_t used = sq.n ? (steps + per - 1) / per : 0;
+    const int64_t first = (int64_t)t * a.n_heads + head, next = (int64_t)a.T * a.n_heads;
+    float M = -INFINITY;
+    for (int32_t s = lane; s < used; s += 64) M = fmaxf(M, ck.piece_ml[first + s * next].x);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
+    const float Ms = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    for (int32_t s = lane; s < used; s += 64) {
+        const float2 ml = ck.piece_ml[first + s * next];
+        const float w = exp2_hw(ml.x - Ms);
+        weight[wave][s] = w;
+        L += ml.y * w;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) L += __shfl_xor(L, o, 64);
+    __builtin_amdgcn_wave_barrier();
+    float v[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = 0.f;
+#pragma unroll 8
+    for (int32_t s = 0; s < used; ++s) {
+        const float *o = ck.piece_o + (first + s * next) * HD + W * lane;
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] += o[i] * weight[wave][s];
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int i = 0; i < W; ++i) from_f32(out + i, v[i] * inv);
+    if (ck.stats && lane == 0) ck.stats[(int64_t)head * a.T + t] = make_float2(Ms, inv);
 }
 
 // ---- scores: the weights once more, summed over the rows ---------------------------------------------
@@ -644,32 +728,74 @@ hipError_t big_lds(const void *kernel, int bytes) {
     return bytes <= 64 * 1024 ? hipSuccess : hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+struct ChunkPlan {
+    int32_t hpw, groups, tiles, ranges;
+    int64_t cap_ld;
+    size_t off_part, off_o, off_ml, total;
+};
+ChunkPlan chunk_plan(int n_heads, int n_kv, int hd, int32_t n_seq, int64_t T, int64_t max_len, bool scores) {
+    ChunkPlan p;
+    const int group = n_heads / n_kv;
+    p.hpw = group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1;
+    p.groups = n_heads / p.hpw;
+    const int32_t tq = 128 / p.hpw;
+    p.tiles = (int32_t)((T + std::min<int64_t>(n_seq, T) * (tq - 1)) / tq);   // at most
+    // A tile's tokens are cut into ranges of 256 or more where the tiles alone do not fill the GPU, two workgroups a CU (one,
+    // head_dim 256).  bfloat16, 32 heads of 128 on 8: 2 x 12 tokens behind up to 12664 287 us whole, 36 in ranges,
+    // 512 behind 15872 412 and 192; float32, 4 heads of 64 on 2, 4 x 1 behind 12898: 955 and 48.  Below 512 tokens the
+    // joining launch costs more (9 x 98 tokens behind 194, 16 heads of 256 on 4: 62 whole, 71 in two).
+    const int64_t wgs = (int64_t)p.groups * p.tiles, most = std::min<int64_t>(max_len / PH, RANGES);
+    const int slots = hd == 256 ? 256 : 512;
+    p.ranges = (int32_t)std::max<int64_t>(1, std::min(slots / std::max<int64_t>(wgs, 1), most));
+    p.cap_ld = (max_len + 63) / 64 * 64;
+    // The size grows with T and max_len, so that what serves the largest call serves them all: ranges * T * n_heads is
+    // at most 128 rows for each of the GPU's workgroups.
+    const int64_t rows = most < 2 ? 0 : std::min<int64_t>(most * T * n_heads, 128 * slots);
+    p.off_part = scores ? up256((size_t)T * n_heads * 8) : 0;
+    p.off_o = p.off_part + (scores ? up256((size_t)n_seq * n_kv * p.cap_ld * 4) : 0);
+    p.off_ml = p.off_o + up256((size_t)rows * hd * 4);
+    p.total = p.off_ml + up256((size_t)rows * 8);
+    return p;
+}
+
 template <typename E, int HD>
 hipError_t run(const KvArgs &a, const KvAttend &at, hipStream_t s) {
     using C = Chunk<E, HD>;
+    const ChunkPlan pl = chunk_plan(a.n_heads, a.n_kv, HD, a.n_seq, a.T, a.cap, at.scores != nullptr);
+    char *ws = (char *)at.ws;
     KvChunk ck;
-    ck.hpw = a.group % 4 == 0 ? 4 : a.group % 2 == 0 ? 2 : 1;
-    const int32_t tq = 128 / ck.hpw;
-    const int32_t groups = a.n_heads / ck.hpw;
-    ck.cap_ld = ((int64_t)a.cap + 63) / 64 * 64;
-    ck.stats = at.scores ? (float2 *)at.ws : nullptr;
-    ck.part = (float *)((char *)at.ws + up256((size_t)a.T * a.n_heads * 8));
+    ck.hpw = pl.hpw;
+    ck.ranges = pl.ranges;
+    ck.cap_ld = pl.cap_ld;
+    ck.stats = at.scores ? (float2 *)ws : nullptr;
+    ck.part = (float *)(ws + pl.off_part);
+    ck.piece_o = (float *)(ws + pl.off_o);
+    ck.piece_ml = (float2 *)(ws + pl.off_ml);
+    const int32_t tq = 128 / ck.hpw, groups = pl.groups;
     constexpr int OUT = C::BF ? 4 * 32 * (C::RB + 16) : 0, LDS = std::max(C::LDS, OUT);
     auto launch = [&](auto kernel, int32_t slots) {
         const hipError_t e = big_lds((const void *)kernel, LDS);
         if (e != hipSuccess) return e;
         ck.slots_x = std::min(slots, (1 << 22) / groups);   // a row of the grid has less than 2^32 threads
-        const dim3 grid((unsigned)(groups * ck.slots_x), (unsigned)((slots + ck.slots_x - 1) / ck.slots_x));
+        const dim3 grid((unsigned)(groups * ck.slots_x), (unsigned)((slots + ck.slots_x - 1) / ck.slots_x), (unsigned)ck.ranges);
         hipLaunchKernelGGL(kernel, grid, dim3(256), LDS, s, a, at, ck);
         return hipSuccess;
     };
-    const int32_t seqs = std::min(a.n_seq, a.T), tiles = a.T / tq + seqs;   // at most
+    const int32_t seqs = std::min(a.n_seq, a.T);
     // Pairs where they fill the GPU, two workgroups a CU, and sequences are so short that starts count (32 heads of 128:
     // 8 x 512 tokens 49.0 us one by one, 46.5 in pairs, 4 x 1024 68.4 and 65.8, 2 x 2048 104.9 and 108.7).  Not for
     // float32 and head_dim 256, which products and registers bind.
     constexpr bool CAN = C::BF && HD <= 128;
-    const hipError_t e = CAN && (int64_t)groups * (a.T / tq) >= 2 * 512 && a.cap <= 1024 ? launch(k_kv_chunk<E, HD, CAN>, (tiles + seqs + 1) / 2)
-                                                                        : launch(k_kv_chunk<E, HD, false>, tiles);
+    hipError_t e;
+    if (ck.ranges > 1) {
+        e = launch(k_kv_chunk<E, HD, false, true>, pl.tiles);
+        if (e == hipSuccess)
+            hipLaunchKernelGGL((k_kv_chunk_join<E, HD>), dim3(a.T, (a.n_heads + 3) / 4), dim3(256), 0, s, a, at, ck);
+    } else if (CAN && (int64_t)groups * (a.T / tq) >= 2 * 512 && a.cap <= 1024) {
+        e = launch(k_kv_chunk<E, HD, CAN, false>, (pl.tiles + seqs + 1) / 2);
+    } else {
+        e = launch(k_kv_chunk<E, HD, false, false>, pl.tiles);
+    }
     if (e != hipSuccess) return e;
     if (at.scores) {
         constexpr int TOK = Scores<E, HD>::TOK;
@@ -687,8 +813,7 @@ hipError_t by_dim(const KvArgs &a, const KvAttend &at, hipStream_t s) {
 }  // namespace
 
 size_t kv_chunk_ws_bytes(int, const lora_kv_layout_t &l, int32_t n_seq, int64_t T, int64_t max_len, bool scores) {
-    if (!scores) return 0;
-    return up256((size_t)T * l.n_heads * 8) + (size_t)n_seq * l.n_kv_heads * ((max_len + 63) / 64 * 64) * 4;
+    return chunk_plan(l.n_heads, l.n_kv_heads, l.head_dim, n_seq, T, max_len, scores).total;
 }
 
 hipError_t launch_kv_chunk(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s) {

@@ -182,6 +182,39 @@ def test_chunk_pairs(geo, lens, new):
     check(c)
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("geo,lens,new", [
+    ("gqa64", [5000, 0, 257, 1, 256, 2], [1, 0, 3, 1, 0, 2]), ("mqa128", [2500], [40]), ("group20", [1300, 511], [33, 1]),
+    ("dim256", [1025, 300], [7, 129]), ("group3", [900, 0, 513], [130, 2, 257]), ("mha64", [777] * 5, [3] * 5),
+])
+def test_chunk_ranges(geo, lens, new, dtype):
+    """Few rows on long caches: the tokens are cut into ranges, joined afterwards."""
+    if 0 in lens and new[lens.index(0)]:                        # a padded row that has new tokens: recorded, zero rows
+        c = Case(geo, dtype, lens, new, seed=8, gap=1)
+        want, tol, _, _ = c.ref()
+        out = c.run(out=torch.full((c.T, c.width), 7.25, dtype=c.dt, device="cuda"))
+        close(out, want, tol, c.dt, "out")
+        return
+    check(Case(geo, dtype, lens, new, seed=8, gap=1))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("at", [0, 255, 256, 700, 990, 999])
+def test_chunk_ranges_pass_infinities(at, dtype):
+    """An infinite value reaches the rows from its own on, whichever range holds it, and no other."""
+    c = Case("gqa64", dtype, [1000], [20])
+    want, tol, _, _ = c.ref()
+    tpp, dim = c.layout.tokens_per_page, c.layout.head_dim
+    c.pool.pages[int(c.table[0, 1, at // tpp]), (at % tpp) * 2 * dim + 3] = float("inf")
+    out = c.run().cpu().to(torch.float64).numpy()
+    hit = np.zeros(want.shape, bool)
+    for h in range(4):
+        hit[max(0, at - 980):, h * dim + 3] = True
+    assert (out[hit] == np.inf).all()
+    want[hit] = out[hit] = 0
+    close(torch.as_tensor(out), want, tol, c.dt, "out")
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("at", [40, 130, 300])
 def test_chunk_pairs_hide_what_comes_later(at, value):

@@ -195,3 +195,14 @@ def test_methods_refuse_a_bookkeeping_pool():
                  lambda: POOL.kv_evict(L, table[None], scores, lens, 4)):
         with pytest.raises(ValueError, match="bookkeeping-only"):
             call()
+
+
+def test_chunk_workspace_of_the_largest_call_serves_all():
+    size = lambda n, T, m, sc: rg.lora_kv_attend_chunk_workspace_size(POOL.handle, L, n, T, m, sc)
+    for sc in (False, True):
+        for m in (8, 255, 300, 512, 5000, 1 << 20):
+            got = [size(4, T, m, sc) for T in (1, 3, 64, 500, 4096, 70000)]
+            assert got == sorted(got)
+        got = [size(4, 64, m, sc) for m in (8, 255, 300, 512, 5000, 1 << 20)]
+        assert got == sorted(got)
+        assert size(4, 64, 5000, sc) <= size(9, 64, 5000, sc)
