@@ -12,9 +12,9 @@
 //
 // bfloat16, head_dim 128, 32 heads: the last 2048 of 16384 tokens on 8 K/V heads (515 GFLOP) 542 us, 950 TFLOP/s, where a
 // large matrix product reaches 1220; one prompt of 4096 tokens (137 GFLOP) 194 us; eight of 512 (17 GFLOP, 134 MB)
-// 48.7 us.  A long cache is bound by one wave's chain of LDS reads, products and softmax with two waves a SIMD; short prompts
+// 46.5 us.  A long cache is bound by one wave's chain of LDS reads, products and softmax with two waves a SIMD; short prompts
 // by what a workgroup does around its steps (8 us: its sequence, its page ids, the first K, the rows' way out;
-// 2 us a step).  float32, head_dim 64, 5 x 201 tokens behind 130: 30.4 us.
+// 2 us a step).  Few rows on a long cache are cut along it: 512 tokens behind 15872 192 us, 700 TFLOP/s.  float32, head_dim 64, 5 x 201 tokens behind 130: 30.4 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -37,7 +37,8 @@ struct KvChunk {
     float *piece_o;           // [ranges][T][n_heads][head_dim]: sums of a range, not divided
     float2 *piece_ml;         // [ranges][T][n_heads]: its maximum (base-2 logits) and sum
     float2 *stats;            // [n_heads][T]: maximum (base-2 logits) and 1 / sum of each row, for the scores; or null
-    float *part;              // [n_seq][n_kv][cap_ld]: a K/V head's share of the scores
+    int32_t hs;               // workgroups that share the query heads of a K/V head, for the scores; divides group
+    float *part;              // [n_seq][n_kv * hs][cap_ld]: their shares of the scores
     int64_t cap_ld;
 };
 
@@ -547,7 +548,7 @@ __global__ __launch_bounds__(256) void k_kv_chunk_join(KvArgs a, KvAttend at, Kv
 // A token's weights can be summed only when its rows' maxima and sums are known.  One workgroup takes 128
 // tokens of one K/V head, K in registers, and walks the query rows of the heads that share it; the logits are
 // multiplied again (half of the attention's products), and a lane sums its query rows' weights for each of its tokens.
-// 8 x 512 tokens, 32 heads of 128: 28.0 us (two blocks of rows at a time; one: 36; 64 tokens a workgroup and rows
+// 8 x 512 tokens, 32 heads of 128 (one to a K/V head): 28.0 us (two blocks of rows at a time; one: 36; 64 tokens a workgroup and rows
 // summed one exchange a token: 44), and 4.1 for the sum over the K/V heads.
 template <typename E, int HD>
 struct Scores {
@@ -567,7 +568,7 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
     constexpr bool BF = P::BF;
     __shared__ __align__(256) char smem[2 * P::BUF];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 31, hh = lane >> 5;
-    const int32_t b = blockIdx.z, kvh = blockIdx.x, t0 = blockIdx.y * P::TOK;
+    const int32_t b = blockIdx.z, kvh = blockIdx.x / ck.hs, heads = a.group / ck.hs, t0 = blockIdx.y * P::TOK;
     const SeqRows sq = seq_rows(a, b);
     if (t0 >= sq.n) return;
     const int32_t old = sq.n - sq.m, tw = t0 + wave * 32;
@@ -592,7 +593,7 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
     // steps: for each head of the group, NQ query rows at a time from the first that sees token t0.  (fh, fr): the
     // next step to fetch, off: its distance in bytes from the first one's rows, where this lane's pieces lie.
     const int32_t r0 = max(0, t0 - old) / NQ * NQ, per = sq.m > r0 ? (sq.m - r0 + NQ - 1) / NQ : 0;
-    const int32_t steps = per * a.group, h0 = kvh * a.group;
+    const int32_t steps = per * heads, h0 = blockIdx.x * heads;
     constexpr int PER = P::BUF / 4096;
     const int64_t row_bytes = at.ldq * (int64_t)sizeof(E);
     const char *piece[PER];
@@ -703,7 +704,7 @@ __global__ __launch_bounds__(256, (Scores<E, HD>::WAVES)) void k_kv_chunk_scores
         }
     v[0] += __shfl_xor(v[0], 1, 64);
     const int x = col >> 1, t = 8 * (x / 4) + 4 * hh + (x & 3);
-    if (!(col & 1) && tw + t < sq.n) ck.part[((int64_t)b * a.n_kv + kvh) * ck.cap_ld + tw + t] = (there >> t) & 1 ? v[0] : 0.f;
+    if (!(col & 1) && tw + t < sq.n) ck.part[((int64_t)b * gridDim.x + blockIdx.x) * ck.cap_ld + tw + t] = (there >> t) & 1 ? v[0] : 0.f;
 }
 
 __global__ __launch_bounds__(256) void k_kv_chunk_sum(KvArgs a, KvAttend at, KvChunk ck) {
@@ -711,9 +712,10 @@ __global__ __launch_bounds__(256) void k_kv_chunk_sum(KvArgs a, KvAttend at, KvC
     const SeqRows sq = seq_rows(a, b);
     if (t >= sq.n) return;
     float s = 0.f;
-    const float *p = ck.part + (int64_t)b * a.n_kv * ck.cap_ld + t;
+    const int32_t shares = a.n_kv * ck.hs;
+    const float *p = ck.part + (int64_t)b * shares * ck.cap_ld + t;
 #pragma unroll 8
-    for (int32_t h = 0; h < a.n_kv; ++h) s += p[(int64_t)h * ck.cap_ld];
+    for (int32_t h = 0; h < shares; ++h) s += p[(int64_t)h * ck.cap_ld];
     const int64_t i = (int64_t)b * at.score_ld + t;
     at.scores[i] = (at.prior ? at.prior[i] : 0.f) + s;
 }
@@ -729,7 +731,7 @@ hipError_t big_lds(const void *kernel, int bytes) {
 }
 
 struct ChunkPlan {
-    int32_t hpw, groups, tiles, ranges;
+    int32_t hpw, groups, tiles, ranges, hs;
     int64_t cap_ld;
     size_t off_part, off_o, off_ml, total;
 };
@@ -752,7 +754,14 @@ ChunkPlan chunk_plan(int n_heads, int n_kv, int hd, int32_t n_seq, int64_t T, in
     // at most 128 rows for each of the GPU's workgroups.
     const int64_t rows = most < 2 ? 0 : std::min<int64_t>(most * T * n_heads, 128 * slots);
     p.off_part = scores ? up256((size_t)T * n_heads * 8) : 0;
-    p.off_o = p.off_part + (scores ? up256((size_t)n_seq * n_kv * p.cap_ld * 4) : 0);
+    // Query heads of a K/V head go to more workgroups while the GPU has room, four a CU (the whole call, float32, 8 heads of
+    // 128 on one, 6 x 377 tokens: 321 us -> 104; bfloat16, 32 on 8, 2 x 1184: 139 -> 82).
+    const int64_t one = (int64_t)n_kv * n_seq * ((max_len + 127) / 128);
+    p.hs = (int32_t)std::max<int64_t>(1, std::min<int64_t>(group, 1024 / std::max<int64_t>(one, 1)));
+    while (group % p.hs) --p.hs;
+    const int64_t shares = std::min<int64_t>((int64_t)n_seq * n_heads * p.cap_ld,
+                                             std::max<int64_t>((int64_t)n_seq * n_kv * p.cap_ld, 1024 * 128));   // never less for a larger call
+    p.off_o = p.off_part + (scores ? up256((size_t)shares * 4) : 0);
     p.off_ml = p.off_o + up256((size_t)rows * hd * 4);
     p.total = p.off_ml + up256((size_t)rows * 8);
     return p;
@@ -766,6 +775,7 @@ hipError_t run(const KvArgs &a, const KvAttend &at, hipStream_t s) {
     KvChunk ck;
     ck.hpw = pl.hpw;
     ck.ranges = pl.ranges;
+    ck.hs = pl.hs;
     ck.cap_ld = pl.cap_ld;
     ck.stats = at.scores ? (float2 *)ws : nullptr;
     ck.part = (float *)(ws + pl.off_part);
@@ -799,7 +809,7 @@ hipError_t run(const KvArgs &a, const KvAttend &at, hipStream_t s) {
     if (e != hipSuccess) return e;
     if (at.scores) {
         constexpr int TOK = Scores<E, HD>::TOK;
-        hipLaunchKernelGGL((k_kv_chunk_scores<E, HD>), dim3(a.n_kv, (a.cap + TOK - 1) / TOK, a.n_seq), dim3(256), 0, s, a, at, ck);
+        hipLaunchKernelGGL((k_kv_chunk_scores<E, HD>), dim3(a.n_kv * ck.hs, (a.cap + TOK - 1) / TOK, a.n_seq), dim3(256), 0, s, a, at, ck);
         hipLaunchKernelGGL(k_kv_chunk_sum, dim3((a.cap + 255) / 256, a.n_seq), dim3(256), 0, s, a, at, ck);
     }
     return hipGetLastError();
