@@ -639,6 +639,35 @@ def test_captured_and_replayed(new):
         assert c.errors() == 0 and d.errors() == 0
 
 
+@pytest.mark.parametrize("geo,lens,new", [("gqa64", [2600, 900, 40], [20, 65, 3]), ("wide64", [300, 257], [300, 257])])
+def test_captured_chunks_of_other_lengths(geo, lens, new):
+    """Ranges and pairs: how the rows are shared out and how long the caches are is read at the replay."""
+    c = Case(geo, "bf16", lens, new, seed=11, extra_pages=0)
+    sc = torch.zeros((c.n, c.cap), device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c.run(scores=sc)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = c.run(scores=sc)
+    for turn in range(4):
+        m = [new[0] - 3 * turn] + [new[1] + 2 * turn if lens[1] > new[1] + 6 else new[1]] + new[2:]
+        c.d_start.copy_(c.dev(np.cumsum([0] + m)))
+        c.d_lens.copy_(c.dev([max(x, n - 200 * turn) if turn < 3 else (0 if b == 1 else n) for b, (n, x) in enumerate(zip(lens, m))]))
+        c.q.copy_(torch.randn_like(c.q.float()).to(c.dt))
+        out.fill_(7.25)
+        sc.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        eager_out, eager = torch.full_like(out, 7.25), torch.zeros_like(sc)
+        c.run(scores=eager, out=eager_out)
+        assert torch.equal(out, eager_out) and torch.equal(sc, eager), turn
+        c.errors()                                              # (the turn with an unused row that has new tokens)
+
+
 def test_streams_of_their_own():
     """Calls on two streams at once, given as stream objects and as a handle, share no workspace."""
     c = Case("gqa64", "bf16", [700, 33, 1500])
