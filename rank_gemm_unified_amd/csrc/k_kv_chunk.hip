@@ -12,9 +12,10 @@
 //
 // bfloat16, head_dim 128, 32 heads: the last 2048 of 16384 tokens on 8 K/V heads (515 GFLOP) 542 us, 950 TFLOP/s, where a
 // large matrix product reaches 1220; one prompt of 4096 tokens (137 GFLOP) 194 us; eight of 512 (17 GFLOP, 134 MB)
-// 46.5 us.  A long cache is bound by one wave's chain of LDS reads, products and softmax with two waves a SIMD; short prompts
-// by what a workgroup does around its steps (8 us: its sequence, its page ids, the first K, the rows' way out;
-// 2 us a step).  Few rows on a long cache are cut along it: 512 tokens behind 15872 192 us, 700 TFLOP/s.  float32, head_dim 64, 5 x 201 tokens behind 130: 30.4 us.
+// 46.5 us.  A long cache is bound by one wave's chain of LDS reads, products and softmax with two waves a SIMD; short
+// prompts by what a workgroup does around its steps (8 us: its sequence, its page ids, the first K, the rows' way out;
+// 2 us a step).  Few rows on a long cache are cut along it: 512 tokens behind 15872 192 us, 700 TFLOP/s.  float32,
+// head_dim 64, 5 x 201 tokens behind 130: 30.4 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -491,7 +492,8 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
     }
 }
 
-// Put the ranges of a row (blockIdx.x) together: a wave to a head.
+// Put the ranges of a row (blockIdx.x) together: a wave to a head.  out = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s; the
+// bytes are the ranges' sums once, at most 128 rows of each workgroup there was (32 MiB at head_dim 128), from the caches.
 constexpr int RANGES = 512;
 template <typename E, int HD>
 __global__ __launch_bounds__(256) void k_kv_chunk_join(KvArgs a, KvAttend at, KvChunk ck) {
