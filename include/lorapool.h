@@ -444,8 +444,8 @@ size_t lora_kv_attend_chunk_workspace_size(const lora_pool *pool, const lora_kv_
  * reach no row before it, whatever they hold (infinities and NaN included).
  *   q, out       device [T][n_heads * head_dim]; sequence b's rows as q_start says
  *   scores       as lora_kv_attend's, summed over the sequence's new tokens too
- * bfloat16 pools: the weights are rounded to bfloat16 for the product with V (scores take them
- * unrounded).  The rest as lora_kv_attend.  Errors: LORA_EINVAL, LORA_EHIP.
+ * bfloat16 pools: the weights are rounded to bfloat16 for the product with V, off by at most 2^-8 of
+ * themselves, the largest not at all (scores take them unrounded).  The rest as lora_kv_attend.  Errors: LORA_EINVAL, LORA_EHIP.
  */
 int lora_kv_attend_chunk(lora_pool *pool, const lora_kv_layout_t *layout, const void *q, int64_t ldq,
                          const int32_t *table, int32_t max_pages, const int32_t *q_start,

@@ -377,9 +377,11 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
 #pragma unroll
                 for (int i = 0; i < 16; ++i) mt = fmaxf(mt, S[nb][i]);
             mt = fmaxf(mt, other_half(mt)) * sc;
-            // The running maximum moves only when a logit passes it by 8: until then weights up to 2^8 do no
-            // harm, and the accumulators need no rescaling.
-            if (__any(mt > m + 8.f)) {
+            // bfloat16: the running maximum follows at once, so that a row's largest weight is one and its rounding, the
+            // one that counts most, is none (weights of up to 2^8 instead would double the variance of the weights' part of
+            // the error: 0.0023 against 0.0020 from float64, behind 14336 tokens).  It costs 3% there, 1.4% at 8 x 512.
+            // float32 rounds no weights: there the maximum moves only when a logit passes it by 8, to rescale less often.
+            if (__any(mt > m + (BF ? 0.f : 8.f))) {
                 const float mn = fmaxf(m, mt), ms = mn == -INFINITY ? 0.f : mn;
                 // (before a row's first weight the accumulators hold zeros, or infinities that the second pass added)
                 const float c = careful.value && m == -INFINITY ? 1.f : exp2_hw(m - ms);

@@ -1,0 +1,41 @@
+"""Rounding, zero weights and values that are not finite in the KV-cache attention calls, on the device."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_kv import Case, _gpu  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("geo,n,at", [
+    ("gqa64", 200, 100), ("mqa128", 200, 64), ("dim256", 300, 70), ("group3", 200, 130),
+    ("gqa64", 1100, 100), ("gqa64", 1100, 700), ("mqa128", 900, 100),       # in ranges
+    ("wide64", 200, 100), ("wide64_kv64", 260, 64),                         # in pairs
+])
+def test_a_chunks_largest_weight_is_not_rounded(geo, n, at):
+    """A row's largest weight is one, whatever smaller maximum the tokens before it had.  Token 0 has logit 0 and
+    values 0, token `at` logit c / 8 and values 1, the others no weight to speak of: out = 1 / (1 + exp(-c / 8)).
+    Only the output's own rounding is left, half a step of 2^-8 in [1/2, 1) and of 2^-7 at 1, and the float32 sums
+    (1e-5 is 80 of their steps)."""
+    rows = 44 if geo.startswith(("gqa", "mqa", "dim", "group")) else 128
+    c = Case(geo, "bf16", [n] * (1 if rows == 44 else 4), [rows] * (1 if rows == 44 else 4))
+    tpp, dim, w = c.layout.tokens_per_page, c.layout.head_dim, c.layout.n_kv_heads * c.layout.head_dim
+    c.pool.pages.zero_()
+    held = c.pool.pages[:, : tpp * w].view(-1, tpp, c.layout.n_kv_heads, dim)
+    for b in range(c.n):
+        ids = [torch.as_tensor(c.table[b, r, np.arange(n) // tpp].astype(np.int64), device="cuda") for r in range(2)]
+        slot = torch.arange(n, device="cuda") % tpp
+        held[ids[0], slot, :, 0] = -1000.0
+        held[ids[0][0], slot[0], :, 0] = 0.0
+        held[ids[0][at], slot[at], :, 0] = 1.0
+        held[ids[1][at], slot[at]] = 1.0
+    step = torch.arange(rows, device="cuda") % 44 + 1                       # logits of 1/8 to 44/8
+    c.q.zero_()
+    c.q.view(c.n, rows, -1, dim)[..., 0] = step[None, :, None].to(c.dt)
+    out = c.run(scale=0.125)
+    assert c.errors() == 0
+    want = 1 / (1 + torch.exp(-step.double() / 8))
+    want[torch.arange(n - rows, n, device="cuda") < at] = 0                 # rows before that token
+    off = (out.view(c.n, rows, -1).double() - want[None, :, None]).abs()
+    assert (off <= 2.0 ** -9 + 1e-5).all(), (off.max().item(), off.amax((0, 2)).topk(3))
