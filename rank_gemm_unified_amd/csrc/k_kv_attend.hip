@@ -274,7 +274,8 @@ __global__ __launch_bounds__(LOCAL ? 256 * split_waves(HD) : 256, split_waves(HD
         if (!mine) return;
         const int64_t pl = ((int64_t)range * 2 + slot) * a.n_heads + head;
         if (g == 0) (whole ? sp.done_ml[(int64_t)p.b * a.n_heads + head] : sp.part_ml[pl]) = make_float2(m, L);
-        const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+        const float inv = whole ? 1.f / L : 1.f;
+        const bool none = whole && L == 0.f;               // no weight: zero, also where a value is not finite
         float *po = sp.part_o + pl * HD;
         E *o = (E *)at.out + (int64_t)p.b * at.ldo + (int64_t)head * HD;
         constexpr int W = BF && HD >= 128 ? 8 : 4;         // consecutive dims of one row of the accumulators
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(LOCAL ? 256 * split_waves(HD) : 256, split_waves(HD
                 const int d = 16 * W * c + W * (4 * g + r);
                 float v[W];
 #pragma unroll
-                for (int i = 0; i < W; ++i) v[i] = acc[W * c + i][r] * inv;
+                for (int i = 0; i < W; ++i) v[i] = none ? 0.f : acc[W * c + i][r] * inv;
                 if (!whole) {
 #pragma unroll
                     for (int i = 0; i < W; i += 4) *(float4 *)(po + d + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
@@ -556,9 +557,10 @@ __global__ __launch_bounds__(256) void k_kv_join(KvArgs a, KvAttend at, KvSplit 
         if (sp.jh == 4 && p.r1 - p.r0 < 8) {                // few pieces: a wave to a head
             if (h0 + wave < a.n_heads) {
                 gather(h0 + wave, p.r0, 1);
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float inv = 1.f / l;
 #pragma unroll
-                for (int i = 0; i < PER; ++i) from_f32(out + (int64_t)(h0 + wave) * HD + 64 * i + lane, acc[i] * inv);
+                for (int i = 0; i < PER; ++i)
+                    from_f32(out + (int64_t)(h0 + wave) * HD + 64 * i + lane, l == 0.f ? 0.f : acc[i] * inv);
             }
             return;
         }
@@ -575,12 +577,12 @@ __global__ __launch_bounds__(256) void k_kv_join(KvArgs a, KvAttend at, KvSplit 
                 w[i] = exp2_hw(sh_m[i] - Ms);
                 L += sh_l[i] * w[i];
             }
-            const float inv = L == 0.f ? 0.f : 1.f / L;
+            const float inv = 1.f / L;
             for (int d = tid; d < HD; d += 256) {
                 float v = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v += sh_o[i][d] * w[i];
-                from_f32(out + (int64_t)h * HD + d, v * inv);
+                from_f32(out + (int64_t)h * HD + d, L == 0.f ? 0.f : v * inv);
             }
             __syncthreads();
         }

@@ -39,3 +39,43 @@ def test_a_chunks_largest_weight_is_not_rounded(geo, n, at):
     want[torch.arange(n - rows, n, device="cuda") < at] = 0                 # rows before that token
     off = (out.view(c.n, rows, -1).double() - want[None, :, None]).abs()
     assert (off <= 2.0 ** -9 + 1e-5).all(), (off.max().item(), off.amax((0, 2)).topk(3))
+
+
+def _all_minus_infinity(c, b):
+    """Sequence b: every product with a query is -inf, and among the values are infinities and NaN."""
+    tpp, dim = c.layout.tokens_per_page, c.layout.head_dim
+    held = c.pool.pages[:, : tpp * c.layout.n_kv_heads * dim].view(-1, tpp, c.layout.n_kv_heads, dim)
+    n = c.lens[b]
+    ids = [torch.as_tensor(c.table[b, r, np.arange(n) // tpp].astype(np.int64), device="cuda") for r in range(2)]
+    slot = torch.arange(n, device="cuda") % tpp
+    held[ids[0], slot, :, 0] = -float("inf")
+    c.q.view(c.T, -1, dim)[..., 0] = 1.0
+    for at, x in ((0, float("inf")), (n // 2, -float("inf")), (n - 1, float("nan"))):
+        held[ids[1][at], slot[at]] = x
+
+
+def _zero_rows(geo, dtype, lens, new, scores):
+    c = Case(geo, dtype, lens, new, seed=21)
+    _all_minus_infinity(c, 1)
+    prior = torch.rand((c.n, c.cap), device="cuda") if scores else None
+    sc = torch.full((c.n, c.cap), -3.0, device="cuda") if scores else None
+    out = c.run(scores=sc, prior=prior)
+    rows = slice(1, 2) if new is None else slice(new[0], new[0] + new[1])
+    assert (out[rows] == 0).all()
+    assert torch.isfinite(out).all() and (out[: rows.start] != 0).any() and (out[rows.stop:] != 0).any()
+    if scores:
+        n = c.lens[1]
+        assert torch.equal(sc[1, :n], prior[1, :n]) and (sc[1, n:] == -3.0).all()
+    assert c.errors() == 0
+
+
+@pytest.mark.parametrize("scores", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("geo,lens", [
+    ("gqa64", [40, 33, 50]), ("mqa128", [90, 64, 31]), ("dim256", [40, 65, 50]),               # one launch without scores
+    ("mha128", [1500, 1, 1500]), ("mqa128", [70] * 300), ("group20", [700, 64, 900]),           # whole in one range, and pieces
+    ("gqa64", [2000, 1500, 3000]), ("dim256", [2000, 1500, 300]), ("gqa64", [900] * 60),        # many pieces, and few
+])
+def test_a_token_no_weight_reaches_is_zero(geo, lens, dtype, scores):
+    """Where every product is -inf the output is zero, whatever the values hold."""
+    _zero_rows(geo, dtype, lens, None, scores)
