@@ -460,6 +460,11 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
         return;
     }
     const float L = l + other_half(l), inv = L == 0.f ? 0.f : 1.f / L;
+    if (L == 0.f)                                           // no weight: zero, also where a value is not finite
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
     if (ck.stats && row_ok && hh == 0) ck.stats[(int64_t)head * a.T + row] = make_float2(m == -INFINITY ? 0.f : m, inv);
     if constexpr (BF) {
         // rows through LDS, so that a row leaves in one piece
@@ -544,7 +549,7 @@ __global__ __launch_bounds__(256) void k_kv_chunk_join(KvArgs a, KvAttend at, Kv
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-    for (int i = 0; i < W; ++i) from_f32(out + i, v[i] * inv);
+    for (int i = 0; i < W; ++i) from_f32(out + i, L == 0.f ? 0.f : v[i] * inv);
     if (ck.stats && lane == 0) ck.stats[(int64_t)head * a.T + t] = make_float2(Ms, inv);
 }
 

@@ -79,3 +79,14 @@ def _zero_rows(geo, dtype, lens, new, scores):
 def test_a_token_no_weight_reaches_is_zero(geo, lens, dtype, scores):
     """Where every product is -inf the output is zero, whatever the values hold."""
     _zero_rows(geo, dtype, lens, None, scores)
+
+
+@pytest.mark.parametrize("scores", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("geo,lens,new", [
+    ("gqa64", [90, 80, 50], [90, 80, 50]), ("mqa128", [200, 150, 70], [20, 33, 70]), ("dim256", [60, 130, 40], [3, 130, 40]),
+    ("gqa64", [900, 1500, 300], [3, 20, 9]), ("dim256", [900, 700, 300], [3, 20, 9]),           # in ranges
+    ("wide64", [300, 257, 200], [300, 257, 200]),                                               # in pairs
+])
+def test_a_chunk_no_weight_reaches_is_zero(geo, lens, new, dtype, scores):
+    _zero_rows(geo, dtype, lens, new, scores)
