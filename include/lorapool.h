@@ -423,8 +423,9 @@ size_t lora_kv_attend_workspace_size(const lora_pool *pool, const lora_kv_layout
  *                overlap it otherwise
  *   workspace    as lora_project's
  * The out element is rounded once from float32; bfloat16 pools: the weights enter the product with V
- * as the sum of two bfloat16 numbers, off by at most 2^-15 of themselves.  Where every weight is zero (no token, or each
- * product is -inf) the output is zero.  Results do not change from call to call of the same shape.
+ * as the sum of two bfloat16 numbers, off by at most 2^-15 of themselves, or by 2^-126 of the row's largest where that
+ * is more; a weight of zero stays zero.  Where every weight is zero (no token, or each product is -inf) the output is
+ * zero.  Results do not change from call to call of the same shape.
  * Errors: LORA_EINVAL, LORA_EHIP.
  */
 int lora_kv_attend(lora_pool *pool, const lora_kv_layout_t *layout, const void *q, int64_t ldq,

@@ -403,15 +403,17 @@ __global__ __launch_bounds__(LOCAL ? 256 * split_waves(HD) : 256, split_waves(HD
 #pragma unroll
             for (int q = 0; q < TT / 32; ++q) {
                 // weights as the sum of two bfloat16 numbers, so that they are off by at most 2^-15: the
-                // first their leading bits, cut off, the second the rest, rounded and never zero -- both have
-                // the weight's sign, so that an infinite value times a weight stays that infinity
+                // first their leading bits, cut off, the second the rest, rounded.  The second is raised to 2^-126 where
+                // the rest is less, unless the weight itself is: an infinite value times a weight stays that infinity,
+                // and a weight of zero stays zero.  (Below 2^-111 a weight is off by up to 2^-126, not by 2^-15 of itself.)
                 u32x4_t hi, lo;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const float a0 = S[2 * q + x / 2][2 * (x & 1)], a1 = S[2 * q + x / 2][2 * (x & 1) + 1];
                     const uint32_t h0 = __float_as_uint(a0) & 0xffff0000u, h1 = __float_as_uint(a1) & 0xffff0000u;
                     hi[x] = h0 >> 16 | h1;
-                    lo[x] = pack2(fmaxf(a0 - __uint_as_float(h0), 0x1p-100f), fmaxf(a1 - __uint_as_float(h1), 0x1p-100f));
+                    const float f0 = __uint_as_float(h0), f1 = __uint_as_float(h1);
+                    lo[x] = pack2(__builtin_amdgcn_fmed3f(a0 - f0, f0, 0x1p-126f), __builtin_amdgcn_fmed3f(a1 - f1, f1, 0x1p-126f));
                 }
                 constexpr int W = HD == 64 ? 4 : 8;
 #pragma unroll

@@ -90,3 +90,51 @@ def test_a_token_no_weight_reaches_is_zero(geo, lens, dtype, scores):
 ])
 def test_a_chunk_no_weight_reaches_is_zero(geo, lens, new, dtype, scores):
     _zero_rows(geo, dtype, lens, new, scores)
+
+
+@pytest.mark.parametrize("scores", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("geo,lens", [("gqa64", [40, 133]), ("mqa128", [90, 64]), ("dim256", [40, 65]), ("gqa64", [2000, 1500])])
+def test_a_weight_of_zero_adds_nothing(geo, lens, dtype, scores):
+    """The largest finite values meet weights that are zero (a product of -inf, or one 200 below the others) and one of
+    exp(-80): what they add is their weight times them.  Token 1: -inf, token 2: -200, token 3: exp(-80), the others 0."""
+    c = Case(geo, dtype, lens, seed=22)
+    tpp, dim = c.layout.tokens_per_page, c.layout.head_dim
+    held = c.pool.pages[:, : tpp * c.layout.n_kv_heads * dim].view(-1, tpp, c.layout.n_kv_heads, dim)
+    big = 2.0 ** 127
+    c.q.zero_()
+    c.q.view(c.T, -1, dim)[..., 0] = 1.0
+    for b, n in enumerate(lens):
+        ids = [torch.as_tensor(c.table[b, r, np.arange(n) // tpp].astype(np.int64), device="cuda") for r in range(2)]
+        slot = torch.arange(n, device="cuda") % tpp
+        held[ids[0], slot] = 0.0
+        held[ids[1], slot] = 1.0
+        for t, x in ((1, -float("inf")), (2, -200.0), (3, -80.0)):
+            held[ids[0][t], slot[t], :, 0] = x
+            held[ids[1][t], slot[t], :, 7 + t] = big
+    sc = torch.zeros((c.n, c.cap), device="cuda") if scores else None
+    out = c.run(scale=1.0, scores=sc).view(c.n, -1, dim).double()
+    for b, n in enumerate(lens):
+        want = torch.full((dim,), (n - 3.0) / (n - 3.0), dtype=torch.float64, device="cuda")
+        want[10] += np.exp(-80.0) * big / (n - 3.0)
+        # half a step of the output (2^-8), the weight's two parts (2^-15), and exp(-80) from a logit that float32 holds
+        # to half a step of 115 in base 2 (2^-18 * ln 2)
+        assert ((out[b] - want).abs() <= want * (2.0 ** -8 + 2.0 ** -14 + 2.0 ** -17)).all(), (b, out[b, 0, 7:12], want[7:12])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("geo,lens", [("gqa64", [40, 133]), ("mqa128", [90, 64]), ("dim256", [40, 65]), ("gqa64", [2000, 1500])])
+def test_a_weight_of_zero_times_infinity_is_not_a_number(geo, lens, dtype):
+    c = Case(geo, dtype, lens, seed=23)
+    tpp, dim = c.layout.tokens_per_page, c.layout.head_dim
+    held = c.pool.pages[:, : tpp * c.layout.n_kv_heads * dim].view(-1, tpp, c.layout.n_kv_heads, dim)
+    c.q.view(c.T, -1, dim)[..., 0] = 1.0
+    for b in range(c.n):
+        k, v = (int(c.table[b, r, 17 // tpp]) for r in range(2))
+        held[k, 17 % tpp, :, 0] = -float("inf")
+        held[v, 17 % tpp, :, 5] = float("inf")
+    for sc in (None, torch.zeros((c.n, c.cap), device="cuda")):
+        out = c.run(scores=sc).view(c.n, -1, dim)
+        assert torch.isnan(out[..., 5]).all()
+        out[..., 5] = 0
+        assert torch.isfinite(out).all()
