@@ -403,7 +403,8 @@ int lora_kv_write(lora_pool *pool, const lora_kv_layout_t *layout, const void *k
                   const int32_t *q_start, const int32_t *lens, int32_t n_seq, int64_t T, void *stream);
 
 /* Bytes of device workspace (256-byte aligned) lora_kv_attend needs; 0 if an argument is out of
- * range.  with_scores: whether the call collects scores. */
+ * range, or if neither this call nor a smaller one uses any.  with_scores: whether the call collects
+ * scores.  Never less for more sequences or tokens, or with scores: a workspace of the largest call serves them all. */
 size_t lora_kv_attend_workspace_size(const lora_pool *pool, const lora_kv_layout_t *layout,
                                      int32_t n_seq, int64_t max_len, int32_t with_scores);
 

@@ -668,7 +668,8 @@ struct SplitPlan {
     int32_t R, ncb, hu, cols;
     int64_t tiles;
     bool local;
-    size_t off_ml, off_done, off_logits, total;
+    size_t off_ml, off_done, off_logits;
+    size_t need, ask;         // bytes of workspace that the call uses, and that it asks for
 };
 SplitPlan split_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int64_t max_len, bool scores) {
     SplitPlan s;
@@ -682,14 +683,19 @@ SplitPlan split_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, in
     // 14.7 (13.8); eight of 1024 23.6 (29.6).  Behind that the ranges are as fast, and lengths that differ leave
     // none of their waves idle.  Scores need every head's sums, so they keep the second launch.
     const int64_t wgs = (int64_t)n_seq * s.hu;
-    s.local = !scores && wgs <= 256 && (max_len + tt - 1) / tt <= (wgs < 64 ? 3 : 4) * 4 * split_waves(hd);
+    auto few = [&](int64_t w) { return (max_len + tt - 1) / tt <= (w < 64 ? 3 : 4) * 4 * split_waves(hd); };
+    s.local = !scores && wgs <= 256 && few(wgs);
     // as many waves as the chip holds; no more ranges than tiles
     s.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, 1024 * split_waves(hd) / s.hu));
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     s.off_ml = up((size_t)s.R * 2 * n_heads * hd * 4);
     s.off_done = s.off_ml + up((size_t)s.R * 2 * n_heads * 8);
     s.off_logits = s.off_done + up((size_t)n_seq * n_heads * 8);
-    s.total = s.local ? 0 : s.off_logits + (scores ? up((size_t)s.hu * tiles * s.cols * tt * 4) : 0);
+    const size_t ranges = s.off_logits + (scores ? up((size_t)s.hu * tiles * s.cols * tt * 4) : 0);
+    s.need = s.local ? 0 : ranges;
+    // What serves the largest call has to serve them all, and of a length at which 64 workgroups take one launch fewer may
+    // take two: nothing is asked for only where one sequence alone would take one launch too.
+    s.ask = s.local && few(s.hu) ? 0 : ranges;
     return s;
 }
 
@@ -731,7 +737,11 @@ hipError_t by_dim(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s)
 }  // namespace
 
 size_t kv_attend_ws_bytes(int dtype, const lora_kv_layout_t &l, int32_t n_seq, int64_t max_len, bool scores) {
-    return split_plan(dtype, l.n_heads, l.n_kv_heads, l.head_dim, n_seq, max_len, scores).total;
+    return split_plan(dtype, l.n_heads, l.n_kv_heads, l.head_dim, n_seq, max_len, scores).ask;
+}
+
+size_t kv_attend_ws_need(int dtype, const lora_kv_layout_t &l, int32_t n_seq, int64_t max_len, bool scores) {
+    return split_plan(dtype, l.n_heads, l.n_kv_heads, l.head_dim, n_seq, max_len, scores).need;
 }
 
 hipError_t launch_kv_attend(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s) {

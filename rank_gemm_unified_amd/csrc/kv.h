@@ -49,7 +49,9 @@ struct KvEvict {
     int *err;
 };
 
+// Workspace to have (never less for a larger call), and what the call itself uses.
 size_t kv_attend_ws_bytes(int dtype, const lora_kv_layout_t &l, int32_t n_seq, int64_t max_len, bool scores);
+size_t kv_attend_ws_need(int dtype, const lora_kv_layout_t &l, int32_t n_seq, int64_t max_len, bool scores);
 size_t kv_chunk_ws_bytes(int dtype, const lora_kv_layout_t &l, int32_t n_seq, int64_t T, int64_t max_len, bool scores);
 
 hipError_t launch_kv_write(int dtype, const KvArgs &a, const void *k, int64_t ldk, const void *v, int64_t ldv,

@@ -121,7 +121,7 @@ int attend(lora_pool *p, const char *fn, const lora_kv_layout_t *l, const void *
             return set_error(LORA_EINVAL, "%s: prior overlaps scores without being them", fn);
     }
     const size_t need = chunk ? kv_chunk_ws_bytes(p->dtype, *l, n_seq, T, max_len, scores != nullptr)
-                              : kv_attend_ws_bytes(p->dtype, *l, n_seq, max_len, scores != nullptr);
+                              : kv_attend_ws_need(p->dtype, *l, n_seq, max_len, scores != nullptr);
     if (need > 0 && (!ws || !aligned(ws, 256) || ws_bytes < need))
         return set_error(LORA_EINVAL, "%s: workspace %zu bytes at %p: %zu needed, 256-byte aligned", fn, ws_bytes, ws, need);
     if (p->bookkeeping_only) return set_error(LORA_EINVAL, "%s: bookkeeping-only pool", fn);
