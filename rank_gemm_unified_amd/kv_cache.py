@@ -22,7 +22,13 @@ class KvCache:
     that were not named are left alone (their output is zero).  Otherwise it is a chunk: the rows of the
     named requests one behind the other, in cache row order (`rows` of the request before that of a later
     one).  The device tensors (table, lens, step_lens, q_start, scores) are the same ones throughout, so a captured decode step
-    may be replayed after each append()."""
+    may be replayed after each append().
+
+    Streams: write() and attend() run on the stream they are given, or the current one.  append(), evict() and finish()
+    change what those read: they put the current stream behind everything queued on the streams of the write() and
+    attend() calls before, and return when their changes are in place, so the calls of the next step may run on any
+    stream.  (A stream that was given has to live until then.)  Calls of one step on several streams are the caller's
+    to order, and so is a graph replayed on another stream than the current one: the cache does not see it."""
 
     def __init__(self, pool, layers, layout, max_seqs, max_tokens, scores=False):
         import rank_gemm_unified_amd as rg
@@ -45,6 +51,32 @@ class KvCache:
         self.rows = {}                                    # request -> row
         self.length = [0] * max_seqs
         self._chunk = False
+        self._used = {}                                   # handle -> stream that calls of this step ran on
+
+    def _runs_on(self, stream):
+        """Note the stream of a call: what changes the cache next comes behind it."""
+        handle = self.pool._where(stream)[0]
+        if handle not in self._used:
+            dev = self.table.device
+            if stream is None:
+                stream = torch.cuda.current_stream(dev)
+            elif isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+            self._used[handle] = stream
+
+    def _behind_the_step(self):
+        """Put the current stream behind the calls since the last change; returns it."""
+        now = torch.cuda.current_stream(self.table.device)
+        for handle, stream in self._used.items():
+            if handle != now.cuda_stream:
+                now.wait_stream(stream)
+        self._used = {now.cuda_stream: now}
+        return now
+
+    def _in_place(self, now):
+        """Wait until the changes, and so the calls they came behind, are done."""
+        now.synchronize()
+        self._used = {}
 
     def _pages(self, tokens):
         return -(-tokens // self.tpp)
@@ -80,6 +112,7 @@ class KvCache:
                     self._rg.lora_pool_free_kv(self.pool.handle, rid)
             raise
         self.rows = rows
+        now = self._behind_the_step()
         if entries:
             dev = self.table.device
             at = torch.tensor([(r, e) for r, e, _ in entries], device=dev)
@@ -96,15 +129,18 @@ class KvCache:
         self.lens.copy_(torch.tensor(self.length, dtype=torch.int32))
         self.step_lens.copy_(torch.tensor([l if n else 0 for l, n in zip(self.length, new)], dtype=torch.int32))
         self.q_start.copy_(torch.tensor(starts, dtype=torch.int32))
+        self._in_place(now)
 
     def write(self, layer, k, v, stream=None):
         """The step's K and V rows into layer `layer`'s pages (Pool.kv_write)."""
+        self._runs_on(stream)
         self.pool.kv_write(self.layout, k, v, self.table[layer], self.step_lens, self.q_start if self._chunk else None,
                            stream=stream)
 
     def attend(self, layer, q, scale=None, max_len=None, out=None, stream=None):
         """The step's attention in layer `layer` (Pool.kv_attend or kv_attend_chunk), its weights added to the
         layer's scores if the cache keeps them.  max_len None: the longest a request may become."""
+        self._runs_on(stream)
         sc = None if self.scores is None else self.scores[layer]
         args = dict(scale=scale, max_len=self.max_tokens if max_len is None else max_len, out=out, scores=sc, prior=sc,
                     stream=stream)
@@ -113,10 +149,11 @@ class KvCache:
         return self.pool.kv_attend(self.layout, q, self.table[layer], self.step_lens, **args)
 
     def evict(self, budget, keep_first=0, keep_last=0):
-        """Thin every request out to about `budget` tokens (Pool.kv_evict) and give its pages back to the pool.
-        Waits for the device.  Returns {request: tokens that left}."""
+        """Thin every request out to about `budget` tokens (Pool.kv_evict) and give its pages back to the pool,
+        when the step's calls are done with them.  Returns {request: tokens that left}."""
         if self.scores is None:
             raise ValueError("this cache keeps no scores")
+        now = self._behind_the_step()
         *_, lens, dropped, n = self.pool.kv_evict(self.layout, self.table, self.scores, self.lens, budget, keep_first,
                                                   keep_last, in_place=True)
         self.lens.copy_(lens)
@@ -124,6 +161,7 @@ class KvCache:
         n, gone = n.tolist(), {}
         most = max(n, default=0)
         ids = dropped[..., :most].cpu() if most else None
+        self._in_place(now)
         for rid, row in self.rows.items():
             if n[row]:
                 self._rg.lora_pool_drop_kv(self.pool.handle, rid, ids[:, row, :, : n[row]].reshape(-1).numpy())
@@ -136,8 +174,10 @@ class KvCache:
         row = self.rows.pop(rid)
         self._rg.lora_pool_free_kv(self.pool.handle, rid)
         self.length[row] = 0
+        now = self._behind_the_step()
         self.table[:, row] = -1
         self.lens[row] = 0
         self.step_lens[row] = 0
         if self.scores is not None:
             self.scores[:, row] = 0
+        self._in_place(now)

@@ -1,0 +1,100 @@
+"""KvCache with its calls on a stream of their own, against the same steps one after the other."""
+import pytest
+import torch
+
+import rank_gemm_unified_amd as rg
+from test_gpu_kv import _gpu  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+NH, NKV, DIM, H, LAYERS, ROWS, MOST = 8, 2, 64, 256, 2, 3, 700
+
+
+class Twin:
+    """Two caches over pools of the same content that make the same steps: `serial` on the current stream, waited for
+    after each; `aside` on a stream of its own that is kept busy, not waited for."""
+
+    def __init__(self, dtype=torch.bfloat16):
+        self.layout, self.dt = rg.lora_kv_layout_t(NH, NKV, DIM, 2), dtype
+        code = rg.LORA_BF16 if dtype is torch.bfloat16 else rg.LORA_F32
+        self.pools = [rg.Pool(2 * LAYERS * ROWS * 360, H, code, max_rank=1) for _ in range(2)]
+        for p in self.pools:
+            p.pages.zero_()
+        self.caches = [rg.KvCache(p, LAYERS, self.layout, ROWS, MOST, scores=True) for p in self.pools]
+        self.stream = torch.cuda.Stream()
+        self.g = torch.Generator(device="cuda").manual_seed(31)
+        self.busy = torch.randn((4096, 4096), device="cuda").bfloat16()
+        self.outs = [[], []]
+        torch.cuda.synchronize()
+
+    def step(self, counts):
+        T = sum(counts.values()) if max(counts.values()) > 1 else ROWS
+        rows = [[torch.empty((T, w * DIM), dtype=self.dt, device="cuda").normal_(generator=self.g) for w in (NKV, NKV, NH)]
+                for _ in range(LAYERS)]
+        serial, aside = self.caches
+        serial.append(counts)
+        for layer, (k, v, q) in enumerate(rows):
+            serial.write(layer, k, v)
+            self.outs[0].append(serial.attend(layer, q))
+        torch.cuda.synchronize()
+        aside.append(counts)
+        with torch.cuda.stream(self.stream):                 # a few milliseconds of work before the step's
+            for _ in range(24):
+                torch.mm(self.busy, self.busy)
+        for layer, (k, v, q) in enumerate(rows):
+            aside.write(layer, k, v, stream=self.stream)
+            self.outs[1].append(aside.attend(layer, q, stream=self.stream if layer else self.stream.cuda_stream))
+        self.rows = rows                                     # read until the next step at least
+
+    def same(self):
+        torch.cuda.synchronize()
+        a, b = self.caches
+        assert a.length == b.length and a.rows == b.rows
+        for name in ("table", "lens", "step_lens", "q_start", "scores"):
+            x, y = getattr(a, name), getattr(b, name)
+            assert torch.equal(x, y), name
+        assert len(self.outs[0]) == len(self.outs[1])
+        for i, (x, y) in enumerate(zip(*self.outs)):
+            assert torch.equal(x, y), i
+        assert torch.equal(self.pools[0].pages, self.pools[1].pages)
+        assert rg.lora_pool_free_list(self.pools[0].handle) == rg.lora_pool_free_list(self.pools[1].handle)
+        for p in self.pools:
+            assert rg.lora_check_device_errors(p.handle, check=False) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_steps_on_another_stream(dtype):
+    """append, evict and finish come behind the step before them, wherever it runs."""
+    t = Twin(dtype)
+    t.step({1: 300, 2: 41})
+    t.step({1: 1, 2: 1})
+    t.step({1: 1, 3: 1})                                      # row 1 pauses: its lengths of the step before change
+    gone = [c.evict(100, 4, 20) for c in t.caches]
+    assert gone[0] == gone[1] and gone[0]
+    t.same()
+    t.step({2: 1, 3: 1})
+    for c in t.caches:
+        c.finish(2)
+    t.step({3: 200, 4: 50})
+    t.step({1: 1, 3: 1, 4: 1})
+    for rid in (1, 3, 4):
+        for c in t.caches:
+            c.finish(rid)
+    t.same()
+
+
+def test_steps_under_another_current_stream():
+    """The streams that were current at the calls count."""
+    t = Twin()
+    t.step({1: 100, 2: 33})
+    other = torch.cuda.Stream()
+    with torch.cuda.stream(other):
+        for c in t.caches:
+            assert c.evict(50, 2, 2)
+    t.same()
+    with torch.cuda.stream(other):
+        t.step({1: 1, 2: 1})
+    for c in t.caches:
+        c.finish(1)
+    t.step({2: 1, 5: 1})
+    t.same()
