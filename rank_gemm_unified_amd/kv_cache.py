@@ -170,9 +170,9 @@ class KvCache:
         return gone
 
     def finish(self, rid):
-        """Request done: its pages go back to the pool and its row is free."""
+        """Request done: its row is free, and its pages go back to the pool, once the step's calls, which may read them,
+        are done: whatever takes the pages next may write them on any stream."""
         row = self.rows.pop(rid)
-        self._rg.lora_pool_free_kv(self.pool.handle, rid)
         self.length[row] = 0
         now = self._behind_the_step()
         self.table[:, row] = -1
@@ -181,3 +181,4 @@ class KvCache:
         if self.scores is not None:
             self.scores[:, row] = 0
         self._in_place(now)
+        self._rg.lora_pool_free_kv(self.pool.handle, rid)

@@ -46,16 +46,19 @@ class Twin:
             self.outs[1].append(aside.attend(layer, q, stream=self.stream if layer else self.stream.cuda_stream))
         self.rows = rows                                     # read until the next step at least
 
-    def same(self):
+    def same_outputs(self):
         torch.cuda.synchronize()
+        assert len(self.outs[0]) == len(self.outs[1])
+        for i, (x, y) in enumerate(zip(*self.outs)):
+            assert torch.equal(x, y), i
+
+    def same(self):
+        self.same_outputs()
         a, b = self.caches
         assert a.length == b.length and a.rows == b.rows
         for name in ("table", "lens", "step_lens", "q_start", "scores"):
             x, y = getattr(a, name), getattr(b, name)
             assert torch.equal(x, y), name
-        assert len(self.outs[0]) == len(self.outs[1])
-        for i, (x, y) in enumerate(zip(*self.outs)):
-            assert torch.equal(x, y), i
         assert torch.equal(self.pools[0].pages, self.pools[1].pages)
         assert rg.lora_pool_free_list(self.pools[0].handle) == rg.lora_pool_free_list(self.pools[1].handle)
         for p in self.pools:
@@ -98,3 +101,18 @@ def test_steps_under_another_current_stream():
         c.finish(1)
     t.step({2: 1, 5: 1})
     t.same()
+
+
+def test_pages_of_a_finished_request_may_be_written_at_once():
+    """What takes them next, an adapter loaded on a stream of its own, say, changes nothing that the step reads."""
+    t = Twin()
+    t.step({1: 400, 2: 300})
+    for c, p in zip(t.caches, t.pools):
+        pages = [rg.lora_pool_kv_pages(p.handle, r) for r in (1, 2)]
+        c.finish(1)
+        c.finish(2)
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            p.pages[torch.as_tensor(sum(pages, [])).to("cuda", non_blocking=False)] = float("nan")
+        s.synchronize()
+    t.same_outputs()

@@ -111,3 +111,14 @@ def test_finish_comes_behind_the_step(world):
     world.cache.finish(1)
     assert ("current", "waits for", "a") in world.log
     assert world.cache.rows == {2: 1} and (world.cache.table[:, 0] == -1).all() and world.cache.lens.tolist() == [0, 1, 0]
+
+
+def test_finish_gives_pages_back_when_nothing_reads_them(world):
+    """Also with the step on the current stream: what takes the pages next may run on any."""
+    for stream in (world.a, None):
+        _step(world, stream)
+        for rid in (1, 2):
+            world.cache.finish(rid)
+            at = world.log.index(("pool", "takes back"))
+            assert ("current", "is waited for") in world.log[:at]
+            world.log.clear()
