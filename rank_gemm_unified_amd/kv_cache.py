@@ -106,7 +106,7 @@ class KvCache:
                     got.setdefault(rid, []).extend(ids)
                     entries.append((row, e, ids))
         except self._rg.LoraError:
-            for rid, ids in got.items():
+            for rid, ids in reversed(got.items()):          # the last taken first: the free list as it was
                 self._rg.lora_pool_drop_kv(self.pool.handle, rid, ids[::-1])
                 if rid in fresh:
                     self._rg.lora_pool_free_kv(self.pool.handle, rid)

@@ -122,3 +122,15 @@ def test_finish_gives_pages_back_when_nothing_reads_them(world):
             at = world.log.index(("pool", "takes back"))
             assert ("current", "is waited for") in world.log[:at]
             world.log.clear()
+
+
+def test_an_append_that_fails_leaves_the_free_list_as_it_was(world):
+    """In its very order: the next pages handed out are the ones that would have been."""
+    world.cache.append({1: 2, 2: 1})
+    free = rg.lora_pool_free_list(world.pool.handle)
+    held = {r: rg.lora_pool_kv_pages(world.pool.handle, r) for r in (1, 2)}
+    with pytest.raises(rg.LoraError):
+        world.cache.append({1: 3, 3: 3, 2: 2})
+    assert rg.lora_pool_free_list(world.pool.handle) == free
+    assert held == {r: rg.lora_pool_kv_pages(world.pool.handle, r) for r in (1, 2)}
+    assert world.cache.rows == {1: 0, 2: 1} and rg.lora_pool_stats(world.pool.handle)["kv_requests"] == 2
