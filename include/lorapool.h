@@ -371,7 +371,9 @@ int lora_project_noalloc(lora_pool *pool, const void *x, const void *W, const in
  * (lora_check_device_errors).
  * Pool dtype throughout (k, v, q, out); products are summed, and softmax statistics and scores held,
  * in float32.  Rows are `ld` elements apart (a column range of a wider matrix, such as the output of
- * one projection for q, k and v, is fine); every row starts on a 16-byte boundary.
+ * one projection for q, k and v, is fine); every row starts on a 16-byte boundary.  What a call writes
+ * may overlap nothing else that it is given, unless it says so below; rows count from the first one's
+ * begin to the last one's end, with what lies between them.
  * Row counts up to LORA_MAX_TOKENS, n_seq up to LORA_MAX_SEQS, max_pages * tokens_per_page up to
  * LORA_MAX_KV_TOKENS, and n_seq times the longest length up to 2^34.  n_seq == 0 or no rows: nothing is done.
  */

@@ -115,15 +115,22 @@ int attend(lora_pool *p, const char *fn, const lora_kv_layout_t *l, const void *
     const Span qs = rows_span(q, T, ldq, width, p->elem), os = rows_span(out, T, ldo, width, p->elem);
     if (os.meets(qs) || os.meets(pages_span(p))) return set_error(LORA_EINVAL, "%s: out overlaps q or the pages", fn);
     const int64_t score_ld = (int64_t)max_pages * l->tokens_per_page;
-    if (prior && prior != scores) {
-        const size_t bytes = (size_t)n_seq * score_ld * 4;
-        if (Span{(const char *)prior, bytes}.meets({(const char *)scores, bytes}))
-            return set_error(LORA_EINVAL, "%s: prior overlaps scores without being them", fn);
-    }
     const size_t need = chunk ? kv_chunk_ws_bytes(p->dtype, *l, n_seq, T, max_len, scores != nullptr)
                               : kv_attend_ws_need(p->dtype, *l, n_seq, max_len, scores != nullptr);
     if (need > 0 && (!ws || !aligned(ws, 256) || ws_bytes < need))
         return set_error(LORA_EINVAL, "%s: workspace %zu bytes at %p: %zu needed, 256-byte aligned", fn, ws_bytes, ws, need);
+    // nothing that is written may overlap anything else, but for scores that are their own prior
+    const size_t table_bytes = (size_t)n_seq * 2 * max_pages * 4, score_bytes = (size_t)n_seq * score_ld * 4;
+    const Span written[] = {os, {(const char *)scores, score_bytes}, {(const char *)(need ? ws : nullptr), need}};
+    const Span read[] = {qs, pages_span(p), {(const char *)table, table_bytes}, {(const char *)lens, (size_t)n_seq * 4},
+                         {(const char *)q_start, ((size_t)n_seq + 1) * 4},
+                         {(const char *)(prior == scores ? nullptr : prior), score_bytes}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Span &r : read)
+            if (written[i].meets(r)) return set_error(LORA_EINVAL, "%s: out, scores or the workspace overlaps another argument", fn);
+        for (int j = 0; j < i; ++j)
+            if (written[i].meets(written[j])) return set_error(LORA_EINVAL, "%s: out, scores and the workspace overlap", fn);
+    }
     if (p->bookkeeping_only) return set_error(LORA_EINVAL, "%s: bookkeeping-only pool", fn);
     DeviceGuard g(p->device);
     if (!g.ok) return set_error(LORA_EHIP, "%s: cannot select the pool's device", fn);
