@@ -1,0 +1,85 @@
+"""The KV-cache attention calls in every form that a rule on sizes can choose, and several of them at once, on the
+device, against plain float64 forms (kv_ref.py)."""
+import numpy as np
+import pytest
+import torch
+
+import rank_gemm_unified_amd as rg
+from test_gpu_kv import DT, GEO, LENS, WIDE, Case, _gpu, check  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# 16 query heads on one K/V head of 256: the most LDS that the one-launch form takes at that head dim
+WIDE["group16_256"] = (16, 1, 256, 256, 1)
+ALL = [*GEO, "group16_256"]
+
+
+def one_launch(c, max_len=None):
+    """Whether attention of one token without scores is one launch: few workgroups, a few tiles to a wave of each."""
+    lay = c.layout
+    group = lay.n_heads // lay.n_kv_heads
+    workgroups = c.n * lay.n_kv_heads * -(-group // 16)
+    tile = 16 if c.dt is torch.float32 and lay.head_dim > 64 else 32
+    waves = 4 if lay.head_dim == 256 else 8
+    return workgroups <= 256 and -(-(max_len or c.cap) // tile) <= (3 if workgroups < 64 else 4) * waves
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("geo", ALL)
+def test_attend_without_scores_in_one_launch(geo, dtype):
+    lens = [1, 0, 2, 31, 32, 33, 64, 129] + ([] if geo == "mha128" else [63, 65, 127, 150])
+    c = Case(geo, dtype, lens, seed=41)
+    assert one_launch(c)
+    check(c, scores=False)
+
+
+@pytest.mark.parametrize("dtype,geo,lens", [
+    ("bf16", "mha64", [1000, 17, 0, 999] * 4), ("f32", "mha64", [1000, 17, 0, 999] * 4), ("bf16", "mqa128", [700, 3]),
+    ("f32", "group16", [300]), ("bf16", "group16", [700, 1]), ("bf16", "group20", [7, 690]), ("f32", "dim256", [150, 77]),
+    ("bf16", "dim256", [350, 129]), ("f32", "group3", [128] * 60), ("bf16", "group16_256", [333]), ("f32", "mha64", [1]),
+    ("bf16", "gqa64", [0]), ("f32", "mqa128", [0, 0]), ("f32", "mha128", [203]), ("bf16", "mha128", [203]),
+])
+def test_attend_without_scores_in_one_launch_shapes(geo, dtype, lens):
+    """The longest caches that the rule lets through, single and empty ones."""
+    c = Case(geo, dtype, lens, seed=42)
+    assert one_launch(c)
+    check(c, scores=False)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("geo", ALL)
+def test_attend_without_scores_in_ranges(geo, dtype):
+    """Whole sequences in one range, and pieces of one sequence in several."""
+    for lens in (LENS + [1300], [3000, 1, 0, 700]):
+        c = Case(geo, dtype, lens, seed=43)
+        assert not one_launch(c)
+        check(c, scores=False)
+
+
+@pytest.mark.parametrize("dtype,geo,lens", [
+    ("f32", "mha64", [33] * 300), ("f32", "group16", [257] * 290), ("bf16", "dim256", [64, 0, 9] * 100), ("f32", "dim256", [40] * 140),
+    ("f32", "mqa128", [4099, 3]), ("bf16", "group16", [2600]), ("f32", "group20", [2049]), ("bf16", "group3", [1, 1900, 0, 513] * 9),
+])
+def test_attend_without_scores_in_ranges_shapes(geo, dtype, lens):
+    c = Case(geo, dtype, lens, seed=44)
+    assert not one_launch(c)
+    check(c, scores=False)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_one_workspace_for_every_batch(dtype):
+    """Made for the largest batch, it serves the smaller ones, one launch or two."""
+    geo, most, longest = "gqa64", 32, 1020
+    forms = set()
+    ws = None
+    for n in (most, 4, 1, 31, 16):
+        c = Case(geo, dtype, [longest] * n, seed=45, extra_pages=2)
+        if ws is None:
+            size = rg.lora_kv_attend_workspace_size(c.pool.handle, c.layout, most, c.cap)
+            assert size > 0
+            ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        forms.add(one_launch(c))
+        want = c.run()
+        assert torch.equal(c.run(workspace=ws), want)
+        assert c.errors() == 0
+    assert forms == {False, True}
