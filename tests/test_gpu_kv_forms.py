@@ -24,6 +24,16 @@ def one_launch(c, max_len=None):
     return workgroups <= 256 and -(-(max_len or c.cap) // tile) <= (3 if workgroups < 64 else 4) * waves
 
 
+def ranges(c):
+    """Ranges that the tokens of a chunk are cut into, at most."""
+    lay = c.layout
+    group = lay.n_heads // lay.n_kv_heads
+    hpw = 4 if group % 4 == 0 else 2 if group % 2 == 0 else 1
+    rows = 128 // hpw
+    tiles = (c.T + min(c.n, c.T) * (rows - 1)) // rows
+    return max(1, min((256 if lay.head_dim == 256 else 512) // (lay.n_heads // hpw * tiles), c.cap // 256, 512))
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("geo", ALL)
 def test_attend_without_scores_in_one_launch(geo, dtype):
@@ -83,3 +93,24 @@ def test_one_workspace_for_every_batch(dtype):
         assert torch.equal(c.run(workspace=ws), want)
         assert c.errors() == 0
     assert forms == {False, True}
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("geo,lens,new,least", [
+    ("gqa64", [40000], [1], 65), ("gqa64", [20000, 40000], [2, 1], 65), ("mqa128", [33000, 5], [3, 1], 65), ("dim256", [20000], [5], 65),
+    ("mqa128", [131071], [2], 512),
+])
+def test_chunk_in_many_ranges(geo, lens, new, least, dtype):
+    """More ranges than the join has lanes, and as many as there can be."""
+    c = Case(geo, dtype, lens, new, seed=46, gap=1)
+    assert ranges(c) >= least
+    check(c)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("geo,lens,new", [("gqa64", [5000, 0, 257], [1, 3, 3]), ("mqa128", [0, 2500], [40, 40]), ("dim256", [1025, 0], [7, 9])])
+def test_chunk_in_ranges_of_rows_without_a_cache(geo, lens, new, dtype):
+    """New tokens of an unused row: zero rows."""
+    c = Case(geo, dtype, lens, new, seed=47, gap=1)
+    assert ranges(c) > 1
+    check(c)
