@@ -114,3 +114,79 @@ def test_chunk_in_ranges_of_rows_without_a_cache(geo, lens, new, dtype):
     c = Case(geo, dtype, lens, new, seed=47, gap=1)
     assert ranges(c) > 1
     check(c)
+
+
+def _together(cases, calls):
+    """calls: one per case and turn, on a stream per case, none waited for; every stream is busy at first, so that the
+    calls behind run at the same time."""
+    want = []
+    for c in cases:
+        sc = torch.zeros((c.n, c.cap), device="cuda")
+        want.append((c.run(scores=sc).clone(), sc, c.run().clone()))
+    streams = [torch.cuda.Stream() for _ in cases]
+    busy = torch.randn((4096, 4096), device="cuda").bfloat16()
+    got = [[] for _ in cases]
+    sums = [[torch.zeros_like(w[1]) for _ in range(calls)] for w in want]
+    torch.cuda.synchronize()
+    for s in streams:
+        with torch.cuda.stream(s):
+            for _ in range(8):
+                torch.mm(busy, busy)
+    for i in range(calls):
+        for c, s, g, z in zip(cases, streams, got, sums):
+            on = s if i % 2 else s.cuda_stream
+            g.append((c.run(scores=z[i], stream=on), c.run(stream=on)))
+    torch.cuda.synchronize()
+    for c, w, g, z in zip(cases, want, got, sums):
+        for i in range(calls):
+            assert torch.equal(g[i][0], w[0]) and torch.equal(g[i][1], w[2]) and torch.equal(z[i], w[1]), (i, c.lens)
+        assert c.errors() == 0
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_calls_at_the_same_time(dtype):
+    """On streams of their own, tokens and chunks, whole, in ranges and in one launch: workspaces and scores do not mix."""
+    _together([Case("gqa64", dtype, [700, 33, 1500], seed=51), Case("gqa64", dtype, [1500, 700, 33], seed=52),
+               Case("gqa64", dtype, [900, 300], [20, 9], seed=53), Case("gqa64", dtype, [300, 900], [9, 20], seed=54)], 12)
+
+
+def test_calls_of_one_pool_at_the_same_time():
+    """One pool and one table, other queries."""
+    a = Case("mqa128", "bf16", [700, 33, 1500], seed=55)
+    b = Case("mqa128", "bf16", [700, 33, 1500], seed=55)
+    b.pool, b.d_table, b.table = a.pool, a.d_table, a.table
+    b.q.normal_(generator=b.g)
+    _together([a, b], 20)
+
+
+@pytest.mark.parametrize("new", [None, [20, 9]])
+def test_graphs_replayed_at_the_same_time(new):
+    """Two captured calls share no workspace: replayed on two streams at once, several times."""
+    cases = [Case("gqa64", "bf16", lens, new, seed=seed, extra_pages=0) for lens, seed in (([900, 1300], 56), ([1300, 900], 57))]
+    sums = [torch.zeros((c.n, c.cap), device="cuda") for c in cases]
+    eager = [torch.zeros_like(z) for z in sums]
+    want = [c.run(scores=z) for c, z in zip(cases, eager)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c, z in zip(cases, sums):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c.run(scores=z))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in cases]
+    busy = torch.randn((4096, 4096), device="cuda").bfloat16()
+    for turn in range(5):
+        for o, z in zip(outs, sums):
+            o.fill_(7.25)
+            z.zero_()
+        torch.cuda.synchronize()
+        for s in streams:
+            with torch.cuda.stream(s):
+                for _ in range(4):
+                    torch.mm(busy, busy)
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for c, o, w, z, e in zip(cases, outs, want, sums, eager):
+            assert torch.equal(o, w) and torch.equal(z, e), turn
