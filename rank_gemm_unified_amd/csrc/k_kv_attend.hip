@@ -13,7 +13,8 @@
 // 64 sequences below.  bfloat16, head_dim 128, 32 heads, with scores: 64 sequences of up to 1031 tokens (637 MB of K, V
 // and scores): 116 - 121 us (5.3 - 5.5 TB/s), and 11.6 us for the join, which reads the logits; 8 of up to 32768 on
 // 8 K/V heads (748 MB): 138 - 146 us (5.1 - 5.4 TB/s), and 15.7.  float32, 16 sequences of up to 777 tokens, 16 heads
-// of 64, in one launch: 18.7 us (3.6 TB/s: few tiles a wave).  A copy of 1 GiB reaches 5.5 TB/s.
+// of 64, in one launch: 18.1 - 20.7 us (3.3 - 3.7 TB/s: few tiles a wave); with scores 19.4 and 6.8 for the join.  A copy of
+// 1 GiB reaches 5.5 TB/s.
 #include <algorithm>
 
 #include "kv_device.h"
@@ -121,8 +122,9 @@ __global__ __launch_bounds__(LOCAL ? 256 * split_waves(HD) : 256, split_waves(HD
     __shared__ int64_t sh_total;
     __shared__ int32_t sh_b[4], sh_j[4];
     // logits on their way to memory.  Stores are waited for in their turn with the loads around them, and take
-    // longest where loads fill the queues, so a wave gathers what it can hold first (8 x 32768 tokens, 32 heads on
-    // 8 K/V heads: 222 us stored tile by tile, 218 gathered in 4 KiB, 202 in 15 KiB, 189 without logits).
+    // longest where loads fill the queues, so a wave gathers what it can hold first (whole calls, 8 sequences of 32768 tokens
+    // each, 32 heads on 8 K/V heads, 1.08 GB: 243 us stored tile by tile, 231 gathered in 4 KiB, 216 in 15 KiB; without
+    // scores, and so without logits, 194).
     __shared__ __align__(16) float sh_log[4][SCORES ? 3840 : 4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
 
@@ -679,9 +681,12 @@ SplitPlan split_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, in
     s.ncb = (group + 15) / 16;
     s.hu = n_kv * s.ncb;
     // One workgroup per (sequence, head), all of them on the chip at once, where none of their waves gets more than a few
-    // tiles: 32 heads of 128, one sequence of 203 tokens 6.3 us (ranges and join: 11.2), of 768 12.2 (12.9), of 1024
-    // 14.7 (13.8); eight of 1024 23.6 (29.6).  Behind that the ranges are as fast, and lengths that differ leave
-    // none of their waves idle.  Scores need every head's sums, so they keep the second launch.
+    // tiles.  Whole calls, 32 heads of 128: one sequence of 203 tokens 8.5 us (ranges and join: 12.5), of 768 12.5 (13.9),
+    // eight of 1024 28.0 (33.4).  With fewer than 64 workgroups three tiles a wave are the most, for float32: one sequence
+    // of 400 tokens would take 17.0 (15.0), of 512 19.0 (16.4).  (bfloat16 keeps to the same, though four would do: one of
+    // 1024 14.8 (15.8), 16 heads of 64 10.5 (13.8), 16 of 256 on 4, 512 tokens, 15.8 (15.4).)  Behind that the ranges are as
+    // fast, and lengths that differ leave none of their waves idle.  Scores need every head's sums, so they keep the second
+    // launch.
     const int64_t wgs = (int64_t)n_seq * s.hu;
     auto few = [&](int64_t w) { return (max_len + tt - 1) / tt <= (w < 64 ? 3 : 4) * 4 * split_waves(hd); };
     s.local = !scores && wgs <= 256 && few(wgs);

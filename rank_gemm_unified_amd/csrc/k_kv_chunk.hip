@@ -10,12 +10,13 @@
 // in place as the right operand of the second: the weights never leave their registers.  V^T comes out of
 // LDS through the transposing read.  Two workgroups a CU: one's softmax runs under the other's products.
 //
-// bfloat16, head_dim 128, 32 heads: the last 2048 of 16384 tokens on 8 K/V heads (515 GFLOP) 542 us, 950 TFLOP/s, where a
-// large matrix product reaches 1220; one prompt of 4096 tokens (137 GFLOP) 194 us; eight of 512 (17 GFLOP, 134 MB)
-// 46.5 us.  A long cache is bound by one wave's chain of LDS reads, products and softmax with two waves a SIMD; short
-// prompts by what a workgroup does around its steps (8 us: its sequence, its page ids, the first K, the rows' way out;
-// 2 us a step).  Few rows on a long cache are cut along it: 512 tokens behind 15872 192 us, 700 TFLOP/s.  float32,
-// head_dim 64, 5 x 201 tokens behind 130: 30.4 us.
+// bfloat16, head_dim 128, 32 heads: the last 2048 of 16384 tokens on 8 K/V heads (515 GFLOP) 562 - 577 us on several cards,
+// 890 - 915 TFLOP/s, where a large matrix product reaches 1220; one prompt of 4096 tokens (137 GFLOP) 181 us; eight of 512
+// (17 GFLOP, 134 MB) 45 - 48 us.  A long cache is bound by one wave's chain of LDS reads, products and softmax with two waves
+// a SIMD; short prompts by what a workgroup does around its steps (8 us: its sequence, its page ids, the first K, the rows'
+// way out; 2 us a step).  Few rows on a long cache are cut along it: 512 tokens behind 15872 173 us, 781 TFLOP/s.  float32,
+// head_dim 64, 5 x 201 tokens behind 130: 30.5 us.  There a step of 32 tokens is 64 products of 64 cycles in one wave,
+// 1.7 us; the 11 steps of the longest rows are 19 us, on fewer waves (640 at most) than the GPU has SIMDs.
 #include <algorithm>
 #include <type_traits>
 
@@ -752,9 +753,11 @@ ChunkPlan chunk_plan(int n_heads, int n_kv, int hd, int32_t n_seq, int64_t T, in
     const int32_t tq = 128 / p.hpw;
     p.tiles = (int32_t)((T + std::min<int64_t>(n_seq, T) * (tq - 1)) / tq);   // at most
     // A tile's tokens are cut into ranges of 256 or more where the tiles alone do not fill the GPU, two workgroups a CU (one,
-    // head_dim 256).  bfloat16, 32 heads of 128 on 8: 2 x 12 tokens behind up to 12664 287 us whole, 36 in ranges,
-    // 512 behind 15872 412 and 192; float32, 4 heads of 64 on 2, 4 x 1 behind 12898: 955 and 48.  Below 512 tokens the
-    // joining launch costs more (9 x 98 tokens behind 194, 16 heads of 256 on 4: 62 whole, 71 in two).
+    // head_dim 256).  Whole calls: bfloat16, 32 heads of 128 on 8: 2 x 12 tokens behind 12652 295 us whole, 42 in ranges,
+    // 512 behind 15872 387 and 173; float32, 4 heads of 64 on 2, 4 x 1 behind 12897: 962 and 50.  Below 512 tokens it goes
+    // either way, and they are left whole: 4 x 64 behind 300, 32 heads of 128 on 8, 17.9 us whole, 24.8 in two, 1 x 8 behind
+    // 480 19.7 and 17.4; float32, 16 heads of 64 35.7 and 30.7; 16 heads of 256 on 4, 2 x 40 behind 400, 38.1 and 32.1, in
+    // float32 161 and 103.
     const int64_t wgs = (int64_t)p.groups * p.tiles, most = std::min<int64_t>(max_len / PH, RANGES);
     const int slots = hd == 256 ? 256 : 512;
     p.ranges = (int32_t)std::max<int64_t>(1, std::min(slots / std::max<int64_t>(wgs, 1), most));
@@ -764,7 +767,7 @@ ChunkPlan chunk_plan(int n_heads, int n_kv, int hd, int32_t n_seq, int64_t T, in
     const int64_t rows = most < 2 ? 0 : std::min<int64_t>(most * T * n_heads, 128 * slots);
     p.off_part = scores ? up256((size_t)T * n_heads * 8) : 0;
     // Query heads of a K/V head go to more workgroups while the GPU has room, four a CU (the whole call, float32, 8 heads of
-    // 128 on one, 6 x 377 tokens: 321 us -> 104; bfloat16, 32 on 8, 2 x 1184: 139 -> 82).
+    // 128 on one, 6 x 377 tokens: 316 us -> 102; bfloat16, 32 on 8, 2 x 1184: 141 -> 88).
     const int64_t one = (int64_t)n_kv * n_seq * ((max_len + 127) / 128);
     p.hs = (int32_t)std::max<int64_t>(1, std::min<int64_t>(group, 1024 / std::max<int64_t>(one, 1)));
     while (group % p.hs) --p.hs;
@@ -802,8 +805,8 @@ hipError_t run(const KvArgs &a, const KvAttend &at, hipStream_t s) {
     };
     const int32_t seqs = std::min(a.n_seq, a.T);
     // Pairs where they fill the GPU, two workgroups a CU, and sequences are so short that starts count (32 heads of 128:
-    // 8 x 512 tokens 49.0 us one by one, 46.5 in pairs, 4 x 1024 68.4 and 65.8, 2 x 2048 104.9 and 108.7).  Not for
-    // float32 and head_dim 256, which products and registers bind.
+    // 8 x 512 tokens 55.6 us one by one, 49.1 in pairs, 4 x 1024 75.9 and 71.3, 2 x 2048 125.6 and 124.4, kernels alone from
+    // a profile's colder clocks).  Not for float32 and head_dim 256, which products and registers bind.
     constexpr bool CAN = C::BF && HD <= 128;
     hipError_t e;
     if (ck.ranges > 1) {
