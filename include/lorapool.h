@@ -181,7 +181,8 @@ int lora_pool_evict_adapter(lora_pool *pool, int32_t adapter_id, void *stream);
  * LORA_EINVAL. */
 int lora_pool_grow_kv(lora_pool *pool, int64_t request_id, int32_t layers, int64_t *page_ids_out);
 
-/* Request finished: its KV pages return to the end of the free list.  Errors: LORA_ENOENT. */
+/* Request finished: its KV pages return to the end of the free list.  The caller must not give back
+ * pages that queued, unfinished work still reads.  Errors: LORA_ENOENT. */
 int lora_pool_free_kv(lora_pool *pool, int64_t request_id);
 
 /* ---- queries (host only, no device work) ----------------------------------------------------- */
@@ -449,7 +450,8 @@ size_t lora_kv_attend_chunk_workspace_size(const lora_pool *pool, const lora_kv_
  *   q, out       device [T][n_heads * head_dim]; sequence b's rows as q_start says
  *   scores       as lora_kv_attend's, summed over the sequence's new tokens too
  * bfloat16 pools: the weights are rounded to bfloat16 for the product with V, off by at most 2^-8 of
- * themselves, the largest not at all (scores take them unrounded).  The rest as lora_kv_attend.  Errors: LORA_EINVAL, LORA_EHIP.
+ * themselves, the largest not at all (scores take them unrounded).  An infinite value whose weight is
+ * zero makes a row NaN or that infinity.  The rest as lora_kv_attend.  Errors: LORA_EINVAL, LORA_EHIP.
  */
 int lora_kv_attend_chunk(lora_pool *pool, const lora_kv_layout_t *layout, const void *q, int64_t ldq,
                          const int32_t *table, int32_t max_pages, const int32_t *q_start,

@@ -7,7 +7,8 @@ import torch
 
 class KvCache:
     """Up to max_seqs requests of up to max_tokens tokens each.  A request takes one row of every table;
-    rows without a request have length 0 (padding).
+    rows without a request have length 0 (padding).  A request's pages belong to one cache: its id is used in no other
+    over the same pool.
 
         cache = KvCache(pool, layers, layout, max_seqs, max_tokens, scores=True)
         cache.append({7: 512, 9: 300})            # two prompts: pages, table rows, lengths
