@@ -53,6 +53,7 @@ class KvCache:
         self.length = [0] * max_seqs
         self._chunk = False
         self._used = {}                                   # handle -> stream that calls of this step ran on
+        self._runs_on(None)                               # what filled the tensors above
 
     def _runs_on(self, stream):
         """Note the stream of a call: what changes the cache next comes behind it."""

@@ -134,3 +134,10 @@ def test_an_append_that_fails_leaves_the_free_list_as_it_was(world):
     assert rg.lora_pool_free_list(world.pool.handle) == free
     assert held == {r: rg.lora_pool_kv_pages(world.pool.handle, r) for r in (1, 2)}
     assert world.cache.rows == {1: 0, 2: 1} and rg.lora_pool_stats(world.pool.handle)["kv_requests"] == 2
+
+
+def test_the_first_append_comes_behind_what_made_the_tables(world):
+    """They are filled on the stream that was current then."""
+    world.current = world.b
+    world.cache.append({1: 2})
+    assert world.log[0] == ("b", "waits for", "current")
