@@ -405,6 +405,10 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_chunk(KvArgs 
                 }
             l += ps;
             if constexpr (BF) {
+                // Weights rounded once to bfloat16, the type that V comes and the output goes in.  With the rest of each as a
+                // second product, as for one token, the error is the output's own rounding (0.0017 from float64 instead of
+                // 0.0020 behind 14336 tokens, 0.0016 instead of 0.0018 at 8 x 512), but these products are what bounds the call:
+                // 567 us would be 734, one prompt of 4096 tokens 181 and 229, 8 x 512 45 and 53.
                 const int i16 = lane & 15;
 #pragma unroll
                 for (int s = 0; s < NT / 16; ++s) {

@@ -116,3 +116,43 @@ def test_pages_of_a_finished_request_may_be_written_at_once():
             p.pages[torch.as_tensor(sum(pages, [])).to("cuda", non_blocking=False)] = float("nan")
         s.synchronize()
     t.same_outputs()
+
+
+def test_a_captured_step_replayed_after_each_append():
+    """write and attend of a decode step, captured once and replayed, against the same steps run eagerly."""
+    t = Twin()
+    t.step({1: 300, 2: 41})
+    torch.cuda.synchronize()
+    eager, replayed = t.caches
+    k, v, q = (torch.zeros((LAYERS, ROWS, w * DIM), dtype=t.dt, device="cuda") for w in (NKV, NKV, NH))
+
+    def calls(cache):
+        outs = []
+        for layer in range(LAYERS):
+            cache.write(layer, k[layer], v[layer])
+            outs.append(cache.attend(layer, q[layer]))
+        return outs
+
+    graph = None
+    for counts in ({1: 1, 2: 1}, {1: 1}, {2: 1, 3: 1}, {1: 1, 2: 1, 3: 1}):
+        for x in (k, v, q):
+            x.normal_(generator=t.g)
+        eager.append(counts)
+        want = calls(eager)
+        replayed.append(counts)
+        if graph is None:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                outs = calls(replayed)
+        for o in outs:
+            o.fill_(7.25)
+        graph.replay()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w), counts
+        if counts == {1: 1}:
+            assert [c.evict(200, 2, 9) for c in t.caches] == [{1: 102}] * 2
+    t.same()
+    for rid in (1, 2, 3):
+        for c in t.caches:
+            c.finish(rid)
+    t.same()
