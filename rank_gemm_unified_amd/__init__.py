@@ -607,6 +607,9 @@ class Pool:
                 if q_start is None else \
                 lora_kv_attend_chunk_workspace_size(self.handle, layout, n, T, max_len, scores is not None)
             workspace = self._empty(here, stream, (need,), torch.uint8) if need else None
+        elif not workspace.is_cuda or workspace.get_device() != self.pages.get_device() or not workspace.is_contiguous():
+            raise ValueError(f"workspace: contiguous memory on {self.pages.device} is wanted, not {tuple(workspace.shape)} on "
+                             f"{workspace.device}, strides {workspace.stride()}")
         args = (None if prior is None else prior.data_ptr(), None if scores is None else scores.data_ptr(),
                 None if workspace is None else workspace.data_ptr(),
                 0 if workspace is None else workspace.numel() * workspace.element_size())

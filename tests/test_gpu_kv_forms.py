@@ -190,3 +190,17 @@ def test_graphs_replayed_at_the_same_time(new):
         torch.cuda.synchronize()
         for c, o, w, z, e in zip(cases, outs, want, sums, eager):
             assert torch.equal(o, w) and torch.equal(z, e), turn
+
+
+@pytest.mark.parametrize("new", [None, [3, 5]])
+def test_workspaces_refused(new):
+    """Memory of the host or with gaps never reaches a kernel; too little of it is the call's own refusal."""
+    c = Case("gqa64", "bf16", [700, 1500], new)
+    size = 1 << 24
+    for ws in (torch.zeros(size, dtype=torch.uint8), torch.zeros(2 * size, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            c.run(workspace=ws)
+    with pytest.raises(rg.LoraError):
+        c.run(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(c.run(workspace=torch.zeros(size, dtype=torch.uint8, device="cuda")), c.run())
+    assert c.errors() == 0
