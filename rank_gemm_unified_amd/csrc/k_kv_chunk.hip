@@ -10,8 +10,8 @@
 // in place as the right operand of the second: the weights never leave their registers.  V^T comes out of
 // LDS through the transposing read.  Two workgroups a CU: one's softmax runs under the other's products.
 //
-// bfloat16, head_dim 128, 32 heads: the last 2048 of 16384 tokens on 8 K/V heads (515 GFLOP) 562 - 577 us on several cards,
-// 890 - 915 TFLOP/s, where a large matrix product reaches 1220; one prompt of 4096 tokens (137 GFLOP) 181 us; eight of 512
+// bfloat16, head_dim 128, 32 heads: the last 2048 of 16384 tokens on 8 K/V heads (515 GFLOP) 558 - 577 us on several cards,
+// 890 - 925 TFLOP/s, where a large matrix product reaches 1220; one prompt of 4096 tokens (137 GFLOP) 181 us; eight of 512
 // (17 GFLOP, 134 MB) 45 - 48 us.  A long cache is bound by one wave's chain of LDS reads, products and softmax with two waves
 // a SIMD; short prompts by what a workgroup does around its steps (8 us: its sequence, its page ids, the first K, the rows'
 // way out; 2 us a step).  Few rows on a long cache are cut along it: 512 tokens behind 15872 173 us, 781 TFLOP/s.  float32,
