@@ -492,6 +492,117 @@ int lora_kv_evict(lora_pool *pool, const lora_kv_layout_t *layout, int32_t layer
  * queued, unfinished work still reads.  Errors: LORA_ENOENT, LORA_EINVAL. */
 int lora_pool_drop_kv(lora_pool *pool, int64_t request_id, const int64_t *page_ids, int64_t n);
 
+/* ---- steps of drafted tokens: planned, written, attended and accepted on the GPU ------------------ */
+
+/*
+ * A step of speculative decoding: each sequence gets a few drafted tokens, a tree of them, the model takes them all at
+ * once, and the path that it agrees with stays.  The calls above serve a step whose lengths the host knows; here the
+ * lengths, the page tables and the free pages live on the GPU, so that a step follows another without the host:
+ *     lora_kv_plan        rows, pages, slots, positions and masks of the step, from each sequence's new tokens
+ *     lora_kv_write_rope  per layer: q and k turned by the positions, K and V to their slots
+ *     lora_kv_attend_tree per layer: attention of the tree's nodes (lora_kv_attend[_chunk] serve steps without trees)
+ *     lora_kv_accept      the agreed path, its K and V closed up in every layer, the new lengths
+ * A sequence's m new tokens are the nodes 0 .. m - 1 of its tree, in the order of its rows; node 0 is the root (the token
+ * chosen last), and parents[row] names each other node's parent, a node before it in the same sequence.
+ * table, lens, q_start, rows and errors as above.  Every buffer is the caller's, on the pool's device.
+ */
+#define LORA_MAX_TREE 256       /* new tokens of a sequence in a step with trees */
+
+/*
+ * Plan a step.  Sequence b, which holds lens[b] tokens in held[b] pages a layer, gets counts[b] >= 0 new ones:
+ *   rows       q_start: prefix sums of the counts; step_lens[b]: its length with the new ones, 0 where counts[b] is 0 or
+ *              the sequence is refused (the calls of the step then leave it alone, its output is zero)
+ *   pages      it holds ceil(length / tokens_per_page) pages of each layer's K and V afterwards.  What it lacks comes from
+ *              the stock, what it has too much (lens[b] shrunk since the last plan) goes back there, behind what can be
+ *              taken in this call: a finished request is lens[b] = 0, counts[b] = 0
+ *   slots      [layers][2][T]: where each row's K and V go: page * tokens_per_page + place in the page; -1 for rows of
+ *              refused sequences and rows behind the last
+ *   positions  [T]: the row's place in its sequence, or, with parents, lens[b] + its depth in the tree; 0 where slots are -1
+ *   mask       [T][(max_nodes + 63) / 64]: bit j of word j / 64: the row sees its sequence's node j (itself and the nodes it
+ *              descends from); 0 where slots are -1.  parents and mask are both given or both NULL
+ *   table      device int32 [layers][n_seq][2][max_pages], as lora_kv_evict's: entries of pages that come are written; those
+ *              of pages that went stay behind the last token's, unread
+ *   stock      device int32 [stock_groups][layers][2]: a ring of page groups, one page of each layer's K and V (what
+ *              lora_pool_grow_kv hands out).  It has room for every group that exists, free or held
+ *   state      device int32 [4]: first free group's place in the ring; free groups; sequences that this call refused
+ *              although they have new tokens (state_out alone); 0 (the call counts its workgroups there)
+ * Sequences are served in order: the first that the free groups do not suffice for, and every later one that needs any, is
+ * refused: its length and pages stay.  So is one that would grow over max_len (recorded in the error word, as are counts
+ * below 0, over T or, with parents, over max_nodes, which count as 0; lengths over max_len or not covered by held; rows
+ * behind T; a parent that is no earlier node, where the walk to the root ends; page ids outside the pool, whose slots
+ * are -1).  No page is taken or given twice as long as held, table, stock and state come from one another.
+ * lens_out [n_seq], held_out [n_seq] and state_out [4] may be lens, held and state themselves.  T == 0 plans a step without
+ * rows (pages may go back).  Errors: LORA_EINVAL, LORA_EHIP.
+ */
+int lora_kv_plan(lora_pool *pool, const lora_kv_layout_t *layout, int32_t layers, int32_t n_seq, const int32_t *counts,
+                 const int32_t *lens, const int32_t *held, int32_t *table, int32_t max_pages, int64_t max_len,
+                 int32_t *stock, int32_t stock_groups, int32_t *state, int64_t T, const int32_t *parents,
+                 int32_t max_nodes, int32_t *step_lens, int32_t *q_start, int64_t *slots, int32_t *positions,
+                 uint64_t *mask, int32_t *lens_out, int32_t *held_out, int32_t *state_out, void *stream);
+
+#define LORA_ROPE_HALVES 0      /* element i of the part that turns pairs with element i + rot_dim / 2 */
+#define LORA_ROPE_NEIGHBOURS 1  /* element 2 i pairs with element 2 i + 1                              */
+
+typedef struct lora_rope {
+    const float *table;         /* device [n_positions][rot_dim / 2][2], 16-byte aligned: cosine and sine of each pair's angle */
+    int32_t n_positions;
+    int32_t rot_dim;            /* a head's first rot_dim elements turn, the rest stay: a multiple of 16 up to head_dim */
+    int32_t pairing;            /* LORA_ROPE_HALVES or LORA_ROPE_NEIGHBOURS */
+} lora_rope_t;
+
+/*
+ * One layer's rows of a step: each pair (a, b) of a q or k head becomes (a c - b s, a s + b c), c and s from the table's
+ * row positions[t], in float32 and rounded once; k and v go to their slots, q to q_out.
+ *   q, q_out     device [T][n_heads * head_dim], rows ldq (ldqo) elements apart; both NULL: k and v alone.  q_out may be q
+ *                (and ldqo ldq), and q, k and v may be column ranges of one matrix; it overlaps nothing else
+ *   k, v         device [T][n_kv_heads * head_dim], rows ldk (ldv) elements apart; outside the pool's pages
+ *   slots        device int64 [2][T], 8-byte aligned: one layer of lora_kv_plan's
+ *   positions    device int32 [T]
+ * A row whose two slots are negative is left alone (q_out too).  So is one with one negative slot, a slot outside the pool
+ * or a position outside the table, and it is recorded in the pool's error word.  Two rows for one slot are the caller's
+ * error.  Errors: LORA_EINVAL, LORA_EHIP.
+ */
+int lora_kv_write_rope(lora_pool *pool, const lora_kv_layout_t *layout, const lora_rope_t *rope, const void *q, int64_t ldq,
+                       void *q_out, int64_t ldqo, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                       const int64_t *slots, const int32_t *positions, int64_t T, void *stream);
+
+/* As lora_kv_attend_workspace_size, for lora_kv_attend_tree.  Never less for more sequences, nodes or tokens. */
+size_t lora_kv_attend_tree_workspace_size(const lora_pool *pool, const lora_kv_layout_t *layout, int32_t n_seq,
+                                          int32_t max_nodes, int64_t max_len);
+
+/*
+ * Attention of trees of new tokens: node i of a sequence reads the tokens cached before its tree, and the nodes whose bits
+ * its mask row has (its own among them, if it is to read itself), whatever any other token's K and V hold.
+ *   q, out       device [T][n_heads * head_dim]; sequence b's rows as q_start says
+ *   mask         device uint64 [T][(max_nodes + 63) / 64], as lora_kv_plan writes it; any other set of nodes will do.
+ *                Bits of nodes that a sequence does not have are not looked at
+ *   max_nodes    no sequence has more new tokens (1 .. LORA_MAX_TREE): one that does counts as empty, and is recorded
+ * A row that sees nothing comes out as zero.  Weights and the rest as lora_kv_attend; an infinite value of a node whose
+ * weight is zero makes a row that sees it NaN or that infinity.  Errors: LORA_EINVAL, LORA_EHIP.
+ */
+int lora_kv_attend_tree(lora_pool *pool, const lora_kv_layout_t *layout, const void *q, int64_t ldq,
+                        const int32_t *table, int32_t max_pages, const int32_t *q_start, const int32_t *lens,
+                        int32_t n_seq, int64_t T, const uint64_t *mask, int32_t max_nodes, int64_t max_len, float scale,
+                        void *out, int64_t ldo, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Keep the drafted tokens that the model agrees with.  tokens[row] is the token a node stands for, targets[row] the one
+ * the model chose behind it.  The path starts at node 0; from node i it goes on to the first child of i whose token is
+ * targets[i].  Node path[k]'s K and V move to place k of the tree, in `layers` layers, and the rest of the tree leaves.
+ *   table        device int32 [layers][n_seq][2][max_pages]; lens, q_start: the step's (step_lens)
+ *   lens_out     device int32 [n_seq]: the tokens before the tree and the path's; of sequences without new tokens or with a
+ *                length of 0 the entry stays as it was.  Must not be lens (it may be what lora_kv_plan next takes as lens)
+ *   path         device int32 [n_seq][max_nodes]: the path's nodes, -1 behind them; n_path [n_seq]: how many, 0 for
+ *                sequences without new tokens
+ *   next         device int32 [n_seq]: targets of the path's last node: the next tree's root; -1 where the path is empty
+ * Pages that hold moved tokens belong to one sequence alone.  A token on a bad page does not move, and is recorded; a
+ * parent that is no earlier node makes its node nobody's child.  Errors: LORA_EINVAL, LORA_EHIP.
+ */
+int lora_kv_accept(lora_pool *pool, const lora_kv_layout_t *layout, int32_t layers, int32_t n_seq, const int32_t *table,
+                   int32_t max_pages, const int32_t *q_start, const int32_t *lens, int64_t T, const int32_t *tokens,
+                   const int32_t *targets, const int32_t *parents, int32_t max_nodes, int32_t *lens_out, int32_t *path,
+                   int32_t *n_path, int32_t *next, void *stream);
+
 /* Wait for all device work, then report and clear the pool's device error word:
  * LORA_OK, or LORA_EDEVICE with a message naming the kinds of fault seen. */
 int lora_check_device_errors(lora_pool *pool);

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -25,6 +26,7 @@ LORA_VICTIM_LOAD_ORDER, LORA_VICTIM_LRU, LORA_VICTIM_FARTHEST = 0, 1, 2
 LORA_MAX_CALL_SLOTS = 4
 LORA_NOALLOC_SCRATCH_MB = 32
 LORA_MAX_SEQS, LORA_MAX_KV_TOKENS, LORA_MAX_TOKENS_PER_PAGE, LORA_MAX_HEADS = 65535, 1 << 22, 256, 1024
+LORA_MAX_TREE, LORA_ROPE_HALVES, LORA_ROPE_NEIGHBOURS = 256, 0, 1
 STATUS_NAMES = {0: "ok", -1: "einval", -2: "enomem", -3: "enoent", -4: "erank", -5: "ebusy",
                 -6: "eexist", -7: "ehip", -8: "edevice"}
 
@@ -57,6 +59,11 @@ class lora_profile_t(ctypes.Structure):
 class lora_kv_layout_t(ctypes.Structure):
     """How heads lie in a page: lora_kv_layout_t(n_heads, n_kv_heads, head_dim, tokens_per_page)."""
     _fields_ = [("n_heads", _i32), ("n_kv_heads", _i32), ("head_dim", _i32), ("tokens_per_page", _i32)]
+
+
+class lora_rope_t(ctypes.Structure):
+    """Rotary embedding: lora_rope_t(table's address, n_positions, rot_dim, pairing)."""
+    _fields_ = [("table", _vp), ("n_positions", _i32), ("rot_dim", _i32), ("pairing", _i32)]
 
 
 _f32 = ctypes.c_float
@@ -96,6 +103,14 @@ _SIGS = {
     "lora_kv_evict": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp,
                                      _i32, _vp, _vp]),
     "lora_pool_drop_kv": (ctypes.c_int, [_vp, _i64, _vp, _i64]),
+    "lora_kv_plan": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _i32, _vp, _i64, _vp, _i32,
+                                    _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "lora_kv_write_rope": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp]),
+    "lora_kv_attend_tree_workspace_size": (_sz, [_vp, _vp, _i32, _i32, _i64]),
+    "lora_kv_attend_tree": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _i64, _vp, _i32, _i64, _f32,
+                                           _vp, _i64, _vp, _sz, _vp]),
+    "lora_kv_accept": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _vp,
+                                      _vp, _vp]),
     "lora_check_device_errors": (ctypes.c_int, [_vp]),
     "lora_profile_start": (ctypes.c_int, [_vp, _i32]),
     "lora_profile_stop": (ctypes.c_int, [_vp, ctypes.POINTER(lora_profile_t)]),
@@ -397,6 +412,46 @@ def lora_kv_evict(pool, layout, layers, n_seq, table, table_out, max_pages, scor
     return _check(rc, "lora_kv_evict") if check else rc
 
 
+def lora_kv_plan(pool, layout, layers, n_seq, counts, lens, held, table, max_pages, max_len, stock, stock_groups, state, T,
+                 parents, max_nodes, step_lens, q_start, slots, positions, mask, lens_out, held_out, state_out, stream=None,
+                 check=True):
+    rc = _lib.lora_kv_plan(pool, ctypes.byref(layout), layers, n_seq, _ptr(counts), _ptr(lens), _ptr(held), _ptr(table),
+                           max_pages, max_len, _ptr(stock), stock_groups, _ptr(state), T, _ptr(parents), max_nodes,
+                           _ptr(step_lens), _ptr(q_start), _ptr(slots), _ptr(positions), _ptr(mask), _ptr(lens_out),
+                           _ptr(held_out), _ptr(state_out), _stream(stream))
+    return _check(rc, "lora_kv_plan") if check else rc
+
+
+def lora_kv_write_rope(pool, layout, rope, q, ldq, q_out, ldqo, k, ldk, v, ldv, slots, positions, T, stream=None,
+                       check=True):
+    rc = _lib.lora_kv_write_rope(pool, ctypes.byref(layout), None if rope is None else ctypes.byref(rope), _ptr(q), ldq,
+                                 _ptr(q_out), ldqo, _ptr(k), ldk, _ptr(v), ldv, _ptr(slots), _ptr(positions), T,
+                                 _stream(stream))
+    return _check(rc, "lora_kv_write_rope") if check else rc
+
+
+def lora_kv_attend_tree_workspace_size(pool, layout, n_seq, max_nodes, max_len):
+    return _lib.lora_kv_attend_tree_workspace_size(pool, ctypes.byref(layout), n_seq, max_nodes, max_len)
+
+
+def lora_kv_attend_tree(pool, layout, q, ldq, table, max_pages, q_start, lens, n_seq, T, mask, max_nodes, max_len, scale,
+                        out, ldo, workspace=None, workspace_bytes=None, stream=None, check=True):
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = _lib.lora_kv_attend_tree(pool, ctypes.byref(layout), _ptr(q), ldq, _ptr(table), max_pages, _ptr(q_start),
+                                  _ptr(lens), n_seq, T, _ptr(mask), max_nodes, max_len, scale, _ptr(out), ldo,
+                                  _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "lora_kv_attend_tree") if check else rc
+
+
+def lora_kv_accept(pool, layout, layers, n_seq, table, max_pages, q_start, lens, T, tokens, targets, parents, max_nodes,
+                   lens_out, path, n_path, next, stream=None, check=True):
+    rc = _lib.lora_kv_accept(pool, ctypes.byref(layout), layers, n_seq, _ptr(table), max_pages, _ptr(q_start), _ptr(lens),
+                             T, _ptr(tokens), _ptr(targets), _ptr(parents), max_nodes, _ptr(lens_out), _ptr(path),
+                             _ptr(n_path), _ptr(next), _stream(stream))
+    return _check(rc, "lora_kv_accept") if check else rc
+
+
 def lora_check_device_errors(pool, check=True):
     rc = _lib.lora_check_device_errors(pool)
     return _check(rc, "lora_check_device_errors") if check else rc
@@ -444,6 +499,52 @@ def run_pool_ops(pool, ops, ranks, adapter_weights, stream=None):
         else:
             raise ValueError(k)
     return out
+
+
+# ---- what the calls of a step of drafted tokens take and give ----------------------------------------
+
+class KvPlan(NamedTuple):
+    """A planned step (Pool.kv_plan): int32 step_lens [n_seq], q_start [n_seq + 1], positions [T]; int64 slots
+    [layers, 2, T], mask [T, words] or None; and int32 lens, held [n_seq] and state [4] after it."""
+    step_lens: object
+    q_start: object
+    slots: object
+    positions: object
+    mask: object
+    lens: object
+    held: object
+    state: object
+
+
+class KvAccepted(NamedTuple):
+    """What Pool.kv_accept keeps: int32 lens, n_path, next [n_seq] and path [n_seq, max_nodes]."""
+    lens: object
+    path: object
+    n_path: object
+    next: object
+
+
+class Rope:
+    """Rotary embedding of kv_write_rope: `table`, contiguous float32 [n_positions, rot_dim / 2, 2] on the device, holds
+    the cosine and sine of each position's and pair's angle.  interleaved: neighbouring elements pair, else the halves
+    of the part that turns."""
+
+    def __init__(self, table, interleaved=False):
+        if table.dtype is not torch.float32 or table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous() \
+                or not table.is_cuda:
+            raise ValueError(f"table: contiguous float32 [n_positions, rot_dim / 2, 2] on the device is wanted, not "
+                             f"{table.dtype} {tuple(table.shape)} on {table.device}")
+        self.table = table
+        self.arg = lora_rope_t(table.data_ptr(), table.shape[0], 2 * table.shape[1],
+                               LORA_ROPE_NEIGHBOURS if interleaved else LORA_ROPE_HALVES)
+
+    @classmethod
+    def of(cls, n_positions, rot_dim, base=10000.0, interleaved=False, device="cuda"):
+        """Position p turns pair i by the angle p * base ** (-2 i / rot_dim), formed in float64 (a float32 angle of a far
+        position is off by thousandths), its cosine and sine rounded once."""
+        at = torch.arange(n_positions, dtype=torch.float64, device=device)
+        angle = at[:, None] * base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+        return cls(torch.stack([angle.cos(), angle.sin()], -1).float(), interleaved)
 
 
 # ---- convenience owner of a pool's device buffers ----------------------------------------------------
@@ -558,6 +659,11 @@ class Pool:
             raise ValueError(f"{what}: contiguous {dtype} {shape} on {self.pages.device} is wanted, not {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
 
+    def _kv_workspace(self, t):
+        if not t.is_cuda or t.get_device() != self.pages.get_device() or not t.is_contiguous():
+            raise ValueError(f"workspace: contiguous memory on {self.pages.device} is wanted, not {tuple(t.shape)} on "
+                             f"{t.device}, strides {t.stride()}")
+
     def _kv_pages(self):
         if self.pages is None:
             raise ValueError("a bookkeeping-only pool holds no KV vectors")
@@ -607,9 +713,8 @@ class Pool:
                 if q_start is None else \
                 lora_kv_attend_chunk_workspace_size(self.handle, layout, n, T, max_len, scores is not None)
             workspace = self._empty(here, stream, (need,), torch.uint8) if need else None
-        elif not workspace.is_cuda or workspace.get_device() != self.pages.get_device() or not workspace.is_contiguous():
-            raise ValueError(f"workspace: contiguous memory on {self.pages.device} is wanted, not {tuple(workspace.shape)} on "
-                             f"{workspace.device}, strides {workspace.stride()}")
+        else:
+            self._kv_workspace(workspace)
         args = (None if prior is None else prior.data_ptr(), None if scores is None else scores.data_ptr(),
                 None if workspace is None else workspace.data_ptr(),
                 0 if workspace is None else workspace.numel() * workspace.element_size())
@@ -656,6 +761,140 @@ class Pool:
                       scores_out.data_ptr(), lens.data_ptr(), lens_out.data_ptr(), budget, keep_first, keep_last,
                       dropped.data_ptr(), max_drop, n_dropped.data_ptr(), stream=handle)
         return table_out, scores_out, lens_out, dropped, n_dropped
+
+
+    # ---- steps of drafted tokens ---------------------------------------------------------------------
+
+    def kv_plan(self, layout, counts, lens, held, table, stock, state, T, max_len=None, parents=None, max_nodes=0, out=None,
+                stream=None):
+        """Plan a step (lora_kv_plan): pages, slots, positions and, from parents, tree masks for counts [n_seq] new tokens,
+        T rows in all.  table: int32 [layers, n_seq, 2, max_pages] and stock: int32 [groups, layers, 2], both changed in
+        place; lens, held: int32 [n_seq], state: int32 [4].  out: a KvPlan to write into, whose lens, held and state may
+        be the ones passed in; None: new ones.  Returns the KvPlan."""
+        self._kv_pages()
+        i32, i64 = torch.int32, torch.int64
+        layers, n, mp, groups = table.shape[0], table.shape[1], table.shape[-1], stock.shape[0]
+        words = 0 if parents is None else (max_nodes + 63) // 64
+        self._kv_ints("table", table, (layers, n, 2, mp), i32)
+        self._kv_ints("stock", stock, (groups, layers, 2), i32)
+        self._kv_ints("counts", counts, (n,), i32)
+        self._kv_ints("lens", lens, (n,), i32)
+        self._kv_ints("held", held, (n,), i32)
+        self._kv_ints("state", state, (4,), i32)
+        if parents is not None:
+            self._kv_ints("parents", parents, (T,), i32)
+        handle, here = self._where(stream)
+        if out is None:
+            new = lambda shape, dtype: self._empty(here, stream, shape, dtype)  # noqa: E731
+            out = KvPlan(new((n,), i32), new((n + 1,), i32), new((layers, 2, T), i64), new((T,), i32),
+                         None if parents is None else new((T, words), i64), new((n,), i32), new((n,), i32), new((4,), i32))
+        else:
+            self._kv_ints("step_lens", out.step_lens, (n,), i32)
+            self._kv_ints("q_start", out.q_start, (n + 1,), i32)
+            self._kv_ints("slots", out.slots, (layers, 2, T), i64)
+            self._kv_ints("positions", out.positions, (T,), i32)
+            self._kv_ints("lens", out.lens, (n,), i32)
+            self._kv_ints("held", out.held, (n,), i32)
+            self._kv_ints("state", out.state, (4,), i32)
+            if parents is not None:
+                if out.mask is None:
+                    raise ValueError("parents without a mask to write")
+                self._kv_ints("mask", out.mask, (T, words), i64)
+        lora_kv_plan(self.handle, layout, layers, n, counts.data_ptr(), lens.data_ptr(), held.data_ptr(), table.data_ptr(), mp,
+                     mp * layout.tokens_per_page if max_len is None else max_len, stock.data_ptr(), groups, state.data_ptr(),
+                     T, None if parents is None else parents.data_ptr(), max_nodes, out.step_lens.data_ptr(),
+                     out.q_start.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
+                     None if parents is None else out.mask.data_ptr(), out.lens.data_ptr(), out.held.data_ptr(),
+                     out.state.data_ptr(), stream=handle)
+        return out
+
+    def kv_write_rope(self, layout, rope, q, k, v, slots, positions, q_out=None, stream=None):
+        """q and k turned by their positions, k and v to their slots (lora_kv_write_rope).  rope: a Rope; slots: int64
+        [2, T], one layer of a plan's; positions: int32 [T].  q None: k and v alone.  q_out None: a new tensor, whose rows
+        without a slot hold anything; it may be q.  Returns q_out."""
+        self._kv_pages()
+        T = k.shape[0]
+        width, wide = layout.n_kv_heads * layout.head_dim, layout.n_heads * layout.head_dim
+        ldk, ldv = self._kv_rows("k", k, width), self._kv_rows("v", v, width)
+        self._kv_ints("slots", slots, (2, T), torch.int64)
+        self._kv_ints("positions", positions, (T,), torch.int32)
+        if rope.table.get_device() != self.pages.get_device():
+            raise ValueError(f"rope: its table is on {rope.table.device}, the pool on {self.pages.device}")
+        handle, here = self._where(stream)
+        ldq = ldo = 0
+        if q is not None:
+            ldq = self._kv_rows("q", q, wide)
+            if q_out is None:
+                q_out = self._empty(here, stream, (T, wide), self.tdtype)
+            ldo = self._kv_rows("q_out", q_out, wide)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        for name, t in (("v", v), ("q", q), ("q_out", q_out)):
+            if t is not None and t.shape[0] != T:
+                raise ValueError(f"{name} has {t.shape[0]} rows and k {T}")
+        lora_kv_write_rope(self.handle, layout, rope.arg, None if q is None else q.data_ptr(), ldq,
+                           None if q is None else q_out.data_ptr(), ldo, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                           slots.data_ptr(), positions.data_ptr(), T, stream=handle)
+        return q_out
+
+    def kv_attend_tree(self, layout, q, table, lens, q_start, mask, max_nodes=None, scale=None, max_len=None, out=None,
+                       workspace=None, stream=None):
+        """Attention of trees of new tokens (lora_kv_attend_tree).  mask: int64 [T, words], a plan's; max_nodes None: 64 a
+        word; the other arguments as kv_attend_chunk's."""
+        n, mp = self._kv_table(table, lens, q_start)
+        T, width, cap = q.shape[0], layout.n_heads * layout.head_dim, mp * layout.tokens_per_page
+        ldq = self._kv_rows("q", q, width)
+        max_nodes = 64 * mask.shape[-1] if max_nodes is None else max_nodes
+        self._kv_ints("mask", mask, (T, (max_nodes + 63) // 64), torch.int64)
+        handle, here = self._where(stream)
+        if out is None:
+            out, ldo = self._empty(here, stream, (T, width), self.tdtype), width
+        else:
+            ldo = self._kv_rows("out", out, width)
+            if out.shape[0] != T:
+                raise ValueError(f"out has {out.shape[0]} rows and q {T}")
+        max_len = cap if max_len is None else max_len
+        if workspace is None:
+            need = lora_kv_attend_tree_workspace_size(self.handle, layout, n, max_nodes, max_len)
+            workspace = self._empty(here, stream, (need,), torch.uint8) if need else None
+        else:
+            self._kv_workspace(workspace)
+        lora_kv_attend_tree(self.handle, layout, q.data_ptr(), ldq, table.data_ptr(), mp, q_start.data_ptr(), lens.data_ptr(),
+                            n, T, mask.data_ptr(), max_nodes, max_len, layout.head_dim ** -0.5 if scale is None else scale,
+                            out.data_ptr(), ldo, None if workspace is None else workspace.data_ptr(),
+                            0 if workspace is None else workspace.numel() * workspace.element_size(), stream=handle)
+        return out
+
+    def kv_accept(self, layout, table, lens, q_start, tokens, targets, parents, max_nodes, out=None, stream=None):
+        """Keep the path of each tree that the model agrees with (lora_kv_accept).  table: int32 [layers, n_seq, 2,
+        max_pages]; lens, q_start: the step's; tokens, targets, parents: int32 [T].  out: a KvAccepted to write into; None:
+        a new one, its lens of sequences without new tokens those of `lens`.  Returns it."""
+        self._kv_pages()
+        i32 = torch.int32
+        layers, n, mp, T = table.shape[0], table.shape[1], table.shape[-1], tokens.shape[0]
+        self._kv_ints("table", table, (layers, n, 2, mp), i32)
+        self._kv_ints("lens", lens, (n,), i32)
+        self._kv_ints("q_start", q_start, (n + 1,), i32)
+        for name, t in (("tokens", tokens), ("targets", targets), ("parents", parents)):
+            self._kv_ints(name, t, (T,), i32)
+        handle, here = self._where(stream)
+        if out is None:
+            new = lambda shape: self._empty(here, stream, shape, i32)  # noqa: E731
+            out = KvAccepted(new((n,)), new((n, max_nodes)), new((n,)), new((n,)))
+            if here:
+                out.lens.copy_(lens)
+            else:
+                with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=self.pages.device)):
+                    out.lens.copy_(lens)
+        else:
+            self._kv_ints("lens", out.lens, (n,), i32)
+            self._kv_ints("path", out.path, (n, max_nodes), i32)
+            self._kv_ints("n_path", out.n_path, (n,), i32)
+            self._kv_ints("next", out.next, (n,), i32)
+        lora_kv_accept(self.handle, layout, layers, n, table.data_ptr(), mp, q_start.data_ptr(), lens.data_ptr(), T,
+                       tokens.data_ptr(), targets.data_ptr(), parents.data_ptr(), max_nodes, out.lens.data_ptr(),
+                       out.path.data_ptr(), out.n_path.data_ptr(), out.next.data_ptr(), stream=handle)
+        return out
 
 
 from .kv_cache import KvCache  # noqa: E402,F401

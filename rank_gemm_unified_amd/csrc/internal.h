@@ -31,6 +31,7 @@ enum : int {
     DEV_ERR_TABLE = 4,     // page-table row does not hold exactly 2*ranks[a] pages
     DEV_ERR_PAGE = 8,      // page id outside [0, num_pages)
     DEV_ERR_LEN = 16,      // a sequence length or row range out of bounds
+    DEV_ERR_TREE = 32,     // a node's parent is not a node before it
 };
 
 // ---- the pool ----------------------------------------------------------------------------------

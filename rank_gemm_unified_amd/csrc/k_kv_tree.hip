@@ -1,0 +1,655 @@
+// Attention of a tree of new tokens per sequence over the paged cache (the verification of drafted tokens).
+//
+// A sequence's m nodes times the query heads that share a K/V head are the rows of a matrix product with the K/V
+// head's tokens, node by node: row r is head r % group of node r / group.  4 * rows * head_dim operations for 2 *
+// head_dim elements of K and V: up to a hundred rows or so HBM bounds it.  The tiles (TT tokens) of all sequences, one
+// sequence behind the other, are cut into equal ranges whatever the lengths; one workgroup takes one range of one K/V
+// head and up to 16 NB rows, its waves every NW-th tile of it, K and V of the next tile in flight.  Where a sequence
+// ends the waves' sums are joined in LDS, so that only what a range has of a sequence it did not see whole goes to
+// the workspace (rows * head_dim numbers of 32 bits, once a workgroup and not once a wave); k_kv_tree_join puts those
+// pieces together.  No atomics: results do not change from call to call.
+#include <algorithm>
+
+#include "kv_ranges.h"
+
+namespace lorapool {
+
+struct KvTreeSplit {
+    int32_t R;                // ranges
+    int32_t ncb;              // blocks of 16 NB rows of one K/V head
+    int32_t rows_ld;          // rows of a piece: ncb * 16 NB
+    int32_t max_nodes, words; // 64-bit words of a row's mask
+    uint32_t group_magic;     // ceil(2^32 / group): r / group = mulhi(r, magic) for r < 2^18, group in 2..1024
+    const uint32_t *mask;     // [T][2 * words]
+    float *part_o;            // [R][2][n_kv][rows_ld][head_dim]: slot 0 a range's first piece, 1 its last
+    float2 *part_ml;          // [R][2][n_kv][rows_ld]: maximum (base-2 logits), sum
+};
+
+template <typename E, int HD, int NB>
+struct TreeTile {
+    static constexpr bool BF = sizeof(E) == 2;
+    static constexpr int TT = BF || HD == 64 ? 32 : 16;    // tokens per step
+    static constexpr int WAVES = HD == 256 || NB == 4 || (!BF && HD == 128 && NB == 2) ? 1 : 2;   // a SIMD holds: registers
+    static constexpr int NW = 4 * WAVES;                   // waves of a workgroup; one workgroup a CU
+    static constexpr int CW = 16 * NB;
+    static constexpr int LDW = HD + 4;                     // floats between rows in LDS: columns in other banks
+    static constexpr int LDS = NW * CW * (LDW * 4 + 8);
+};
+
+// Sequence b's rows and length; more new tokens than a tree may have count as none.
+__device__ __forceinline__ SeqRows tree_rows(const KvArgs &a, int32_t max_nodes, int32_t b) {
+    SeqRows s = seq_rows(a, b);
+    if (s.m > max_nodes) {
+        s.m = 0;
+        s.err = DEV_ERR_LEN;
+    }
+    return s;
+}
+template <int TT>
+__device__ __forceinline__ int32_t tree_tiles(const SeqRows &s) { return s.m ? (s.n + TT - 1) / TT : 0; }
+
+__device__ __forceinline__ int32_t node_of(const KvArgs &a, const KvTreeSplit &tr, int32_t r) {
+    return a.group == 1 ? r : (int32_t)__umulhi((uint32_t)r, tr.group_magic);
+}
+
+// LOCAL: a workgroup takes one whole sequence (blockIdx.y) of a K/V head: no second launch.  For few or short ones.
+template <typename E, int HD, int NB, bool LOCAL>
+__global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB>::WAVES)) void k_kv_tree(KvArgs a, KvAttend at, KvTreeSplit tr) {
+    using C = TreeTile<E, HD, NB>;
+    constexpr int TT = C::TT, NS = TT / 16, NW = C::NW, CW = C::CW, LDW = C::LDW, THREADS = 64 * NW;
+    constexpr bool BF = C::BF;
+    constexpr int KS = HD * (int)sizeof(E) / 64;           // 16-byte loads of a lane per token row of K
+    constexpr int NV = BF ? (TT / 32) * 8 : NS * 4;        // tokens of V a lane holds parts of
+    constexpr int VC = BF ? (HD == 64 ? 1 : HD / 128) : HD / 64;   // 16-byte (bf16, 64: 8-byte) parts of each
+    constexpr int NA = HD / 16;                            // accumulators: 16 dims x 16 rows each
+    constexpr int W = BF && HD >= 128 ? 8 : 4;             // consecutive dims of one row of the accumulators
+    extern __shared__ __align__(16) float sh_o[];          // [NW][CW][LDW], then maxima and sums [NW][CW]
+    float2 *sh_s = (float2 *)(sh_o + NW * CW * LDW);
+    __shared__ int64_t sh_sum[NW];
+    __shared__ int32_t sh_b, sh_j;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
+
+    int32_t range = 0, count = 0, b0 = 0, j0 = 0, rest = blockIdx.x;
+    const int32_t kvh = rest % a.n_kv;
+    rest /= a.n_kv;
+    const int32_t cb = rest % tr.ncb;
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        int bits = 0;
+        for (int32_t b = tid; b < a.n_seq; b += THREADS) bits |= tree_rows(a, tr.max_nodes, b).err;
+        record(a, bits);
+    }
+    // ---- where this workgroup begins ----
+    if constexpr (LOCAL) {
+        b0 = blockIdx.y;
+        count = tree_tiles<TT>(tree_rows(a, tr.max_nodes, b0));
+    } else {
+        range = rest / tr.ncb;
+        if (tid == 0) sh_b = sh_j = 0;
+        const int32_t per = (a.n_seq + THREADS - 1) / THREADS, f0 = min(a.n_seq, tid * per), f1 = min(a.n_seq, f0 + per);
+        int64_t mine = 0;
+        for (int32_t b = f0; b < f1; ++b) mine += tree_tiles<TT>(tree_rows(a, tr.max_nodes, b));
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int64_t x = __shfl_up(incl, o, 64);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 63) sh_sum[wave] = incl;
+        __syncthreads();
+        int64_t excl = incl - mine, total = 0;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            excl += i < wave ? sh_sum[i] : 0;
+            total += sh_sum[i];
+        }
+        const Ranges rg = ranges_of(total, tr.R);
+        if (range >= rg.R) return;
+        const int64_t s = rg.start(range);
+        count = uniform((int32_t)(rg.start(range + 1) - s));
+        if (mine > 0 && s >= excl && s < excl + mine) {    // one thread
+            int64_t at0 = excl;
+            int32_t b = f0;
+            for (; b < f1; ++b) {
+                const int32_t t = tree_tiles<TT>(tree_rows(a, tr.max_nodes, b));
+                if (s < at0 + t) break;
+                at0 += t;
+            }
+            sh_b = b;
+            sh_j = (int32_t)(s - at0);
+        }
+        __syncthreads();
+        b0 = uniform(sh_b);
+        j0 = uniform(sh_j);
+    }
+
+    const int64_t head_bytes = (int64_t)kvh * HD * sizeof(E);
+    const uint32_t page_units = (uint32_t)(a.page_bytes >> 7), tok_units = (uint32_t)(a.tok_bytes >> 7);
+    const float scale2 = at.scale * 1.4426950408889634f;
+
+    struct Pos { int32_t b, j, n, m, first, tiles; };      // a sequence and a tile of it
+    auto pos_of = [&](int32_t b, int32_t j) {
+        const SeqRows s = tree_rows(a, tr.max_nodes, b);
+        return Pos{b, j, uniform(s.n), uniform(s.m), uniform(s.first), uniform(tree_tiles<TT>(s))};
+    };
+    auto advance = [&](Pos p, int32_t by) {                // only called while there is such a tile
+        p.j += by;
+        while (p.j >= p.tiles && p.b + 1 < a.n_seq) p = pos_of(p.b + 1, p.j - p.tiles);
+        return p;
+    };
+    // page ids of a tile's tokens, each lane those of token lane % TT; -1 behind the sequence's end
+    auto load_ids = [&](const Pos &p, int32_t *kid, int32_t *vid) {
+        const int32_t t = p.j * TT + (lane & (TT - 1));
+        int32_t e, slot;
+        page_of(a, t, &e, &slot);
+        const int32_t *row = a.table + (int64_t)p.b * 2 * a.max_pages + e;
+        *kid = *vid = -1;
+        if (t < p.n) { *kid = row[0]; *vid = row[a.max_pages]; }
+    };
+    int bad = 0;
+    auto to_units = [&](const Pos &p, int32_t kid, int32_t vid, uint32_t *ku, uint32_t *vu) -> uint64_t {
+        const int32_t t = p.j * TT + (lane & (TT - 1));
+        int32_t e, slot;
+        page_of(a, t, &e, &slot);
+        const bool ok = kid >= 0 && vid >= 0 && kid < a.num_pages && vid < a.num_pages;
+        if (t < p.n && !ok) bad = DEV_ERR_PAGE;
+        *ku = ok ? (uint32_t)kid * page_units + (uint32_t)slot * tok_units : 0u;
+        *vu = ok ? (uint32_t)vid * page_units + (uint32_t)slot * tok_units : 0u;
+        return __ballot(ok);
+    };
+    const char *base = a.pages + head_bytes;
+    u32x4_t K[NS][KS], V[NV][VC];
+    auto load_k = [&](uint32_t ku) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            const uint32_t u = __shfl(ku, 16 * s + col, 64);
+            const char *p = base + ((uint64_t)u << 7) + 16 * g;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) K[s][i] = load16(p + 64 * i);
+        }
+    };
+    auto v_token = [&](int j) { return BF ? 32 * (j >> 3) + 16 * ((j >> 2) & 1) + 4 * g + (j & 3) : 16 * (j >> 2) + 4 * g + (j & 3); };
+    auto load_v = [&](uint32_t vu) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const uint32_t u = __shfl(vu, v_token(j), 64);
+            const char *p = base + ((uint64_t)u << 7);
+            if constexpr (BF && HD == 64) {
+                const uint2 x = *(const uint2 *)(p + 8 * col);
+                V[j][0][0] = x.x;
+                V[j][0][1] = x.y;
+            } else {
+#pragma unroll
+                for (int c = 0; c < VC; ++c) V[j][c] = load16(p + 16 * col + 256 * c);
+            }
+        }
+    };
+    // Rows of this lane's columns: cb * CW + 16 x + col.  Columns without a row take the sequence's first (they are
+    // never stored).
+    auto row_of = [&](const Pos &p, int x) {
+        const int32_t r = cb * CW + 16 * x + col;
+        return r < p.m * a.group ? r : 0;
+    };
+    u32x4_t Q[NB][KS];
+    auto load_q = [&](const Pos &p) {
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+            const int32_t r = row_of(p, x), node = node_of(a, tr, r);
+            const char *q = (const char *)at.q + ((int64_t)(p.first + node) * at.ldq + (int64_t)(kvh * a.group + r - node * a.group) * HD) * sizeof(E) + 16 * g;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) Q[x][i] = load16(q + 64 * i);
+        }
+    };
+    // Two neighbouring 32-bit words of each row's mask, from the one that the tile's first node lies in.
+    uint32_t mlo[NB], mhi[NB];
+    auto load_mask = [&](const Pos &p) {
+        const int32_t s = p.j * TT - (p.n - p.m), d = max(s, 0) >> 5;
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+            const uint32_t *w = tr.mask + (int64_t)(p.first + node_of(a, tr, row_of(p, x))) * 2 * tr.words;
+            mlo[x] = w[min(d, 2 * tr.words - 1)];
+            mhi[x] = w[min(d + 1, 2 * tr.words - 1)];
+        }
+    };
+    // Which of a tile's tokens, cached or nodes, a row sees.
+    auto window = [&](int32_t s, uint32_t lo, uint32_t hi) -> uint32_t {
+        if (s <= -32) return ~0u;
+        if (s < 0) return lo << -s | ((1u << -s) - 1);
+        return __builtin_amdgcn_alignbit(((s >> 5) + 1 < 2 * tr.words) ? hi : 0u, lo, s & 31);
+    };
+
+    f32x4_t acc[NB][NA];
+    float m[NB], l[NB];
+    bool odd = false;                                      // some node's V holds an infinity or NaN
+    auto reset = [&]() {
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+#pragma unroll
+            for (int i = 0; i < NA; ++i) acc[x][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            m[x] = -INFINITY;
+            l[x] = 0.f;
+        }
+        odd = false;
+    };
+
+    // The segment: what the range has of one sequence, its tiles [base, end) of the range, the sequence's from `from` on.
+    Pos seg = pos_of(b0, j0);
+    int32_t from = j0, begin = 0, end = min(count, seg.tiles - j0);
+    bool first_piece = true;
+    // Infinities and NaN of nodes' V, which the products leave out, to the rows that see them: into this wave's sums in LDS.
+    auto put_odd = [&]() {
+        const int32_t old = seg.n - seg.m;
+        const int32_t *row = a.table + (int64_t)seg.b * 2 * a.max_pages;
+#pragma unroll 1
+        for (int32_t t = old; t < seg.n; ++t) {
+            const int32_t i = begin + t / TT - from, j = t - old;
+            if (t / TT < from || i >= end || i % NW != wave || token_offset(a, row, t) < 0) continue;
+            const int64_t off = token_offset(a, row + a.max_pages, t);
+            if (off < 0) continue;
+            const E *v = (const E *)(base + off);
+#pragma unroll 1
+            for (int32_t d = lane; d < HD; d += 64) {
+                const float y = to_f32(v[d]);
+                if (y - y == 0.f) continue;
+#pragma unroll 1
+                for (int32_t c = 0; c < CW; ++c) {
+                    const int32_t r = cb * CW + c;
+                    if (r >= seg.m * a.group) break;
+                    const uint32_t *w = tr.mask + (int64_t)(seg.first + node_of(a, tr, r)) * 2 * tr.words;
+                    if (w[j >> 5] >> (j & 31) & 1) sh_o[(wave * CW + c) * LDW + d] += y;
+                }
+            }
+        }
+    };
+    // Join the waves' sums of the segment; out if the range saw the sequence whole, else to the workspace.
+    auto flush = [&]() {
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+            float L = l[x] + __shfl_xor(l[x], 16, 64);
+            L += __shfl_xor(L, 32, 64);
+            float *o = sh_o + (wave * CW + 16 * x + col) * LDW;
+#pragma unroll
+            for (int c = 0; c < NA / W; ++c)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int i = 0; i < W; i += 4)
+                        *(f32x4_t *)(o + 16 * W * c + W * (4 * g + r) + i) =
+                            f32x4_t{acc[x][W * c + i][r], acc[x][W * c + i + 1][r], acc[x][W * c + i + 2][r], acc[x][W * c + i + 3][r]};
+            if (g == 0) sh_s[wave * CW + 16 * x + col] = make_float2(m[x], L);
+        }
+        if (__any(odd)) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            put_odd();
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        const bool whole = from == 0 && end - begin == seg.tiles;
+        const int32_t rows = min(CW, seg.m * a.group - cb * CW);
+        const int64_t piece = (((int64_t)range * 2 + (first_piece ? 0 : 1)) * a.n_kv + kvh) * tr.rows_ld + cb * CW;
+        for (int32_t x = tid; x < rows * (HD / 4); x += THREADS) {
+            const int32_t r = x / (HD / 4), d = 4 * (x % (HD / 4));
+            float M = -INFINITY, sum = 0.f;
+            f32x4_t v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < NW; ++w) M = fmaxf(M, sh_s[w * CW + r].x);
+            const float Ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float2 ml = sh_s[w * CW + r];
+                const float f = exp2_hw(ml.x - Ms);
+                sum += ml.y * f;
+                // (a wave that saw none of the row's tokens holds zeros, or infinities of nodes whose weights are zero)
+                v += *(const f32x4_t *)(sh_o + (w * CW + r) * LDW + d) * f;
+            }
+            if (!whole) {
+                if (d == 0) tr.part_ml[piece + r] = make_float2(M, sum);
+                *(f32x4_t *)(tr.part_o + (piece + r) * HD + d) = v;
+                continue;
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            if (sum == 0.f) v = f32x4_t{0.f, 0.f, 0.f, 0.f};   // no weight: zero, also where a value is not finite
+            const int32_t rr = cb * CW + r, node = node_of(a, tr, rr);
+            E *o = (E *)at.out + (int64_t)(seg.first + node) * at.ldo + (int64_t)(kvh * a.group + rr - node * a.group) * HD + d;
+            if constexpr (BF) *(uint2 *)o = make_uint2(pack2(v[0] * inv, v[1] * inv), pack2(v[2] * inv, v[3] * inv));
+            else *(f32x4_t *)o = v * inv;
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+    };
+    if (LOCAL && cb * CW >= seg.m * a.group) return;       // no rows in this block
+
+    // ---- the pipeline: page ids two tiles ahead, K and V one ----
+    // The loads of the next tile are issued whether there is one or not (behind the last tile they read the
+    // pool's first page): a load under a condition would make every later wait a wait for all.
+    int32_t i = wave;                                      // this wave's tile of the range
+    Pos p0 = seg, p1, p2;
+    int32_t kid, vid;
+    uint32_t ku, vu;
+    uint64_t there;
+    if (i < count) p0 = advance(seg, i);
+    load_ids(p0, &kid, &vid);
+    load_q(p0);
+    load_mask(p0);
+    reset();
+    p1 = p0;
+    if (i + NW < count) p1 = advance(p0, NW);
+    there = to_units(p0, kid, vid, &ku, &vu);
+    load_ids(p1, &kid, &vid);
+    load_k(i < count ? ku : 0u);
+    load_v(i < count ? vu : 0u);
+    for (;;) {
+        while (i >= end) {                                 // this wave has no more of the segment
+            flush();
+            if (end >= count) {
+                if (bad) record(a, bad);
+                return;
+            }
+            first_piece = false;
+            reset();
+            begin = end;
+            do { seg = pos_of(seg.b + 1, 0); } while (seg.tiles == 0);
+            from = 0;
+            end = min(count, begin + seg.tiles);
+        }
+        // logits: rows are tokens, columns the query rows
+        f32x4_t S[NB][NS];
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                S[x][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    if constexpr (BF) {
+                        S[x][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, K[s][k]),
+                                                                          __builtin_bit_cast(bf16x8_t, Q[x][k]), S[x][s], 0, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            S[x][s] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(K[s][k][e]), __uint_as_float(Q[x][k][e]), S[x][s], 0, 0, 0);
+                    }
+                }
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        const bool more = i + NW < count;
+        const int32_t s0 = p0.j * TT - (p0.n - p0.m);      // the tile's first token as a node; below 0: cached before
+        uint32_t sees[NB];
+#pragma unroll
+        for (int x = 0; x < NB; ++x) sees[x] = window(s0, mlo[x], mhi[x]) & (uint32_t)there;
+        if (more && p1.b != p0.b) load_q(p1);
+        uint32_t ku1, vu1;
+        const uint64_t there1 = to_units(p1, kid, vid, &ku1, &vu1);
+        p2 = p1;
+        if (i + 2 * NW < count) p2 = advance(p1, NW);
+        load_ids(p2, &kid, &vid);
+        load_mask(p1);
+        load_k(more ? ku1 : 0u);
+        __builtin_amdgcn_sched_barrier(0);
+        const bool nodes = s0 + TT > 0;
+        const bool full = (~there & ((1ull << TT) - 1)) == 0;
+        if (!full) {                                       // what lies where no token is must not reach the products
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (!((there >> v_token(j)) & 1))
+#pragma unroll
+                    for (int c = 0; c < VC; ++c) V[j][c] = u32x4_t{0, 0, 0, 0};
+        }
+        if (nodes) {                                       // infinities and NaN of nodes: not by the products
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (s0 + v_token(j) >= 0)
+#pragma unroll
+                    for (int c = 0; c < VC; ++c)
+#pragma unroll
+                        for (int y = 0; y < (BF && HD == 64 ? 2 : 4); ++y) {
+                            const uint32_t w = V[j][c][y];
+                            uint32_t out;
+                            if constexpr (BF) out = ((w & 0x7f80u) == 0x7f80u ? w & 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? w & 0xffff0000u : 0u);
+                            else out = (w & 0x7f800000u) == 0x7f800000u ? w : 0u;
+                            if (out) odd = true;
+                            V[j][c][y] = w ^ out;
+                        }
+        }
+        // weights; statistics of this lane's rows: the four lane groups hold different tokens
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+            float mt = -INFINITY;
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float y = S[x][s][r] * scale2;
+                    if ((nodes || !full) && !(sees[x] >> (16 * s + 4 * g + r) & 1)) y = -INFINITY;
+                    S[x][s][r] = y;
+                    mt = fmaxf(mt, y);
+                }
+            mt = fmaxf(mt, __shfl_xor(mt, 16, 64));
+            mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
+            const float mn = fmaxf(m[x], mt), ms = mn == -INFINITY ? 0.f : mn;
+            const float c = exp2_hw(m[x] - ms);
+            m[x] = mn;
+            float ps = 0.f;
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    S[x][s][r] = exp2_hw(S[x][s][r] - ms);
+                    ps += S[x][s][r];
+                }
+            l[x] = l[x] * c + ps;
+#pragma unroll
+            for (int y = 0; y < NA; ++y) acc[x][y] *= c;
+        }
+        // out^T += V^T P^T: rows are dims, columns the query rows
+        if constexpr (BF) {
+#pragma unroll
+            for (int q = 0; q < TT / 32; ++q) {
+                // weights as the sum of two bfloat16 numbers, off by at most 2^-15: the first their leading bits, cut off,
+                // the second the rest, rounded, and raised to 2^-126 where it is less, unless the weight itself is: an
+                // infinite value times a weight stays that infinity, and a weight of zero stays zero.
+                u32x4_t hi[NB], lo[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float a0 = S[b][2 * q + x / 2][2 * (x & 1)], a1 = S[b][2 * q + x / 2][2 * (x & 1) + 1];
+                        const uint32_t h0 = __float_as_uint(a0) & 0xffff0000u, h1 = __float_as_uint(a1) & 0xffff0000u;
+                        hi[b][x] = h0 >> 16 | h1;
+                        const float f0 = __uint_as_float(h0), f1 = __uint_as_float(h1);
+                        lo[b][x] = pack2(__builtin_amdgcn_fmed3f(a0 - f0, f0, 0x1p-126f), __builtin_amdgcn_fmed3f(a1 - f1, f1, 0x1p-126f));
+                    }
+                constexpr int WV = HD == 64 ? 4 : 8;
+#pragma unroll
+                for (int c = 0; c < VC; ++c)
+#pragma unroll
+                    for (int x = 0; x < WV; ++x) {
+                        u32x4_t f;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            f[y] = __builtin_amdgcn_perm(V[8 * q + 2 * y + 1][c][x / 2], V[8 * q + 2 * y][c][x / 2],
+                                                         x & 1 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            acc[b][WV * c + x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8_t, f), __builtin_bit_cast(bf16x8_t, lo[b]), acc[b][WV * c + x], 0, 0, 0);
+                            acc[b][WV * c + x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8_t, f), __builtin_bit_cast(bf16x8_t, hi[b]), acc[b][WV * c + x], 0, 0, 0);
+                        }
+                    }
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int c = 0; c < VC; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+#pragma unroll
+                            for (int b = 0; b < NB; ++b)
+                                acc[b][4 * c + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(V[4 * s + r][c][e]), S[b][s][r],
+                                                                                        acc[b][4 * c + e], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        load_v(more ? vu1 : 0u);
+        p0 = p1;
+        p1 = p2;
+        there = there1;
+        i += NW;
+    }
+}
+
+// Put the pieces of a sequence (blockIdx.y) together, a wave to a row: out = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s.
+constexpr int JOIN_ROWS = 16;                              // rows a workgroup takes
+template <typename E, int HD, int TT>
+__global__ __launch_bounds__(256) void k_kv_tree_join(KvArgs a, KvAttend at, KvTreeSplit tr) {
+    __shared__ int64_t sh[8];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int32_t b = blockIdx.y, first = blockIdx.x * JOIN_ROWS;
+    const SeqRows sq = tree_rows(a, tr.max_nodes, b);
+    const int32_t rows = sq.m * a.n_heads, nt = tree_tiles<TT>(sq);
+    if (first >= rows) return;
+    int64_t before = 0, total = 0;
+    for (int32_t x = tid; x < a.n_seq; x += 256) {
+        const int32_t t = tree_tiles<TT>(tree_rows(a, tr.max_nodes, x));
+        total += t;
+        before += x < b ? t : 0;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        total += __shfl_xor(total, o, 64);
+        before += __shfl_xor(before, o, 64);
+    }
+    if (lane == 0) {
+        sh[wave] = total;
+        sh[4 + wave] = before;
+    }
+    __syncthreads();
+    total = sh[0] + sh[1] + sh[2] + sh[3];
+    before = sh[4] + sh[5] + sh[6] + sh[7];
+    Pieces p{0, -1, 0};
+    if (nt) {
+        p = pieces_of(before, before + nt, ranges_of(total, tr.R));
+        if (p.r0 == p.r1) return;                          // one range saw it whole
+    }
+    constexpr int PER = HD / 64;
+    for (int32_t x = first + wave; x < min(first + JOIN_ROWS, rows); x += 4) {
+        const int32_t node = x / a.n_heads, head = x - node * a.n_heads, kvh = head / a.group, r = node * a.group + head - kvh * a.group;
+        float m = -INFINITY, l = 0.f, acc[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+        for (int32_t s = p.r0; s <= p.r1; s += 4) {        // four loads at once
+            float2 ml[4];
+            float v[4][PER];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int32_t su = min(s + u, p.r1);
+                const int64_t pl = (((int64_t)su * 2 + (su == p.r0 ? p.s0 : 0)) * a.n_kv + kvh) * tr.rows_ld + r;
+                ml[u] = tr.part_ml[pl];
+#pragma unroll
+                for (int i = 0; i < PER; ++i) v[u][i] = tr.part_o[pl * HD + 64 * i + lane];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (s + u > p.r1) break;
+                const float mn = fmaxf(m, ml[u].x), ms = mn == -INFINITY ? 0.f : mn;
+                const float c = exp2_hw(m - ms), w = exp2_hw(ml[u].x - ms);
+                l = l * c + ml[u].y * w;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) acc[i] = acc[i] * c + v[u][i] * w;
+                m = mn;
+            }
+        }
+        E *out = (E *)at.out + (int64_t)(sq.first + node) * at.ldo + (int64_t)head * HD;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) from_f32(out + 64 * i + lane, l == 0.f ? 0.f : acc[i] * inv);
+    }
+}
+
+// ---- host ----------------------------------------------------------------------------------------
+namespace {
+
+struct TreePlan {
+    int32_t nb, ncb, R;
+    bool local;
+    size_t off_ml, total;
+};
+TreePlan tree_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int32_t max_nodes, int64_t max_len) {
+    TreePlan p;
+    const int group = n_heads / n_kv, tt = dtype == LORA_F32 && hd > 64 ? 16 : 32;
+    const int64_t rows = (int64_t)max_nodes * group, tiles = (max_len + tt - 1) / tt * n_seq;
+    p.nb = rows <= 16 || hd == 256 ? 1 : rows <= 32 || dtype == LORA_F32 ? 2 : 4;
+    p.ncb = (int32_t)((rows + 16 * p.nb - 1) / (16 * p.nb));
+    const int64_t hu = (int64_t)n_kv * p.ncb;
+    // A workgroup a CU.
+    p.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, 256 / hu));
+    p.local = n_seq * hu <= 256 && max_len <= 1024;
+    // Room for at least 256 workgroups' pieces, so that what serves the largest call serves them all: the ranges of more
+    // rows are fewer.
+    const size_t pieces = 2 * (size_t)std::min<int64_t>(tiles * hu, std::max<int64_t>(256, hu)) * 16 * p.nb;
+    p.off_ml = (pieces * hd * 4 + 255) & ~size_t(255);
+    p.total = p.local ? 0 : p.off_ml + ((pieces * 8 + 255) & ~size_t(255));
+    return p;
+}
+
+template <typename E, int HD, int NB>
+hipError_t run(const KvArgs &a, const KvAttend &at, const KvTreeArgs &ta, const TreePlan &pl, hipStream_t s) {
+    using C = TreeTile<E, HD, NB>;
+    KvTreeSplit tr{};
+    tr.R = pl.R;
+    tr.ncb = pl.ncb;
+    tr.rows_ld = pl.ncb * C::CW;
+    tr.max_nodes = ta.max_nodes;
+    tr.words = (ta.max_nodes + 63) / 64;
+    tr.group_magic = a.group == 1 ? 0 : (uint32_t)(((uint64_t(1) << 32) + a.group - 1) / a.group);
+    tr.mask = (const uint32_t *)ta.mask;
+    tr.part_o = (float *)at.ws;
+    tr.part_ml = (float2 *)((char *)at.ws + pl.off_ml);
+    const unsigned hu = (unsigned)(a.n_kv * pl.ncb);
+    auto launch = [&](auto kernel, dim3 grid) {
+        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+        if (e == hipSuccess) hipLaunchKernelGGL(kernel, grid, dim3(64 * C::NW), C::LDS, s, a, at, tr);
+        return e;
+    };
+    hipError_t e;
+    if (pl.local) {
+        e = launch(k_kv_tree<E, HD, NB, true>, dim3(hu, (unsigned)a.n_seq));
+    } else {
+        e = launch(k_kv_tree<E, HD, NB, false>, dim3(hu * pl.R));
+        if (e == hipSuccess)
+            hipLaunchKernelGGL((k_kv_tree_join<E, HD, C::TT>), dim3((unsigned)(((int64_t)ta.max_nodes * a.n_heads + JOIN_ROWS - 1) / JOIN_ROWS), (unsigned)a.n_seq),
+                               dim3(256), 0, s, a, at, tr);
+    }
+    return e == hipSuccess ? hipGetLastError() : e;
+}
+
+template <typename E, int HD>
+hipError_t by_rows(const KvArgs &a, const KvAttend &at, const KvTreeArgs &ta, hipStream_t s) {
+    const TreePlan pl = tree_plan(sizeof(E) == 4 ? LORA_F32 : LORA_BF16, a.n_heads, a.n_kv, HD, a.n_seq, ta.max_nodes, a.cap);
+    if (pl.nb == 1) return run<E, HD, 1>(a, at, ta, pl, s);
+    if constexpr (HD <= 128)
+        if (pl.nb == 2) return run<E, HD, 2>(a, at, ta, pl, s);
+    if constexpr (sizeof(E) == 2 && HD <= 128)
+        if (pl.nb == 4) return run<E, HD, 4>(a, at, ta, pl, s);
+    return hipErrorInvalidValue;
+}
+
+template <typename E>
+hipError_t by_dim(const KvArgs &a, const KvAttend &at, const KvTreeArgs &ta, hipStream_t s) {
+    return a.head_dim == 64 ? by_rows<E, 64>(a, at, ta, s) : a.head_dim == 128 ? by_rows<E, 128>(a, at, ta, s)
+                                                                               : by_rows<E, 256>(a, at, ta, s);
+}
+
+}  // namespace
+
+size_t kv_tree_ws_bytes(int dtype, const lora_kv_layout_t &l, int32_t n_seq, int32_t max_nodes, int64_t max_len) {
+    return tree_plan(dtype, l.n_heads, l.n_kv_heads, l.head_dim, n_seq, max_nodes, max_len).total;
+}
+
+hipError_t launch_kv_tree(int dtype, const KvArgs &a, const KvAttend &at, const KvTreeArgs &ta, hipStream_t s) {
+    return dtype == LORA_F32 ? by_dim<float>(a, at, ta, s) : by_dim<uint16_t>(a, at, ta, s);
+}
+
+}  // namespace lorapool

@@ -36,6 +36,51 @@ struct KvAttend {
     void *ws;
 };
 
+struct KvTreeArgs {
+    const uint64_t *mask;     // [T][(max_nodes + 63) / 64]: bit j of row i: it sees node j of its sequence
+    int32_t max_nodes;        // new tokens of a sequence, at most
+};
+
+struct KvPlan {
+    char *pages;
+    int64_t num_pages;
+    int32_t layers, n_seq, max_pages, tpp, T;
+    uint32_t tpp_magic;       // as in KvArgs
+    int32_t cap;              // largest length a sequence may reach
+    const int32_t *counts, *lens, *held, *state;
+    int32_t *table, *stock;   // [layers][n_seq][2][max_pages]; [groups][layers][2]
+    int32_t groups;
+    int32_t *step_lens, *q_start, *positions, *lens_out, *held_out, *state_out;
+    int64_t *slots;           // [layers][2][T]
+    const int32_t *parents;   // [T] or null
+    uint64_t *mask;           // [T][words]
+    int32_t max_nodes, words;
+    int *err;
+};
+
+struct KvRope {
+    char *pages;
+    int64_t num_pages, page_bytes;
+    int32_t tpp, T;
+    uint32_t tpp_magic;
+    int32_t n_heads, n_kv, head_dim, tok_bytes;
+    const float *table;       // [n_positions][rot / 2][2]
+    int32_t n_positions, rot, pairs;
+    const void *q, *k, *v;
+    void *q_out;
+    int64_t ldq, ldqo, ldk, ldv;
+    const int64_t *slots;     // [2][T]
+    const int32_t *positions;
+    int *err;
+};
+
+struct KvAccept {
+    KvArgs a;                 // table: [layers][n_seq][2][max_pages]
+    int32_t layers, max_nodes;
+    const int32_t *tokens, *targets, *parents;
+    int32_t *lens_out, *path, *n_path, *next;
+};
+
 struct KvEvict {
     int32_t layers, n_seq, max_pages, tpp;
     const int32_t *table;
@@ -53,11 +98,16 @@ struct KvEvict {
 size_t kv_attend_ws_bytes(int dtype, const lora_kv_layout_t &l, int32_t n_seq, int64_t max_len, bool scores);
 size_t kv_attend_ws_need(int dtype, const lora_kv_layout_t &l, int32_t n_seq, int64_t max_len, bool scores);
 size_t kv_chunk_ws_bytes(int dtype, const lora_kv_layout_t &l, int32_t n_seq, int64_t T, int64_t max_len, bool scores);
+size_t kv_tree_ws_bytes(int dtype, const lora_kv_layout_t &l, int32_t n_seq, int32_t max_nodes, int64_t max_len);
 
 hipError_t launch_kv_write(int dtype, const KvArgs &a, const void *k, int64_t ldk, const void *v, int64_t ldv,
                            hipStream_t s);
 hipError_t launch_kv_attend(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s);
 hipError_t launch_kv_chunk(int dtype, const KvArgs &a, const KvAttend &at, hipStream_t s);
+hipError_t launch_kv_tree(int dtype, const KvArgs &a, const KvAttend &at, const KvTreeArgs &ta, hipStream_t s);
+hipError_t launch_kv_plan(const KvPlan &p, hipStream_t s);
+hipError_t launch_kv_rope(int dtype, const KvRope &r, hipStream_t s);
+hipError_t launch_kv_accept(const KvAccept &c, hipStream_t s);
 hipError_t launch_kv_evict(const KvEvict &e, hipStream_t s);
 
 }  // namespace lorapool

@@ -26,6 +26,15 @@ int check_layout(const lora_pool *p, const char *fn, const lora_kv_layout_t *l) 
     return LORA_OK;
 }
 
+int check_layers(const char *fn, int32_t layers) {
+    return layers < 1 || layers > 65535 ? set_error(LORA_EINVAL, "%s: layers %d not in [1, 65535]", fn, layers) : LORA_OK;
+}
+int check_nodes(const char *fn, int32_t max_nodes) {
+    return max_nodes < 1 || max_nodes > LORA_MAX_TREE ? set_error(LORA_EINVAL, "%s: max_nodes %d not in [1, %d]", fn, max_nodes, LORA_MAX_TREE)
+                                                      : LORA_OK;
+}
+uint32_t magic_of(int32_t tpp) { return tpp == 1 ? 0 : (uint32_t)(((uint64_t(1) << 32) + tpp - 1) / tpp); }
+
 struct Span {
     const char *at;
     size_t bytes;
@@ -71,7 +80,7 @@ int common(lora_pool *p, const char *fn, const lora_kv_layout_t *l, const int32_
     a->head_dim = l->head_dim;
     a->group = l->n_heads / l->n_kv_heads;
     a->tpp = l->tokens_per_page;
-    a->tpp_magic = a->tpp == 1 ? 0 : (uint32_t)(((uint64_t(1) << 32) + a->tpp - 1) / a->tpp);
+    a->tpp_magic = magic_of(a->tpp);
     a->tok_bytes = l->n_kv_heads * l->head_dim * p->elem;
     return LORA_OK;
 }
@@ -199,13 +208,209 @@ extern "C" int lora_kv_attend_chunk(lora_pool *p, const lora_kv_layout_t *l, con
                   ldo, prior, scores, ws, ws_bytes, stream, true);
 }
 
+extern "C" size_t lora_kv_attend_tree_workspace_size(const lora_pool *p, const lora_kv_layout_t *l, int32_t n_seq,
+                                                     int32_t max_nodes, int64_t max_len) {
+    if (!sizes_ok(p, l, n_seq, 1, max_len) || max_nodes < 1 || max_nodes > LORA_MAX_TREE) return 0;
+    return kv_tree_ws_bytes(p->dtype, *l, n_seq, max_nodes, max_len);
+}
+
+extern "C" int lora_kv_attend_tree(lora_pool *p, const lora_kv_layout_t *l, const void *q, int64_t ldq,
+                                   const int32_t *table, int32_t max_pages, const int32_t *q_start, const int32_t *lens,
+                                   int32_t n_seq, int64_t T, const uint64_t *mask, int32_t max_nodes, int64_t max_len,
+                                   float scale, void *out, int64_t ldo, void *ws, size_t ws_bytes, void *stream) {
+    const char *fn = "lora_kv_attend_tree";
+    const int rc0 = begin(p, fn, l, n_seq, T);
+    if (rc0) return rc0 < 0 ? rc0 : LORA_OK;
+    KvArgs a{};
+    if (int rc = common(p, fn, l, table, max_pages, q_start, lens, n_seq, T, max_len, &a)) return rc;
+    const int64_t width = (int64_t)l->n_heads * l->head_dim;
+    if (int rc = check_rows(p, fn, "q", q, ldq, width, T == 1)) return rc;
+    if (int rc = check_rows(p, fn, "out", out, ldo, width, T == 1)) return rc;
+    if (!(scale == scale) || scale - scale != 0.f) return set_error(LORA_EINVAL, "%s: scale is not finite", fn);
+    if (int rc = check_nodes(fn, max_nodes)) return rc;
+    if (!q_start || !mask) return set_error(LORA_EINVAL, "%s: q_start or mask is NULL", fn);
+    if (!aligned(mask, 8)) return set_error(LORA_EINVAL, "%s: misaligned mask (8 B)", fn);
+    const size_t need = kv_tree_ws_bytes(p->dtype, *l, n_seq, max_nodes, max_len);
+    if (need > 0 && (!ws || !aligned(ws, 256) || ws_bytes < need))
+        return set_error(LORA_EINVAL, "%s: workspace %zu bytes at %p: %zu needed, 256-byte aligned", fn, ws_bytes, ws, need);
+    const Span written[] = {rows_span(out, T, ldo, width, p->elem), {(const char *)(need ? ws : nullptr), need}};
+    const Span read[] = {rows_span(q, T, ldq, width, p->elem), pages_span(p), {(const char *)table, (size_t)n_seq * 2 * max_pages * 4},
+                         {(const char *)lens, (size_t)n_seq * 4}, {(const char *)q_start, ((size_t)n_seq + 1) * 4},
+                         {(const char *)mask, (size_t)T * ((max_nodes + 63) / 64) * 8}};
+    for (const Span &w : written)
+        for (const Span &r : read)
+            if (w.meets(r)) return set_error(LORA_EINVAL, "%s: out or the workspace overlaps another argument", fn);
+    if (written[0].meets(written[1])) return set_error(LORA_EINVAL, "%s: out and the workspace overlap", fn);
+    if (p->bookkeeping_only) return set_error(LORA_EINVAL, "%s: bookkeeping-only pool", fn);
+    DeviceGuard g(p->device);
+    if (!g.ok) return set_error(LORA_EHIP, "%s: cannot select the pool's device", fn);
+    const KvAttend at{q, out, ldq, ldo, scale, nullptr, nullptr, 0, ws};
+    const hipError_t e = launch_kv_tree(p->dtype, a, at, KvTreeArgs{mask, max_nodes}, (hipStream_t)stream);
+    return e == hipSuccess ? LORA_OK : hip_error(e, fn);
+}
+
+extern "C" int lora_kv_plan(lora_pool *p, const lora_kv_layout_t *l, int32_t layers, int32_t n_seq, const int32_t *counts,
+                            const int32_t *lens, const int32_t *held, int32_t *table, int32_t max_pages, int64_t max_len,
+                            int32_t *stock, int32_t stock_groups, int32_t *state, int64_t T, const int32_t *parents,
+                            int32_t max_nodes, int32_t *step_lens, int32_t *q_start, int64_t *slots, int32_t *positions,
+                            uint64_t *mask, int32_t *lens_out, int32_t *held_out, int32_t *state_out, void *stream) {
+    const char *fn = "lora_kv_plan";
+    if (int rc = check_layers(fn, layers)) return rc;
+    const int rc0 = begin(p, fn, l, n_seq, T);
+    if (rc0 < 0) return rc0;
+    if (n_seq == 0) return LORA_OK;
+    const int64_t cap = (int64_t)max_pages * l->tokens_per_page;
+    if (max_pages < 1 || cap > LORA_MAX_KV_TOKENS)
+        return set_error(LORA_EINVAL, "%s: max_pages %d: %lld tokens not in [1, %d]", fn, max_pages, (long long)cap,
+                         LORA_MAX_KV_TOKENS);
+    if (max_len < 1 || max_len > cap)
+        return set_error(LORA_EINVAL, "%s: max_len %lld not in [1, %lld]", fn, (long long)max_len, (long long)cap);
+    if (stock_groups < 1 || (int64_t)stock_groups * 2 * layers > (int64_t(1) << 31))
+        return set_error(LORA_EINVAL, "%s: stock of %d groups of 2 * %d pages: 1 group to 2^31 pages", fn, stock_groups, layers);
+    if ((parents == nullptr) != (mask == nullptr)) return set_error(LORA_EINVAL, "%s: parents and mask go together", fn);
+    if (parents)
+        if (int rc = check_nodes(fn, max_nodes)) return rc;
+    const int32_t words = parents ? (max_nodes + 63) / 64 : 0;
+    const size_t nb = (size_t)n_seq * 4, tb = (size_t)T * 4;
+    // nothing that is written may overlap anything else, but for the three pairs that may be one buffer
+    const struct { const void *at; size_t bytes; bool written, always; int align; } sp[] = {
+        {counts, nb, false, true, 4}, {lens, nb, false, true, 4}, {held, nb, false, true, 4}, {state, 16, false, true, 4},
+        {parents, tb, false, false, 4}, {lens_out, nb, true, true, 4}, {held_out, nb, true, true, 4}, {state_out, 16, true, true, 4},
+        {table, (size_t)layers * n_seq * 2 * max_pages * 4, true, true, 4}, {stock, (size_t)stock_groups * 2 * layers * 4, true, true, 4},
+        {step_lens, nb, true, true, 4}, {q_start, nb + 4, true, true, 4}, {slots, (size_t)layers * 2 * T * 8, true, T > 0, 8},
+        {positions, tb, true, T > 0, 4}, {mask, (size_t)T * words * 8, true, false, 8}};
+    for (int i = 0; i < 15; ++i) {
+        if (!sp[i].at && sp[i].always) return set_error(LORA_EINVAL, "%s: NULL pointer argument", fn);
+        if (!aligned(sp[i].at, sp[i].align)) return set_error(LORA_EINVAL, "%s: misaligned pointer (4 B; slots, mask: 8 B)", fn);
+        for (int j = 0; j < i; ++j) {
+            if ((!sp[i].written && !sp[j].written) || (i >= 5 && i <= 7 && j == i - 4 && sp[i].at == sp[j].at)) continue;
+            if (Span{(const char *)sp[i].at, sp[i].bytes}.meets({(const char *)sp[j].at, sp[j].bytes}))
+                return set_error(LORA_EINVAL, "%s: an output overlaps another argument", fn);
+        }
+    }
+    if (p->bookkeeping_only) return set_error(LORA_EINVAL, "%s: bookkeeping-only pool", fn);
+    DeviceGuard g(p->device);
+    if (!g.ok) return set_error(LORA_EHIP, "%s: cannot select the pool's device", fn);
+    KvPlan k{};
+    k.num_pages = p->num_pages;
+    k.layers = layers;
+    k.n_seq = n_seq;
+    k.max_pages = max_pages;
+    k.tpp = l->tokens_per_page;
+    k.tpp_magic = magic_of(k.tpp);
+    k.T = (int32_t)T;
+    k.cap = (int32_t)max_len;
+    k.counts = counts; k.lens = lens; k.held = held; k.state = state;
+    k.table = table; k.stock = stock;
+    k.groups = stock_groups;
+    k.step_lens = step_lens; k.q_start = q_start; k.positions = positions;
+    k.lens_out = lens_out; k.held_out = held_out; k.state_out = state_out;
+    k.slots = slots;
+    k.parents = parents; k.mask = mask; k.max_nodes = max_nodes; k.words = words;
+    k.err = p->dev_err;
+    const hipError_t e = launch_kv_plan(k, (hipStream_t)stream);
+    return e == hipSuccess ? LORA_OK : hip_error(e, fn);
+}
+
+extern "C" int lora_kv_write_rope(lora_pool *p, const lora_kv_layout_t *l, const lora_rope_t *rope, const void *q, int64_t ldq,
+                                  void *q_out, int64_t ldqo, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                                  const int64_t *slots, const int32_t *positions, int64_t T, void *stream) {
+    const char *fn = "lora_kv_write_rope";
+    const int rc0 = begin(p, fn, l, 1, T);
+    if (rc0) return rc0 < 0 ? rc0 : LORA_OK;
+    if (!rope || !rope->table || !aligned(rope->table, 16) || rope->n_positions < 1)
+        return set_error(LORA_EINVAL, "%s: rope: a table of at least one position, on 16 bytes, is wanted", fn);
+    if (rope->rot_dim < 16 || rope->rot_dim % 16 || rope->rot_dim > l->head_dim)
+        return set_error(LORA_EINVAL, "%s: rot_dim %d not a multiple of 16 in [16, %d]", fn, rope->rot_dim, l->head_dim);
+    if (rope->pairing != LORA_ROPE_HALVES && rope->pairing != LORA_ROPE_NEIGHBOURS)
+        return set_error(LORA_EINVAL, "%s: pairing %d is neither halves nor neighbours", fn, rope->pairing);
+    const int64_t width = (int64_t)l->n_kv_heads * l->head_dim, wide = (int64_t)l->n_heads * l->head_dim;
+    if (!q != !q_out) return set_error(LORA_EINVAL, "%s: q and q_out go together", fn);
+    if (q) {
+        if (int rc = check_rows(p, fn, "q", q, ldq, wide, T == 1)) return rc;
+        if (int rc = check_rows(p, fn, "q_out", q_out, ldqo, wide, T == 1)) return rc;
+    }
+    if (int rc = check_rows(p, fn, "k", k, ldk, width, T == 1)) return rc;
+    if (int rc = check_rows(p, fn, "v", v, ldv, width, T == 1)) return rc;
+    if (!slots || !positions) return set_error(LORA_EINVAL, "%s: NULL pointer argument", fn);
+    if (!aligned(slots, 8) || !aligned(positions, 4))
+        return set_error(LORA_EINVAL, "%s: misaligned pointer (slots: 8 B, positions: 4 B)", fn);
+    const Span qo = rows_span(q_out, q ? T : 0, ldqo, wide, p->elem), pg = pages_span(p);
+    const struct { Span span; int64_t ld, width; } read[] = {
+        {rows_span(k, T, ldk, width, p->elem), ldk, width}, {rows_span(v, T, ldv, width, p->elem), ldv, width},
+        {rows_span(q, q ? T : 0, ldq, wide, p->elem), q == q_out && ldq == ldqo ? ldq : -1, q == q_out ? 0 : wide},   // in place: no overlap
+        {{(const char *)slots, (size_t)T * 16}, -1, 0}, {{(const char *)positions, (size_t)T * 4}, -1, 0},
+        {{(const char *)rope->table, (size_t)rope->n_positions * rope->rot_dim * 4}, -1, 0}};
+    for (const auto &r : read) {
+        if (pg.meets(r.span)) return set_error(LORA_EINVAL, "%s: an input lies in the pool's pages", fn);
+        if (!qo.meets(r.span)) continue;
+        // q_out may be a column range of the matrix that k and v are others of
+        const int64_t ld = ldqo * p->elem, at = r.ld == ldqo ? (((const char *)r.span.at - qo.at) % ld + ld) % ld : 0;
+        if (r.ld != ldqo || (r.width > 0 && (at < wide * p->elem || at + r.width * p->elem > ld)))
+            return set_error(LORA_EINVAL, "%s: q_out overlaps another argument", fn);
+    }
+    if (qo.meets(pg)) return set_error(LORA_EINVAL, "%s: q_out lies in the pool's pages", fn);
+    if (p->bookkeeping_only) return set_error(LORA_EINVAL, "%s: bookkeeping-only pool", fn);
+    DeviceGuard g(p->device);
+    if (!g.ok) return set_error(LORA_EHIP, "%s: cannot select the pool's device", fn);
+    KvRope r{};
+    r.pages = (char *)p->pages;
+    r.num_pages = p->num_pages;
+    r.page_bytes = (int64_t)p->hidden * p->elem;
+    r.tpp = l->tokens_per_page;
+    r.T = (int32_t)T;
+    r.n_heads = l->n_heads; r.n_kv = l->n_kv_heads; r.head_dim = l->head_dim;
+    r.tok_bytes = (int32_t)(width * p->elem);
+    r.table = rope->table; r.n_positions = rope->n_positions; r.rot = rope->rot_dim; r.pairs = rope->pairing;
+    r.q = q; r.k = k; r.v = v; r.q_out = q_out;
+    r.ldq = ldq; r.ldqo = ldqo; r.ldk = ldk; r.ldv = ldv;
+    r.slots = slots; r.positions = positions;
+    r.err = p->dev_err;
+    const hipError_t e = launch_kv_rope(p->dtype, r, (hipStream_t)stream);
+    return e == hipSuccess ? LORA_OK : hip_error(e, fn);
+}
+
+extern "C" int lora_kv_accept(lora_pool *p, const lora_kv_layout_t *l, int32_t layers, int32_t n_seq, const int32_t *table,
+                              int32_t max_pages, const int32_t *q_start, const int32_t *lens, int64_t T,
+                              const int32_t *tokens, const int32_t *targets, const int32_t *parents, int32_t max_nodes,
+                              int32_t *lens_out, int32_t *path, int32_t *n_path, int32_t *next, void *stream) {
+    const char *fn = "lora_kv_accept";
+    if (int rc = check_layers(fn, layers)) return rc;
+    const int rc0 = begin(p, fn, l, n_seq, T);
+    if (rc0) return rc0 < 0 ? rc0 : LORA_OK;
+    KvAccept c{};
+    if (int rc = common(p, fn, l, table, max_pages, q_start, lens, n_seq, T, (int64_t)max_pages * l->tokens_per_page, &c.a)) return rc;
+    if (int rc = check_nodes(fn, max_nodes)) return rc;
+    const size_t nb = (size_t)n_seq * 4, tb = (size_t)T * 4;
+    const struct { const void *at; size_t bytes; bool written; } sp[] = {
+        {table, (size_t)layers * nb * 2 * max_pages, false}, {q_start, nb + 4, false}, {lens, nb, false}, {tokens, tb, false},
+        {targets, tb, false}, {parents, tb, false}, {p->pages, pages_span(p).bytes, true}, {lens_out, nb, true}, {path, nb * max_nodes, true},
+        {n_path, nb, true}, {next, nb, true}};
+    for (int i = 0; i < 11; ++i) {
+        if (!sp[i].at && i != 6) return set_error(LORA_EINVAL, "%s: NULL pointer argument", fn);
+        if (!aligned(sp[i].at, 4)) return set_error(LORA_EINVAL, "%s: misaligned pointer (4 B)", fn);
+        for (int j = 0; j < i; ++j)
+            if ((sp[i].written || sp[j].written) && Span{(const char *)sp[i].at, sp[i].bytes}.meets({(const char *)sp[j].at, sp[j].bytes}))
+                return set_error(LORA_EINVAL, "%s: an output overlaps another argument", fn);
+    }
+    if (p->bookkeeping_only) return set_error(LORA_EINVAL, "%s: bookkeeping-only pool", fn);
+    DeviceGuard g(p->device);
+    if (!g.ok) return set_error(LORA_EHIP, "%s: cannot select the pool's device", fn);
+    c.layers = layers;
+    c.max_nodes = max_nodes;
+    c.tokens = tokens; c.targets = targets; c.parents = parents;
+    c.lens_out = lens_out; c.path = path; c.n_path = n_path; c.next = next;
+    const hipError_t e = launch_kv_accept(c, (hipStream_t)stream);
+    return e == hipSuccess ? LORA_OK : hip_error(e, fn);
+}
+
 extern "C" int lora_kv_evict(lora_pool *p, const lora_kv_layout_t *l, int32_t layers, int32_t n_seq,
                              const int32_t *table, int32_t *table_out, int32_t max_pages, const float *scores,
                              float *scores_out, const int32_t *lens, int32_t *lens_out, int32_t budget,
                              int32_t keep_first, int32_t keep_last, int32_t *dropped, int32_t max_drop,
                              int32_t *n_dropped, void *stream) {
     const char *fn = "lora_kv_evict";
-    if (layers < 1 || layers > 65535) return set_error(LORA_EINVAL, "%s: layers %d not in [1, 65535]", fn, layers);
+    if (int rc = check_layers(fn, layers)) return rc;
     const int rc0 = begin(p, fn, l, n_seq, 1);
     if (rc0) return rc0 < 0 ? rc0 : LORA_OK;
     const int64_t cap = (int64_t)max_pages * l->tokens_per_page;

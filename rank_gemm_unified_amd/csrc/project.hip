@@ -399,9 +399,10 @@ extern "C" int lora_check_device_errors(lora_pool *p) {
     LP_HIP(hipMemcpy(&word, p->dev_err, sizeof word, hipMemcpyDeviceToHost));
     if (!word) return LORA_OK;
     LP_HIP(hipMemset(p->dev_err, 0, sizeof word));
-    return set_error(LORA_EDEVICE, "device check failed:%s%s%s%s%s", word & DEV_ERR_ID ? " adapter-id-out-of-range" : "",
+    return set_error(LORA_EDEVICE, "device check failed:%s%s%s%s%s%s", word & DEV_ERR_ID ? " adapter-id-out-of-range" : "",
                      word & DEV_ERR_RANK ? " rank-out-of-range" : "",
                      word & DEV_ERR_TABLE ? " adapter-not-loaded-at-this-rank" : "",
                      word & DEV_ERR_PAGE ? " page-id-out-of-range" : "",
-                     word & DEV_ERR_LEN ? " sequence-length-or-rows-out-of-range" : "");
+                     word & DEV_ERR_LEN ? " sequence-length-or-rows-out-of-range" : "",
+                     word & DEV_ERR_TREE ? " tree-parent-out-of-range" : "");
 }
