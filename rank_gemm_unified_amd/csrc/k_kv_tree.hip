@@ -10,47 +10,20 @@
 // pieces together.  No atomics: results do not change from call to call.
 #include <algorithm>
 
-#include "kv_ranges.h"
+#include "kv_tree.h"
 
 namespace lorapool {
-
-struct KvTreeSplit {
-    int32_t R;                // ranges
-    int32_t ncb;              // blocks of 16 NB rows of one K/V head
-    int32_t rows_ld;          // rows of a piece: ncb * 16 NB
-    int32_t max_nodes, words; // 64-bit words of a row's mask
-    uint32_t group_magic;     // ceil(2^32 / group): r / group = mulhi(r, magic) for r < 2^18, group in 2..1024
-    const uint32_t *mask;     // [T][2 * words]
-    float *part_o;            // [R][2][n_kv][rows_ld][head_dim]: slot 0 a range's first piece, 1 its last
-    float2 *part_ml;          // [R][2][n_kv][rows_ld]: maximum (base-2 logits), sum
-};
 
 template <typename E, int HD, int NB>
 struct TreeTile {
     static constexpr bool BF = sizeof(E) == 2;
     static constexpr int TT = BF || HD == 64 ? 32 : 16;    // tokens per step
-    static constexpr int WAVES = HD == 256 || NB == 4 || (!BF && HD == 128 && NB == 2) ? 1 : 2;   // a SIMD holds: registers
+    static constexpr int WAVES = HD == 256 || (!BF && HD == 128 && NB == 2) ? 1 : 2;   // a SIMD holds: registers
     static constexpr int NW = 4 * WAVES;                   // waves of a workgroup; one workgroup a CU
     static constexpr int CW = 16 * NB;
     static constexpr int LDW = HD + 4;                     // floats between rows in LDS: columns in other banks
     static constexpr int LDS = NW * CW * (LDW * 4 + 8);
 };
-
-// Sequence b's rows and length; more new tokens than a tree may have count as none.
-__device__ __forceinline__ SeqRows tree_rows(const KvArgs &a, int32_t max_nodes, int32_t b) {
-    SeqRows s = seq_rows(a, b);
-    if (s.m > max_nodes) {
-        s.m = 0;
-        s.err = DEV_ERR_LEN;
-    }
-    return s;
-}
-template <int TT>
-__device__ __forceinline__ int32_t tree_tiles(const SeqRows &s) { return s.m ? (s.n + TT - 1) / TT : 0; }
-
-__device__ __forceinline__ int32_t node_of(const KvArgs &a, const KvTreeSplit &tr, int32_t r) {
-    return a.group == 1 ? r : (int32_t)__umulhi((uint32_t)r, tr.group_magic);
-}
 
 // LOCAL: a workgroup takes one whole sequence (blockIdx.y) of a K/V head: no second launch.  For few or short ones.
 template <typename E, int HD, int NB, bool LOCAL>
@@ -65,79 +38,29 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
     constexpr int W = BF && HD >= 128 ? 8 : 4;             // consecutive dims of one row of the accumulators
     extern __shared__ __align__(16) float sh_o[];          // [NW][CW][LDW], then maxima and sums [NW][CW]
     float2 *sh_s = (float2 *)(sh_o + NW * CW * LDW);
-    __shared__ int64_t sh_sum[NW];
-    __shared__ int32_t sh_b, sh_j;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
 
-    int32_t range = 0, count = 0, b0 = 0, j0 = 0, rest = blockIdx.x;
-    const int32_t kvh = rest % a.n_kv;
-    rest /= a.n_kv;
-    const int32_t cb = rest % tr.ncb;
+    const int32_t kvh = blockIdx.x % a.n_kv, rest = blockIdx.x / a.n_kv, r0 = rest % tr.ncb * CW, range = rest / tr.ncb;
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         int bits = 0;
-        for (int32_t b = tid; b < a.n_seq; b += THREADS) bits |= tree_rows(a, tr.max_nodes, b).err;
+        for (int32_t b = tid; b < a.n_seq; b += THREADS) bits |= tree_rows(a, tr, b).err;
         record(a, bits);
     }
-    // ---- where this workgroup begins ----
+    TreeBegin w;
     if constexpr (LOCAL) {
-        b0 = blockIdx.y;
-        count = tree_tiles<TT>(tree_rows(a, tr.max_nodes, b0));
+        w = TreeBegin{(int32_t)blockIdx.y, 0, tree_tiles<TT>(a, tree_rows(a, tr, blockIdx.y), r0)};
     } else {
-        range = rest / tr.ncb;
-        if (tid == 0) sh_b = sh_j = 0;
-        const int32_t per = (a.n_seq + THREADS - 1) / THREADS, f0 = min(a.n_seq, tid * per), f1 = min(a.n_seq, f0 + per);
-        int64_t mine = 0;
-        for (int32_t b = f0; b < f1; ++b) mine += tree_tiles<TT>(tree_rows(a, tr.max_nodes, b));
-        int64_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int64_t x = __shfl_up(incl, o, 64);
-            if (lane >= o) incl += x;
-        }
-        if (lane == 63) sh_sum[wave] = incl;
-        __syncthreads();
-        int64_t excl = incl - mine, total = 0;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            excl += i < wave ? sh_sum[i] : 0;
-            total += sh_sum[i];
-        }
-        const Ranges rg = ranges_of(total, tr.R);
-        if (range >= rg.R) return;
-        const int64_t s = rg.start(range);
-        count = uniform((int32_t)(rg.start(range + 1) - s));
-        if (mine > 0 && s >= excl && s < excl + mine) {    // one thread
-            int64_t at0 = excl;
-            int32_t b = f0;
-            for (; b < f1; ++b) {
-                const int32_t t = tree_tiles<TT>(tree_rows(a, tr.max_nodes, b));
-                if (s < at0 + t) break;
-                at0 += t;
-            }
-            sh_b = b;
-            sh_j = (int32_t)(s - at0);
-        }
-        __syncthreads();
-        b0 = uniform(sh_b);
-        j0 = uniform(sh_j);
+        w = tree_begin<TT, THREADS>(a, tr, r0, range);
+        if (w.count == 0) return;
     }
+    const int32_t count = w.count;
 
     const int64_t head_bytes = (int64_t)kvh * HD * sizeof(E);
     const uint32_t page_units = (uint32_t)(a.page_bytes >> 7), tok_units = (uint32_t)(a.tok_bytes >> 7);
     const float scale2 = at.scale * 1.4426950408889634f;
 
-    struct Pos { int32_t b, j, n, m, first, tiles; };      // a sequence and a tile of it
-    auto pos_of = [&](int32_t b, int32_t j) {
-        const SeqRows s = tree_rows(a, tr.max_nodes, b);
-        return Pos{b, j, uniform(s.n), uniform(s.m), uniform(s.first), uniform(tree_tiles<TT>(s))};
-    };
-    auto advance = [&](Pos p, int32_t by) {                // only called while there is such a tile
-        p.j += by;
-        while (p.j >= p.tiles && p.b + 1 < a.n_seq) p = pos_of(p.b + 1, p.j - p.tiles);
-        return p;
-    };
     // page ids of a tile's tokens, each lane those of token lane % TT; -1 behind the sequence's end
-    auto load_ids = [&](const Pos &p, int32_t *kid, int32_t *vid) {
+    auto load_ids = [&](const TreePos &p, int32_t *kid, int32_t *vid) {
         const int32_t t = p.j * TT + (lane & (TT - 1));
         int32_t e, slot;
         page_of(a, t, &e, &slot);
@@ -146,7 +69,7 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
         if (t < p.n) { *kid = row[0]; *vid = row[a.max_pages]; }
     };
     int bad = 0;
-    auto to_units = [&](const Pos &p, int32_t kid, int32_t vid, uint32_t *ku, uint32_t *vu) -> uint64_t {
+    auto to_units = [&](const TreePos &p, int32_t kid, int32_t vid, uint32_t *ku, uint32_t *vu) -> uint64_t {
         const int32_t t = p.j * TT + (lane & (TT - 1));
         int32_t e, slot;
         page_of(a, t, &e, &slot);
@@ -183,14 +106,14 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
             }
         }
     };
-    // Rows of this lane's columns: cb * CW + 16 x + col.  Columns without a row take the sequence's first (they are
+    // Rows of this lane's columns: r0 + 16 x + col.  Columns without a row take the sequence's first (they are
     // never stored).
-    auto row_of = [&](const Pos &p, int x) {
-        const int32_t r = cb * CW + 16 * x + col;
+    auto row_of = [&](const TreePos &p, int x) {
+        const int32_t r = r0 + 16 * x + col;
         return r < p.m * a.group ? r : 0;
     };
     u32x4_t Q[NB][KS];
-    auto load_q = [&](const Pos &p) {
+    auto load_q = [&](const TreePos &p) {
 #pragma unroll
         for (int x = 0; x < NB; ++x) {
             const int32_t r = row_of(p, x), node = node_of(a, tr, r);
@@ -199,22 +122,10 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
             for (int i = 0; i < KS; ++i) Q[x][i] = load16(q + 64 * i);
         }
     };
-    // Two neighbouring 32-bit words of each row's mask, from the one that the tile's first node lies in.
-    uint32_t mlo[NB], mhi[NB];
-    auto load_mask = [&](const Pos &p) {
-        const int32_t s = p.j * TT - (p.n - p.m), d = max(s, 0) >> 5;
+    uint64_t mlo[NB], mhi[NB];
+    auto load_mask = [&](const TreePos &p) {
 #pragma unroll
-        for (int x = 0; x < NB; ++x) {
-            const uint32_t *w = tr.mask + (int64_t)(p.first + node_of(a, tr, row_of(p, x))) * 2 * tr.words;
-            mlo[x] = w[min(d, 2 * tr.words - 1)];
-            mhi[x] = w[min(d + 1, 2 * tr.words - 1)];
-        }
-    };
-    // Which of a tile's tokens, cached or nodes, a row sees.
-    auto window = [&](int32_t s, uint32_t lo, uint32_t hi) -> uint32_t {
-        if (s <= -32) return ~0u;
-        if (s < 0) return lo << -s | ((1u << -s) - 1);
-        return __builtin_amdgcn_alignbit(((s >> 5) + 1 < 2 * tr.words) ? hi : 0u, lo, s & 31);
+        for (int x = 0; x < NB; ++x) mask_at(tr, p.first + node_of(a, tr, row_of(p, x)), p.j * TT - (p.n - p.m), &mlo[x], &mhi[x]);
     };
 
     f32x4_t acc[NB][NA];
@@ -232,8 +143,8 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
     };
 
     // The segment: what the range has of one sequence, its tiles [base, end) of the range, the sequence's from `from` on.
-    Pos seg = pos_of(b0, j0);
-    int32_t from = j0, begin = 0, end = min(count, seg.tiles - j0);
+    TreePos seg = tree_pos<TT>(a, tr, r0, w.b, w.j);
+    int32_t from = w.j, begin = 0, end = min(count, seg.tiles - from);
     bool first_piece = true;
     // Infinities and NaN of nodes' V, which the products leave out, to the rows that see them: into this wave's sums in LDS.
     auto put_odd = [&]() {
@@ -252,10 +163,10 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
                 if (y - y == 0.f) continue;
 #pragma unroll 1
                 for (int32_t c = 0; c < CW; ++c) {
-                    const int32_t r = cb * CW + c;
+                    const int32_t r = r0 + c;
                     if (r >= seg.m * a.group) break;
-                    const uint32_t *w = tr.mask + (int64_t)(seg.first + node_of(a, tr, r)) * 2 * tr.words;
-                    if (w[j >> 5] >> (j & 31) & 1) sh_o[(wave * CW + c) * LDW + d] += y;
+                    const uint64_t *w = tr.mask + (int64_t)(seg.first + node_of(a, tr, r)) * tr.words;
+                    if (w[j >> 6] >> (j & 63) & 1) sh_o[(wave * CW + c) * LDW + d] += y;
                 }
             }
         }
@@ -284,8 +195,8 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         const bool whole = from == 0 && end - begin == seg.tiles;
-        const int32_t rows = min(CW, seg.m * a.group - cb * CW);
-        const int64_t piece = (((int64_t)range * 2 + (first_piece ? 0 : 1)) * a.n_kv + kvh) * tr.rows_ld + cb * CW;
+        const int32_t rows = min(CW, seg.m * a.group - r0);
+        const int64_t piece = (((int64_t)range * 2 + (first_piece ? 0 : 1)) * a.n_kv + kvh) * tr.rows_ld + r0;
         for (int32_t x = tid; x < rows * (HD / 4); x += THREADS) {
             const int32_t r = x / (HD / 4), d = 4 * (x % (HD / 4));
             float M = -INFINITY, sum = 0.f;
@@ -308,7 +219,7 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             if (sum == 0.f) v = f32x4_t{0.f, 0.f, 0.f, 0.f};   // no weight: zero, also where a value is not finite
-            const int32_t rr = cb * CW + r, node = node_of(a, tr, rr);
+            const int32_t rr = r0 + r, node = node_of(a, tr, rr);
             E *o = (E *)at.out + (int64_t)(seg.first + node) * at.ldo + (int64_t)(kvh * a.group + rr - node * a.group) * HD + d;
             if constexpr (BF) *(uint2 *)o = make_uint2(pack2(v[0] * inv, v[1] * inv), pack2(v[2] * inv, v[3] * inv));
             else *(f32x4_t *)o = v * inv;
@@ -316,23 +227,23 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
     };
-    if (LOCAL && cb * CW >= seg.m * a.group) return;       // no rows in this block
+    if (LOCAL && r0 >= seg.m * a.group) return;       // no rows in this block
 
     // ---- the pipeline: page ids two tiles ahead, K and V one ----
     // The loads of the next tile are issued whether there is one or not (behind the last tile they read the
     // pool's first page): a load under a condition would make every later wait a wait for all.
     int32_t i = wave;                                      // this wave's tile of the range
-    Pos p0 = seg, p1, p2;
+    TreePos p0 = seg, p1, p2;
     int32_t kid, vid;
     uint32_t ku, vu;
     uint64_t there;
-    if (i < count) p0 = advance(seg, i);
+    if (i < count) p0 = tree_next<TT>(a, tr, r0, seg, i);
     load_ids(p0, &kid, &vid);
     load_q(p0);
     load_mask(p0);
     reset();
     p1 = p0;
-    if (i + NW < count) p1 = advance(p0, NW);
+    if (i + NW < count) p1 = tree_next<TT>(a, tr, r0, p0, NW);
     there = to_units(p0, kid, vid, &ku, &vu);
     load_ids(p1, &kid, &vid);
     load_k(i < count ? ku : 0u);
@@ -347,7 +258,7 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
             first_piece = false;
             reset();
             begin = end;
-            do { seg = pos_of(seg.b + 1, 0); } while (seg.tiles == 0);
+            do { seg = tree_pos<TT>(a, tr, r0, seg.b + 1, 0); } while (seg.tiles == 0);
             from = 0;
             end = min(count, begin + seg.tiles);
         }
@@ -375,12 +286,12 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
         const int32_t s0 = p0.j * TT - (p0.n - p0.m);      // the tile's first token as a node; below 0: cached before
         uint32_t sees[NB];
 #pragma unroll
-        for (int x = 0; x < NB; ++x) sees[x] = window(s0, mlo[x], mhi[x]) & (uint32_t)there;
+        for (int x = 0; x < NB; ++x) sees[x] = (uint32_t)(mask_window(tr, s0, mlo[x], mhi[x]) & there);
         if (more && p1.b != p0.b) load_q(p1);
         uint32_t ku1, vu1;
         const uint64_t there1 = to_units(p1, kid, vid, &ku1, &vu1);
         p2 = p1;
-        if (i + 2 * NW < count) p2 = advance(p1, NW);
+        if (i + 2 * NW < count) p2 = tree_next<TT>(a, tr, r0, p1, NW);
         load_ids(p2, &kid, &vid);
         load_mask(p1);
         load_k(more ? ku1 : 0u);
@@ -403,9 +314,7 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
 #pragma unroll
                         for (int y = 0; y < (BF && HD == 64 ? 2 : 4); ++y) {
                             const uint32_t w = V[j][c][y];
-                            uint32_t out;
-                            if constexpr (BF) out = ((w & 0x7f80u) == 0x7f80u ? w & 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? w & 0xffff0000u : 0u);
-                            else out = (w & 0x7f800000u) == 0x7f800000u ? w : 0u;
+                            const uint32_t out = not_finite<E>(w);
                             if (out) odd = true;
                             V[j][c][y] = w ^ out;
                         }
@@ -500,19 +409,21 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
     }
 }
 
-// Put the pieces of a sequence (blockIdx.y) together, a wave to a row: out = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s.
-constexpr int JOIN_ROWS = 16;                              // rows a workgroup takes
-template <typename E, int HD, int TT>
-__global__ __launch_bounds__(256) void k_kv_tree_join(KvArgs a, KvAttend at, KvTreeSplit tr) {
+// Put the pieces of a sequence (blockIdx.y) together: out = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s.  A thread takes
+// four dims of a row; blockIdx.x: a K/V head and JOIN_ROWS of its rows, which lie in one block of CW.
+constexpr int JOIN_ROWS = 8;
+template <typename E, int HD>
+__global__ __launch_bounds__(256) void k_kv_tree_join(KvArgs a, KvAttend at, KvTreeSplit tr, int32_t tt, int32_t cw) {
     __shared__ int64_t sh[8];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int32_t b = blockIdx.y, first = blockIdx.x * JOIN_ROWS;
-    const SeqRows sq = tree_rows(a, tr.max_nodes, b);
-    const int32_t rows = sq.m * a.n_heads, nt = tree_tiles<TT>(sq);
+    const int32_t b = blockIdx.y, kvh = blockIdx.x % a.n_kv, first = blockIdx.x / a.n_kv * JOIN_ROWS, r0 = first / cw * cw;
+    const SeqRows sq = tree_rows(a, tr, b);
+    const int32_t rows = sq.m * a.group, nt = (sq.n + tt - 1) / tt;
     if (first >= rows) return;
     int64_t before = 0, total = 0;
     for (int32_t x = tid; x < a.n_seq; x += 256) {
-        const int32_t t = tree_tiles<TT>(tree_rows(a, tr.max_nodes, x));
+        const SeqRows s = tree_rows(a, tr, x);
+        const int32_t t = s.m * a.group > r0 ? (s.n + tt - 1) / tt : 0;
         total += t;
         before += x < b ? t : 0;
     }
@@ -533,38 +444,37 @@ __global__ __launch_bounds__(256) void k_kv_tree_join(KvArgs a, KvAttend at, KvT
         p = pieces_of(before, before + nt, ranges_of(total, tr.R));
         if (p.r0 == p.r1) return;                          // one range saw it whole
     }
-    constexpr int PER = HD / 64;
-    for (int32_t x = first + wave; x < min(first + JOIN_ROWS, rows); x += 4) {
-        const int32_t node = x / a.n_heads, head = x - node * a.n_heads, kvh = head / a.group, r = node * a.group + head - kvh * a.group;
-        float m = -INFINITY, l = 0.f, acc[PER];
+    for (int32_t x = tid; x < JOIN_ROWS * (HD / 4); x += 256) {
+        const int32_t r = first + x / (HD / 4), d = 4 * (x % (HD / 4));
+        if (r >= rows) break;
+        float m = -INFINITY, l = 0.f;
+        f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int32_t s = p.r0; s <= p.r1; s += 8) {        // eight loads at once
+            float2 ml[8];
+            f32x4_t v[8];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-        for (int32_t s = p.r0; s <= p.r1; s += 4) {        // four loads at once
-            float2 ml[4];
-            float v[4][PER];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 8; ++u) {
                 const int32_t su = min(s + u, p.r1);
                 const int64_t pl = (((int64_t)su * 2 + (su == p.r0 ? p.s0 : 0)) * a.n_kv + kvh) * tr.rows_ld + r;
                 ml[u] = tr.part_ml[pl];
-#pragma unroll
-                for (int i = 0; i < PER; ++i) v[u][i] = tr.part_o[pl * HD + 64 * i + lane];
+                v[u] = *(const f32x4_t *)(tr.part_o + pl * HD + d);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 8; ++u) {
                 if (s + u > p.r1) break;
                 const float mn = fmaxf(m, ml[u].x), ms = mn == -INFINITY ? 0.f : mn;
                 const float c = exp2_hw(m - ms), w = exp2_hw(ml[u].x - ms);
                 l = l * c + ml[u].y * w;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) acc[i] = acc[i] * c + v[u][i] * w;
+                acc = acc * c + v[u] * w;
                 m = mn;
             }
         }
-        E *out = (E *)at.out + (int64_t)(sq.first + node) * at.ldo + (int64_t)head * HD;
+        const int32_t node = node_of(a, tr, r);
+        E *o = (E *)at.out + (int64_t)(sq.first + node) * at.ldo + (int64_t)(kvh * a.group + r - node * a.group) * HD + d;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) from_f32(out + 64 * i + lane, l == 0.f ? 0.f : acc[i] * inv);
+        if (l == 0.f) acc = f32x4_t{0.f, 0.f, 0.f, 0.f};   // no weight: zero, also where a value is not finite
+        if constexpr (sizeof(E) == 2) *(uint2 *)o = make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
+        else *(f32x4_t *)o = acc * inv;
     }
 }
 
@@ -572,74 +482,71 @@ __global__ __launch_bounds__(256) void k_kv_tree_join(KvArgs a, KvAttend at, KvT
 namespace {
 
 struct TreePlan {
-    int32_t nb, ncb, R;
+    int32_t nb, cw, ncb, R, tt;   // nb: blocks of 16 rows; 0: the kernel for many rows
     bool local;
     size_t off_ml, total;
 };
 TreePlan tree_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int32_t max_nodes, int64_t max_len) {
     TreePlan p;
-    const int group = n_heads / n_kv, tt = dtype == LORA_F32 && hd > 64 ? 16 : 32;
-    const int64_t rows = (int64_t)max_nodes * group, tiles = (max_len + tt - 1) / tt * n_seq;
-    p.nb = rows <= 16 || hd == 256 ? 1 : rows <= 32 || dtype == LORA_F32 ? 2 : 4;
-    p.ncb = (int32_t)((rows + 16 * p.nb - 1) / (16 * p.nb));
-    const int64_t hu = (int64_t)n_kv * p.ncb;
-    // A workgroup a CU.
-    p.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, 256 / hu));
-    p.local = n_seq * hu <= 256 && max_len <= 1024;
-    // Room for at least 256 workgroups' pieces, so that what serves the largest call serves them all: the ranges of more
-    // rows are fewer.
-    const size_t pieces = 2 * (size_t)std::min<int64_t>(tiles * hu, std::max<int64_t>(256, hu)) * 16 * p.nb;
+    const int group = n_heads / n_kv;
+    const int64_t rows = (int64_t)max_nodes * group;
+    p.nb = rows <= 16 ? 1 : rows <= 32 && hd < 256 && dtype == LORA_F32 ? 2 : 0;
+    p.cw = p.nb ? 16 * p.nb : WIDE_ROWS;
+    p.tt = p.nb ? (dtype == LORA_F32 && hd > 64 ? 16 : 32) : (dtype == LORA_F32 ? 32 : 64);
+    const int64_t tiles = (max_len + p.tt - 1) / p.tt * n_seq;
+    p.ncb = (int32_t)((rows + p.cw - 1) / p.cw);
+    const int64_t hu = (int64_t)n_kv * p.ncb, slots = p.nb || hd == 256 ? 256 : 512;
+    // A workgroup a CU, two of the kernel for many rows.
+    p.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, slots / hu));
+    p.local = n_seq * hu <= slots && max_len <= (p.nb ? 1024 : 512);
+    // Room for at least `slots` workgroups' pieces, so that what serves the largest call serves them all: the ranges of
+    // more rows are fewer.
+    const size_t pieces = 2 * (size_t)std::min<int64_t>(tiles * hu, std::max<int64_t>(slots, hu)) * p.cw;
     p.off_ml = (pieces * hd * 4 + 255) & ~size_t(255);
     p.total = p.local ? 0 : p.off_ml + ((pieces * 8 + 255) & ~size_t(255));
     return p;
 }
 
 template <typename E, int HD, int NB>
-hipError_t run(const KvArgs &a, const KvAttend &at, const KvTreeArgs &ta, const TreePlan &pl, hipStream_t s) {
+hipError_t few(const KvArgs &a, const KvAttend &at, const KvTreeSplit &tr, bool local, hipStream_t s) {
     using C = TreeTile<E, HD, NB>;
-    KvTreeSplit tr{};
-    tr.R = pl.R;
-    tr.ncb = pl.ncb;
-    tr.rows_ld = pl.ncb * C::CW;
-    tr.max_nodes = ta.max_nodes;
-    tr.words = (ta.max_nodes + 63) / 64;
-    tr.group_magic = a.group == 1 ? 0 : (uint32_t)(((uint64_t(1) << 32) + a.group - 1) / a.group);
-    tr.mask = (const uint32_t *)ta.mask;
-    tr.part_o = (float *)at.ws;
-    tr.part_ml = (float2 *)((char *)at.ws + pl.off_ml);
-    const unsigned hu = (unsigned)(a.n_kv * pl.ncb);
+    const unsigned hu = (unsigned)(a.n_kv * tr.ncb);
     auto launch = [&](auto kernel, dim3 grid) {
         const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
-        if (e == hipSuccess) hipLaunchKernelGGL(kernel, grid, dim3(64 * C::NW), C::LDS, s, a, at, tr);
-        return e;
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(kernel, grid, dim3(64 * C::NW), C::LDS, s, a, at, tr);
+        return hipGetLastError();
     };
-    hipError_t e;
-    if (pl.local) {
-        e = launch(k_kv_tree<E, HD, NB, true>, dim3(hu, (unsigned)a.n_seq));
-    } else {
-        e = launch(k_kv_tree<E, HD, NB, false>, dim3(hu * pl.R));
-        if (e == hipSuccess)
-            hipLaunchKernelGGL((k_kv_tree_join<E, HD, C::TT>), dim3((unsigned)(((int64_t)ta.max_nodes * a.n_heads + JOIN_ROWS - 1) / JOIN_ROWS), (unsigned)a.n_seq),
-                               dim3(256), 0, s, a, at, tr);
-    }
-    return e == hipSuccess ? hipGetLastError() : e;
+    return local ? launch(k_kv_tree<E, HD, NB, true>, dim3(hu, (unsigned)a.n_seq)) : launch(k_kv_tree<E, HD, NB, false>, dim3(hu * tr.R));
 }
 
 template <typename E, int HD>
-hipError_t by_rows(const KvArgs &a, const KvAttend &at, const KvTreeArgs &ta, hipStream_t s) {
-    const TreePlan pl = tree_plan(sizeof(E) == 4 ? LORA_F32 : LORA_BF16, a.n_heads, a.n_kv, HD, a.n_seq, ta.max_nodes, a.cap);
-    if (pl.nb == 1) return run<E, HD, 1>(a, at, ta, pl, s);
-    if constexpr (HD <= 128)
-        if (pl.nb == 2) return run<E, HD, 2>(a, at, ta, pl, s);
-    if constexpr (sizeof(E) == 2 && HD <= 128)
-        if (pl.nb == 4) return run<E, HD, 4>(a, at, ta, pl, s);
-    return hipErrorInvalidValue;
+hipError_t run(int dtype, const KvArgs &a, const KvAttend &at, const KvTreeArgs &ta, hipStream_t s) {
+    const TreePlan pl = tree_plan(dtype, a.n_heads, a.n_kv, HD, a.n_seq, ta.max_nodes, a.cap);
+    KvTreeSplit tr{};
+    tr.R = pl.R;
+    tr.ncb = pl.ncb;
+    tr.rows_ld = pl.ncb * pl.cw;
+    tr.max_nodes = ta.max_nodes;
+    tr.words = (ta.max_nodes + 63) / 64;
+    tr.group_magic = a.group == 1 ? 0 : (uint32_t)(((uint64_t(1) << 32) + a.group - 1) / a.group);
+    tr.mask = ta.mask;
+    tr.part_o = (float *)at.ws;
+    tr.part_ml = (float2 *)((char *)at.ws + pl.off_ml);
+    hipError_t e = hipErrorInvalidValue;
+    if (pl.nb == 0) e = launch_tree_wide(dtype, a, at, tr, pl.local, s);
+    else if (pl.nb == 1) e = few<E, HD, 1>(a, at, tr, pl.local, s);
+    else if constexpr (HD < 256 && sizeof(E) == 4) e = few<E, HD, 2>(a, at, tr, pl.local, s);
+    if (e != hipSuccess || pl.local) return e;
+    const unsigned chunks = (unsigned)(((int64_t)ta.max_nodes * a.group + JOIN_ROWS - 1) / JOIN_ROWS);
+    hipLaunchKernelGGL((k_kv_tree_join<E, HD>), dim3(chunks * a.n_kv, (unsigned)a.n_seq), dim3(256), 0, s, a, at, tr, pl.tt, pl.cw);
+    return hipGetLastError();
 }
 
 template <typename E>
-hipError_t by_dim(const KvArgs &a, const KvAttend &at, const KvTreeArgs &ta, hipStream_t s) {
-    return a.head_dim == 64 ? by_rows<E, 64>(a, at, ta, s) : a.head_dim == 128 ? by_rows<E, 128>(a, at, ta, s)
-                                                                               : by_rows<E, 256>(a, at, ta, s);
+hipError_t by_dim(int dtype, const KvArgs &a, const KvAttend &at, const KvTreeArgs &ta, hipStream_t s) {
+    return a.head_dim == 64 ? run<E, 64>(dtype, a, at, ta, s) : a.head_dim == 128 ? run<E, 128>(dtype, a, at, ta, s)
+                                                                                  : run<E, 256>(dtype, a, at, ta, s);
 }
 
 }  // namespace
@@ -649,7 +556,7 @@ size_t kv_tree_ws_bytes(int dtype, const lora_kv_layout_t &l, int32_t n_seq, int
 }
 
 hipError_t launch_kv_tree(int dtype, const KvArgs &a, const KvAttend &at, const KvTreeArgs &ta, hipStream_t s) {
-    return dtype == LORA_F32 ? by_dim<float>(a, at, ta, s) : by_dim<uint16_t>(a, at, ta, s);
+    return dtype == LORA_F32 ? by_dim<float>(dtype, a, at, ta, s) : by_dim<uint16_t>(dtype, a, at, ta, s);
 }
 
 }  // namespace lorapool

@@ -1,0 +1,123 @@
+// What the kernels over trees of new tokens share: rows, the ranges of a block of rows, masks.
+//
+// The rows of a K/V head are its sequence's nodes times the query heads that share it, node by node: row r is head
+// r % group of node r / group.  A workgroup takes one block of CW rows, and one range of the tiles (TT tokens) of all the
+// sequences that have rows in that block.
+#pragma once
+
+#include "kv_ranges.h"
+
+namespace lorapool {
+
+struct KvTreeSplit {
+    int32_t R;                // ranges of a block's tiles, at most
+    int32_t ncb;              // blocks of CW rows of one K/V head
+    int32_t rows_ld;          // rows of a piece: ncb * CW
+    int32_t max_nodes, words; // 64-bit words of a row's mask
+    uint32_t group_magic;     // ceil(2^32 / group): r / group = mulhi(r, magic) for r < 2^18, group in 2..1024
+    const uint64_t *mask;     // [T][words]
+    float *part_o;            // [R][2][n_kv][rows_ld][head_dim]: slot 0 a range's first piece, 1 its last
+    float2 *part_ml;          // [R][2][n_kv][rows_ld]: maximum (base-2 logits), sum
+};
+
+// Sequence b's rows and length; more new tokens than a tree may have count as none.
+__device__ __forceinline__ SeqRows tree_rows(const KvArgs &a, const KvTreeSplit &tr, int32_t b) {
+    SeqRows s = seq_rows(a, b);
+    if (s.m > tr.max_nodes) {
+        s.m = 0;
+        s.err = DEV_ERR_LEN;
+    }
+    return s;
+}
+// Tiles of a sequence in the block of rows that begins at row r0.
+template <int TT>
+__device__ __forceinline__ int32_t tree_tiles(const KvArgs &a, const SeqRows &s, int32_t r0) {
+    return s.m * a.group > r0 ? (s.n + TT - 1) / TT : 0;
+}
+
+__device__ __forceinline__ int32_t node_of(const KvArgs &a, const KvTreeSplit &tr, int32_t r) {
+    return a.group == 1 ? r : (int32_t)__umulhi((uint32_t)r, tr.group_magic);
+}
+
+// Where a workgroup's range begins: sequence and tile of it; its tiles (0: there is no such range).  All threads call.
+struct TreeBegin { int32_t b, j, count; };
+template <int TT, int THREADS>
+__device__ __forceinline__ TreeBegin tree_begin(const KvArgs &a, const KvTreeSplit &tr, int32_t r0, int32_t range) {
+    __shared__ int64_t sum[THREADS / 64];
+    __shared__ int32_t sh_b, sh_j;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (tid == 0) sh_b = sh_j = 0;
+    const int32_t per = (a.n_seq + THREADS - 1) / THREADS, f0 = min(a.n_seq, tid * per), f1 = min(a.n_seq, f0 + per);
+    int64_t mine = 0;
+    for (int32_t b = f0; b < f1; ++b) mine += tree_tiles<TT>(a, tree_rows(a, tr, b), r0);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int64_t x = __shfl_up(incl, o, 64);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 63) sum[wave] = incl;
+    __syncthreads();
+    int64_t excl = incl - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 64; ++i) {
+        excl += i < wave ? sum[i] : 0;
+        total += sum[i];
+    }
+    const Ranges rg = ranges_of(total, tr.R);
+    if (range >= rg.R) return TreeBegin{0, 0, 0};
+    const int64_t s = rg.start(range);
+    if (mine > 0 && s >= excl && s < excl + mine) {        // one thread
+        int64_t at = excl;
+        int32_t b = f0;
+        for (; b < f1; ++b) {
+            const int32_t t = tree_tiles<TT>(a, tree_rows(a, tr, b), r0);
+            if (s < at + t) break;
+            at += t;
+        }
+        sh_b = b;
+        sh_j = (int32_t)(s - at);
+    }
+    __syncthreads();
+    return TreeBegin{uniform(sh_b), uniform(sh_j), uniform((int32_t)(rg.start(range + 1) - s))};
+}
+
+struct TreePos { int32_t b, j, n, m, first, tiles; };      // a sequence and a tile of it
+template <int TT>
+__device__ __forceinline__ TreePos tree_pos(const KvArgs &a, const KvTreeSplit &tr, int32_t r0, int32_t b, int32_t j) {
+    const SeqRows s = tree_rows(a, tr, b);
+    return TreePos{b, j, uniform(s.n), uniform(s.m), uniform(s.first), uniform(tree_tiles<TT>(a, s, r0))};
+}
+template <int TT>
+__device__ __forceinline__ TreePos tree_next(const KvArgs &a, const KvTreeSplit &tr, int32_t r0, TreePos p, int32_t by) {
+    p.j += by;                                             // only called while there is such a tile
+    while (p.j >= p.tiles && p.b + 1 < a.n_seq) p = tree_pos<TT>(a, tr, r0, p.b + 1, p.j - p.tiles);
+    return p;
+}
+
+// Two neighbouring words of a row's mask, from the one that the tile's first node lies in (s: the tile's first token as a
+// node; below 0: cached before), and which of the tile's up to 64 tokens, cached or nodes, the row sees by them.
+__device__ __forceinline__ void mask_at(const KvTreeSplit &tr, int32_t row, int32_t s, uint64_t *lo, uint64_t *hi) {
+    const uint64_t *w = tr.mask + (int64_t)row * tr.words;
+    const int32_t d = max(s, 0) >> 6;
+    *lo = w[min(d, tr.words - 1)];
+    *hi = w[min(d + 1, tr.words - 1)];
+}
+__device__ __forceinline__ uint64_t mask_window(const KvTreeSplit &tr, int32_t s, uint64_t lo, uint64_t hi) {
+    if (s <= -64) return ~0ull;
+    if (s < 0) return lo << -s | ((1ull << -s) - 1);
+    const int32_t k = s & 63;
+    return k == 0 ? lo : lo >> k | ((s >> 6) + 1 < tr.words ? hi << (64 - k) : 0);
+}
+
+template <typename E>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {   // the parts of a dword that are infinite or NaN, the rest zero
+    if constexpr (sizeof(E) == 4) return (w & 0x7f800000u) == 0x7f800000u ? w : 0u;
+    else return ((w & 0x7f80u) == 0x7f80u ? w & 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? w & 0xffff0000u : 0u);
+}
+
+// More than 32 rows (k_kv_tree_wide.hip)
+constexpr int WIDE_ROWS = 128;
+hipError_t launch_tree_wide(int dtype, const KvArgs &a, const KvAttend &at, const KvTreeSplit &tr, bool local, hipStream_t s);
+
+}  // namespace lorapool

@@ -74,9 +74,11 @@ class Trees:
         return self.pool.kv_attend_tree(self.layout, self.q, self.d_table, self.d_lens, self.d_start, self.mask(), **{**args, **kw})
 
     def ref(self):
-        # weights go into the product with V as two bfloat16 numbers (kv_ref.ROUNDED, one token), float32 as they are
+        # bfloat16 weights in the product with V: two numbers, as one token's, up to 16 rows (nodes times query heads) of a
+        # K/V head; of more rows rounded once, as a chunk's (kv_ref.ROUNDED).  float32 as they are
+        rows = self.nodes * (self.layout.n_heads // self.layout.n_kv_heads)
         return draft_ref.attend(self.pool.pages, self.layout, self.q, self.table, self.lens, self.starts, self.bits, self.scale,
-                                kv_ref.ROUNDED[self.dt, False])
+                                kv_ref.ROUNDED[self.dt, rows > 16])
 
     def errors(self):
         return rg.lora_check_device_errors(self.pool.handle, check=False)
