@@ -19,6 +19,7 @@ struct TreeTile {
     static constexpr bool BF = sizeof(E) == 2;
     static constexpr int TT = BF || HD == 64 ? 32 : 16;    // tokens per step
     static constexpr int WAVES = HD == 256 || (!BF && HD == 128 && NB == 2) ? 1 : 2;   // a SIMD holds: registers
+    static constexpr bool AHEAD = NB == 1;                 // V of the next tile has registers of its own
     static constexpr int NW = 4 * WAVES;                   // waves of a workgroup; one workgroup a CU
     static constexpr int CW = 16 * NB;
     static constexpr int LDW = HD + 4;                     // floats between rows in LDS: columns in other banks
@@ -36,51 +37,62 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
     constexpr int VC = BF ? (HD == 64 ? 1 : HD / 128) : HD / 64;   // 16-byte (bf16, 64: 8-byte) parts of each
     constexpr int NA = HD / 16;                            // accumulators: 16 dims x 16 rows each
     constexpr int W = BF && HD >= 128 ? 8 : 4;             // consecutive dims of one row of the accumulators
-    extern __shared__ __align__(16) float sh_o[];          // [NW][CW][LDW], then maxima and sums [NW][CW]
-    float2 *sh_s = (float2 *)(sh_o + NW * CW * LDW);
+    constexpr int SLOTS = LOCAL ? 1 : 2;
+    extern __shared__ __align__(16) float sh_o[];          // [NW][SLOTS][CW][LDW], then maxima and sums [NW][SLOTS][CW]
+    float2 *sh_s = (float2 *)(sh_o + NW * SLOTS * CW * LDW);
+    __shared__ int32_t piece_b[NW * SLOTS], piece_at[NW * SLOTS];   // of each: its sequence, or -1, and where in the range that begins
+    __shared__ TreeBegin parts[NW];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
 
-    const int32_t kvh = blockIdx.x % a.n_kv, rest = blockIdx.x / a.n_kv, r0 = rest % tr.ncb * CW, range = rest / tr.ncb;
+    // LOCAL: all waves take one head.  Else `hw` neighbouring ones, so that neighbouring pieces of a page are read at the same
+    // time, and each head's waves a part of the range each.
+    const int32_t hw = LOCAL ? 1 : tr.hw, head0 = blockIdx.x % (a.n_kv / hw) * hw, rest = blockIdx.x / (a.n_kv / hw);
+    const int32_t kvh = head0 + wave % hw, part = wave / hw, n_parts = NW / hw, r0 = rest % tr.ncb * CW, range = rest / tr.ncb;
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         int bits = 0;
         for (int32_t b = tid; b < a.n_seq; b += THREADS) bits |= tree_rows(a, tr, b).err;
         record(a, bits);
     }
-    TreeBegin w;
+    int32_t total, begin, count, from = 0, b0 = blockIdx.y, range_b = b0;
     if constexpr (LOCAL) {
-        w = TreeBegin{(int32_t)blockIdx.y, 0, tree_tiles<TT>(a, tree_rows(a, tr, blockIdx.y), r0)};
+        total = count = tree_tiles<TT>(a, tree_rows_scalar(a, tr, b0), r0);
+        begin = 0;
     } else {
-        w = tree_begin<TT, THREADS>(a, tr, r0, range);
-        if (w.count == 0) return;
+        total = tree_begin<TT, THREADS>(a, tr, r0, range, n_parts, parts);
+        if (total == 0) return;
+        range_b = uniform(parts[0].b);
+        b0 = uniform(parts[part].b);
+        from = uniform(parts[part].j);
+        begin = uniform(part_of(total, part, n_parts));    // this wave's tiles [begin, count) of the range
+        count = uniform(part_of(total, part + 1, n_parts));
     }
-    const int32_t count = w.count;
 
     const int64_t head_bytes = (int64_t)kvh * HD * sizeof(E);
     const uint32_t page_units = (uint32_t)(a.page_bytes >> 7), tok_units = (uint32_t)(a.tok_bytes >> 7);
     const float scale2 = at.scale * 1.4426950408889634f;
 
-    // page ids of a tile's tokens, each lane those of token lane % TT; -1 behind the sequence's end
+    // page ids of a tile's tokens, each lane those of token lane % TT
     auto load_ids = [&](const TreePos &p, int32_t *kid, int32_t *vid) {
         const int32_t t = p.j * TT + (lane & (TT - 1));
         int32_t e, slot;
         page_of(a, t, &e, &slot);
-        const int32_t *row = a.table + (int64_t)p.b * 2 * a.max_pages + e;
-        *kid = *vid = -1;
-        if (t < p.n) { *kid = row[0]; *vid = row[a.max_pages]; }
+        const int32_t *row = a.table + (int64_t)p.b * 2 * a.max_pages + (t < p.n ? e : 0);   // (there is a first entry)
+        *kid = row[0];
+        *vid = row[a.max_pages];
     };
     int bad = 0;
     auto to_units = [&](const TreePos &p, int32_t kid, int32_t vid, uint32_t *ku, uint32_t *vu) -> uint64_t {
         const int32_t t = p.j * TT + (lane & (TT - 1));
         int32_t e, slot;
         page_of(a, t, &e, &slot);
-        const bool ok = kid >= 0 && vid >= 0 && kid < a.num_pages && vid < a.num_pages;
+        const bool ok = t < p.n && kid >= 0 && vid >= 0 && kid < a.num_pages && vid < a.num_pages;
         if (t < p.n && !ok) bad = DEV_ERR_PAGE;
         *ku = ok ? (uint32_t)kid * page_units + (uint32_t)slot * tok_units : 0u;
         *vu = ok ? (uint32_t)vid * page_units + (uint32_t)slot * tok_units : 0u;
         return __ballot(ok);
     };
     const char *base = a.pages + head_bytes;
-    u32x4_t K[NS][KS], V[NV][VC];
+    u32x4_t K[NS][KS], V0[NV][VC], V1[NV][VC];
     auto load_k = [&](uint32_t ku) {
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
@@ -91,7 +103,7 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
         }
     };
     auto v_token = [&](int j) { return BF ? 32 * (j >> 3) + 16 * ((j >> 2) & 1) + 4 * g + (j & 3) : 16 * (j >> 2) + 4 * g + (j & 3); };
-    auto load_v = [&](uint32_t vu) {
+    auto load_v = [&](u32x4_t (&V)[NV][VC], uint32_t vu) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const uint32_t u = __shfl(vu, v_token(j), 64);
@@ -142,18 +154,19 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
         odd = false;
     };
 
-    // The segment: what the range has of one sequence, its tiles [base, end) of the range, the sequence's from `from` on.
-    TreePos seg = tree_pos<TT>(a, tr, r0, w.b, w.j);
-    int32_t from = w.j, begin = 0, end = min(count, seg.tiles - from);
-    bool first_piece = true;
+    // The segment: what the wave has of one sequence, its tiles [begin, end) of the range, the sequence's from `from` on.
+    TreePos seg = tree_pos<TT>(a, tr, r0, b0, from);
+    if (LOCAL && r0 >= seg.m * a.group) return;            // no rows in this block
+    int32_t end = min(count, begin + seg.tiles - from);
+    if (lane < SLOTS) piece_b[wave * SLOTS + lane] = -1;
     // Infinities and NaN of nodes' V, which the products leave out, to the rows that see them: into this wave's sums in LDS.
-    auto put_odd = [&]() {
+    auto put_odd = [&](float *so) {
         const int32_t old = seg.n - seg.m;
         const int32_t *row = a.table + (int64_t)seg.b * 2 * a.max_pages;
 #pragma unroll 1
         for (int32_t t = old; t < seg.n; ++t) {
-            const int32_t i = begin + t / TT - from, j = t - old;
-            if (t / TT < from || i >= end || i % NW != wave || token_offset(a, row, t) < 0) continue;
+            const int32_t j = t - old;
+            if (t / TT < from || (LOCAL ? t / TT % NW != wave : begin + t / TT - from >= end) || token_offset(a, row, t) < 0) continue;
             const int64_t off = token_offset(a, row + a.max_pages, t);
             if (off < 0) continue;
             const E *v = (const E *)(base + off);
@@ -166,18 +179,33 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
                     const int32_t r = r0 + c;
                     if (r >= seg.m * a.group) break;
                     const uint64_t *w = tr.mask + (int64_t)(seg.first + node_of(a, tr, r)) * tr.words;
-                    if (w[j >> 6] >> (j & 63) & 1) sh_o[(wave * CW + c) * LDW + d] += y;
+                    if (w[j >> 6] >> (j & 63) & 1) so[c * LDW + d] += y;
                 }
             }
         }
     };
-    // Join the waves' sums of the segment; out if the range saw the sequence whole, else to the workspace.
+    auto out_at = [&](int32_t first, int32_t kvh, int32_t r, int32_t d) {
+        const int32_t node = node_of(a, tr, r0 + r);
+        return (E *)at.out + (int64_t)(first + node) * at.ldo + (int64_t)(kvh * a.group + r0 + r - node * a.group) * HD + d;
+    };
+    auto put_out = [&](E *o, f32x4_t v, float sum) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (sum == 0.f) v = f32x4_t{0.f, 0.f, 0.f, 0.f};   // no weight: zero, also where a value is not finite
+        if constexpr (BF) *(uint2 *)o = make_uint2(pack2(v[0] * inv, v[1] * inv), pack2(v[2] * inv, v[3] * inv));
+        else *(f32x4_t *)o = v * inv;
+    };
+    // The segment's sums to LDS, and out if the wave saw the sequence whole: a wave waits for no other while it has tiles.
+    bool first_piece = true;
     auto flush = [&]() {
+        const bool whole = !LOCAL && from == 0 && end - begin == seg.tiles;
+        const int slot = wave * SLOTS + (LOCAL || (first_piece && !whole) ? 0 : 1);
+        float *so = sh_o + slot * CW * LDW;
+        float2 *ss = sh_s + slot * CW;
 #pragma unroll
         for (int x = 0; x < NB; ++x) {
             float L = l[x] + __shfl_xor(l[x], 16, 64);
             L += __shfl_xor(L, 32, 64);
-            float *o = sh_o + (wave * CW + 16 * x + col) * LDW;
+            float *o = so + (16 * x + col) * LDW;
 #pragma unroll
             for (int c = 0; c < NA / W; ++c)
 #pragma unroll
@@ -186,82 +214,49 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
                     for (int i = 0; i < W; i += 4)
                         *(f32x4_t *)(o + 16 * W * c + W * (4 * g + r) + i) =
                             f32x4_t{acc[x][W * c + i][r], acc[x][W * c + i + 1][r], acc[x][W * c + i + 2][r], acc[x][W * c + i + 3][r]};
-            if (g == 0) sh_s[wave * CW + 16 * x + col] = make_float2(m[x], L);
+            if (g == 0) ss[16 * x + col] = make_float2(m[x], L);
         }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         if (__any(odd)) {
+            put_odd(so);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            put_odd();
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        const bool whole = from == 0 && end - begin == seg.tiles;
-        const int32_t rows = min(CW, seg.m * a.group - r0);
-        const int64_t piece = (((int64_t)range * 2 + (first_piece ? 0 : 1)) * a.n_kv + kvh) * tr.rows_ld + r0;
-        for (int32_t x = tid; x < rows * (HD / 4); x += THREADS) {
-            const int32_t r = x / (HD / 4), d = 4 * (x % (HD / 4));
-            float M = -INFINITY, sum = 0.f;
-            f32x4_t v = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int w = 0; w < NW; ++w) M = fmaxf(M, sh_s[w * CW + r].x);
-            const float Ms = M == -INFINITY ? 0.f : M;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float2 ml = sh_s[w * CW + r];
-                const float f = exp2_hw(ml.x - Ms);
-                sum += ml.y * f;
-                // (a wave that saw none of the row's tokens holds zeros, or infinities of nodes whose weights are zero)
-                v += *(const f32x4_t *)(sh_o + (w * CW + r) * LDW + d) * f;
+        if (whole) {
+            const int32_t rows = min(CW, seg.m * a.group - r0);
+            for (int32_t x = lane; x < rows * (HD / 4); x += 64) {
+                const int32_t r = x / (HD / 4), d = 4 * (x % (HD / 4));
+                put_out(out_at(seg.first, kvh, r, d), *(const f32x4_t *)(so + r * LDW + d), ss[r].y);
             }
-            if (!whole) {
-                if (d == 0) tr.part_ml[piece + r] = make_float2(M, sum);
-                *(f32x4_t *)(tr.part_o + (piece + r) * HD + d) = v;
-                continue;
-            }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            if (sum == 0.f) v = f32x4_t{0.f, 0.f, 0.f, 0.f};   // no weight: zero, also where a value is not finite
-            const int32_t rr = r0 + r, node = node_of(a, tr, rr);
-            E *o = (E *)at.out + (int64_t)(seg.first + node) * at.ldo + (int64_t)(kvh * a.group + rr - node * a.group) * HD + d;
-            if constexpr (BF) *(uint2 *)o = make_uint2(pack2(v[0] * inv, v[1] * inv), pack2(v[2] * inv, v[3] * inv));
-            else *(f32x4_t *)o = v * inv;
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        } else if (lane == 0) {
+            piece_b[slot] = seg.b;
+            piece_at[slot] = begin - from;
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
     };
-    if (LOCAL && r0 >= seg.m * a.group) return;       // no rows in this block
 
     // ---- the pipeline: page ids two tiles ahead, K and V one ----
     // The loads of the next tile are issued whether there is one or not (behind the last tile they read the
     // pool's first page): a load under a condition would make every later wait a wait for all.
-    int32_t i = wave;                                      // this wave's tile of the range
+    constexpr int STEP = LOCAL ? NW : 1;                   // whole sequences: every NW-th tile
+    int32_t i = begin + (LOCAL ? wave : 0);                // tile of the range
     TreePos p0 = seg, p1, p2;
+    if constexpr (LOCAL) p0.j = wave;
     int32_t kid, vid;
     uint32_t ku, vu;
     uint64_t there;
-    if (i < count) p0 = tree_next<TT>(a, tr, r0, seg, i);
     load_ids(p0, &kid, &vid);
     load_q(p0);
     load_mask(p0);
     reset();
     p1 = p0;
-    if (i + NW < count) p1 = tree_next<TT>(a, tr, r0, p0, NW);
+    if (i + STEP < count) p1 = tree_next<TT>(a, tr, r0, p0, STEP);
     there = to_units(p0, kid, vid, &ku, &vu);
     load_ids(p1, &kid, &vid);
+    __builtin_amdgcn_sched_barrier(0);                     // loads in the order in which they are waited for
     load_k(i < count ? ku : 0u);
-    load_v(i < count ? vu : 0u);
-    for (;;) {
-        while (i >= end) {                                 // this wave has no more of the segment
-            flush();
-            if (end >= count) {
-                if (bad) record(a, bad);
-                return;
-            }
-            first_piece = false;
-            reset();
-            begin = end;
-            do { seg = tree_pos<TT>(a, tr, r0, seg.b + 1, 0); } while (seg.tiles == 0);
-            from = 0;
-            end = min(count, begin + seg.tiles);
-        }
+    __builtin_amdgcn_sched_barrier(0);
+    load_v(V0, i < count ? vu : 0u);
+    auto step = [&](u32x4_t (&V)[NV][VC], u32x4_t (&Vn)[NV][VC]) {
         // logits: rows are tokens, columns the query rows
         f32x4_t S[NB][NS];
 #pragma unroll
@@ -282,7 +277,7 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
                 }
             }
         __builtin_amdgcn_sched_barrier(0);
-        const bool more = i + NW < count;
+        const bool more = i + STEP < count;
         const int32_t s0 = p0.j * TT - (p0.n - p0.m);      // the tile's first token as a node; below 0: cached before
         uint32_t sees[NB];
 #pragma unroll
@@ -291,10 +286,13 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
         uint32_t ku1, vu1;
         const uint64_t there1 = to_units(p1, kid, vid, &ku1, &vu1);
         p2 = p1;
-        if (i + 2 * NW < count) p2 = tree_next<TT>(a, tr, r0, p1, NW);
+        if (i + 2 * STEP < count) p2 = tree_next<TT>(a, tr, r0, p1, STEP);
         load_ids(p2, &kid, &vid);
         load_mask(p1);
+        __builtin_amdgcn_sched_barrier(0);
         load_k(more ? ku1 : 0u);
+        __builtin_amdgcn_sched_barrier(0);
+        if (C::AHEAD) load_v(Vn, more ? vu1 : 0u);
         __builtin_amdgcn_sched_barrier(0);
         const bool nodes = s0 + TT > 0;
         const bool full = (~there & ((1ull << TT) - 1)) == 0;
@@ -401,11 +399,91 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
                                                                                         acc[b][4 * c + e], 0, 0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
-        load_v(more ? vu1 : 0u);
+        if (!C::AHEAD) load_v(V, more ? vu1 : 0u);
         p0 = p1;
         p1 = p2;
         there = there1;
-        i += NW;
+        i += STEP;
+        if (i >= end) {
+            flush();
+            if (i < count) {
+                first_piece = false;
+                reset();
+                begin = i;
+                seg = p0;
+                from = 0;
+                end = min(count, begin + seg.tiles);
+            }
+        }
+    };
+    while (i < count) {
+        step(V0, V1);
+        if (C::AHEAD && i < count) step(V1, V0);
+    }
+    if (bad) record(a, bad);
+    // ---- the waves' sums of the sequence, or of those that no wave saw whole, put together ----
+    __syncthreads();
+    const int32_t mine = lane < NW * SLOTS ? piece_b[lane] : -1;
+    auto held = [&](int32_t y) { return __builtin_amdgcn_readlane(mine, y); };   // the sequence of piece y, or -1
+    auto join = [&](int32_t x, int32_t b, int32_t y0, int32_t y1, int32_t by, f32x4_t *v, float *sum) {   // of y0, y0 + by, ... < y1
+        const int32_t r = x / (HD / 4), d = 4 * (x % (HD / 4));
+        float M = -INFINITY;
+        for (int32_t y = y0; y < y1; y += by)
+            if (held(y) == b) M = fmaxf(M, sh_s[y * CW + r].x);
+        const float Ms = M == -INFINITY ? 0.f : M;
+        *sum = 0.f;
+        *v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int32_t y = y0; y < y1; y += by)
+            if (held(y) == b) {
+                const float2 ml = sh_s[y * CW + r];
+                const float f = exp2_hw(ml.x - Ms);
+                *sum += ml.y * f;
+                // (a wave that saw none of the row's tokens holds zeros, or infinities of nodes whose weights are zero)
+                *v += *(const f32x4_t *)(sh_o + (y * CW + r) * LDW + d) * f;
+            }
+        return M;
+    };
+    f32x4_t v;
+    float sum;
+    if constexpr (LOCAL) {
+        const int32_t rows = min(CW, seg.m * a.group - r0);
+        for (int32_t x = tid; x < rows * (HD / 4); x += THREADS) {
+            join(x, seg.b, 0, NW, 1, &v, &sum);
+            put_out(out_at(seg.first, kvh, x / (HD / 4), 4 * (x % (HD / 4))), v, sum);
+        }
+        return;
+    }
+    // A sequence is put together by the wave that holds its first piece; the others lie in the first slots of its head's next
+    // waves (some of which may have no piece: no tiles, or whole sequences alone).
+    for (int s = 0; s < SLOTS; ++s) {
+        const int32_t y0 = wave * SLOTS + s, b = held(y0);
+        if (b < 0) continue;
+        if (s == 0) {                                      // not the first, if a wave before ended inside the sequence
+            int32_t w = wave - hw;
+            while (w >= 0 && held(w * SLOTS) < 0 && held(w * SLOTS + 1) < 0) w -= hw;
+            if (w >= 0 && (held(w * SLOTS) == b || held(w * SLOTS + 1) == b)) continue;
+        }
+        const int32_t at0 = uniform(piece_at[y0]);
+        const SeqRows sq = tree_rows_scalar(a, tr, b);
+        const int32_t rows = min(CW, sq.m * a.group - r0), tiles = tree_tiles<TT>(a, sq, r0);
+        const bool whole = at0 >= 0 && at0 + tiles <= total;
+        const int64_t piece = (((int64_t)range * 2 + (b == range_b ? 0 : 1)) * a.n_kv + kvh) * tr.rows_ld + r0;
+        for (int32_t x = lane; x < rows * (HD / 4); x += 64) {
+            const int32_t r = x / (HD / 4), d = 4 * (x % (HD / 4));
+            f32x4_t v1;
+            float sum1;
+            const float M1 = join(x, b, (wave + hw) * SLOTS, NW * SLOTS, hw * SLOTS, &v1, &sum1);
+            const float2 ml = sh_s[y0 * CW + r];
+            const float M = fmaxf(M1, ml.x), Ms = M == -INFINITY ? 0.f : M, f = exp2_hw(ml.x - Ms), f1 = exp2_hw(M1 - Ms);
+            sum = ml.y * f + sum1 * f1;
+            v = *(const f32x4_t *)(sh_o + (y0 * CW + r) * LDW + d) * f + v1 * f1;
+            if (whole) {
+                put_out(out_at(sq.first, kvh, r, d), v, sum);
+            } else {
+                if (d == 0) tr.part_ml[piece + r] = make_float2(M, sum);
+                *(f32x4_t *)(tr.part_o + (piece + r) * HD + d) = v;
+            }
+        }
     }
 }
 
@@ -482,7 +560,7 @@ __global__ __launch_bounds__(256) void k_kv_tree_join(KvArgs a, KvAttend at, KvT
 namespace {
 
 struct TreePlan {
-    int32_t nb, cw, ncb, R, tt;   // nb: blocks of 16 rows; 0: the kernel for many rows
+    int32_t nb, cw, ncb, R, tt, hw;   // nb: blocks of 16 rows; 0: the kernel for many rows
     bool local;
     size_t off_ml, total;
 };
@@ -497,11 +575,12 @@ TreePlan tree_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int3
     p.ncb = (int32_t)((rows + p.cw - 1) / p.cw);
     const int64_t hu = (int64_t)n_kv * p.ncb, slots = p.nb || hd == 256 ? 256 : 512;
     // A workgroup a CU, two of the kernel for many rows.
-    p.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, slots / hu));
+    p.hw = p.nb == 0 ? 1 : n_kv % 4 == 0 ? 4 : n_kv % 2 == 0 ? 2 : 1;
+    p.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, slots * p.hw / hu));
     p.local = n_seq * hu <= slots && max_len <= (p.nb ? 1024 : 512);
     // Room for at least `slots` workgroups' pieces, so that what serves the largest call serves them all: the ranges of
     // more rows are fewer.
-    const size_t pieces = 2 * (size_t)std::min<int64_t>(tiles * hu, std::max<int64_t>(slots, hu)) * p.cw;
+    const size_t pieces = 2 * (size_t)std::min<int64_t>(tiles * hu, std::max<int64_t>(slots * p.hw, hu)) * p.cw;
     p.off_ml = (pieces * hd * 4 + 255) & ~size_t(255);
     p.total = p.local ? 0 : p.off_ml + ((pieces * 8 + 255) & ~size_t(255));
     return p;
@@ -512,12 +591,13 @@ hipError_t few(const KvArgs &a, const KvAttend &at, const KvTreeSplit &tr, bool 
     using C = TreeTile<E, HD, NB>;
     const unsigned hu = (unsigned)(a.n_kv * tr.ncb);
     auto launch = [&](auto kernel, dim3 grid) {
-        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+        const int lds = (local ? 1 : 2) * C::LDS;
+        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(kernel, grid, dim3(64 * C::NW), C::LDS, s, a, at, tr);
+        hipLaunchKernelGGL(kernel, grid, dim3(64 * C::NW), lds, s, a, at, tr);
         return hipGetLastError();
     };
-    return local ? launch(k_kv_tree<E, HD, NB, true>, dim3(hu, (unsigned)a.n_seq)) : launch(k_kv_tree<E, HD, NB, false>, dim3(hu * tr.R));
+    return local ? launch(k_kv_tree<E, HD, NB, true>, dim3(hu, (unsigned)a.n_seq)) : launch(k_kv_tree<E, HD, NB, false>, dim3(hu / tr.hw * tr.R));
 }
 
 template <typename E, int HD>
@@ -525,6 +605,7 @@ hipError_t run(int dtype, const KvArgs &a, const KvAttend &at, const KvTreeArgs 
     const TreePlan pl = tree_plan(dtype, a.n_heads, a.n_kv, HD, a.n_seq, ta.max_nodes, a.cap);
     KvTreeSplit tr{};
     tr.R = pl.R;
+    tr.hw = pl.hw;
     tr.ncb = pl.ncb;
     tr.rows_ld = pl.ncb * pl.cw;
     tr.max_nodes = ta.max_nodes;

@@ -27,17 +27,19 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_tree_wide(KvA
         for (int32_t b = tid; b < a.n_seq; b += 256) bits |= tree_rows(a, tr, b).err;
         record(a, bits);
     }
-    TreeBegin w;
+    __shared__ TreeBegin w;
+    int32_t count, from = 0, b0 = blockIdx.y;
     if constexpr (LOCAL) {
-        w = TreeBegin{(int32_t)blockIdx.y, 0, tree_tiles<NT>(a, tree_rows(a, tr, blockIdx.y), r0)};
+        count = tree_tiles<NT>(a, tree_rows(a, tr, b0), r0);
     } else {
-        w = tree_begin<NT, 256>(a, tr, r0, range);
-        if (w.count == 0) return;
+        count = tree_begin<NT, 256>(a, tr, r0, range, 1, &w);
+        if (count == 0) return;
+        b0 = uniform(w.b);
+        from = uniform(w.j);
     }
-    const int32_t count = w.count;
-    TreePos seg = tree_pos<NT>(a, tr, r0, w.b, w.j);
+    TreePos seg = tree_pos<NT>(a, tr, r0, b0, from);
     if (LOCAL && r0 >= seg.m * a.group) return;
-    int32_t from = w.j, begin = 0, end = min(count, seg.tiles - from);
+    int32_t begin = 0, end = min(count, seg.tiles - from);
     bool first_piece = true;
 
     const char *base = a.pages + (int64_t)kvh * RB;
@@ -55,15 +57,15 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_tree_wide(KvA
         const int32_t t = p.j * NT + (lane & (NT - 1));
         int32_t e, slot;
         page_of(a, t, &e, &slot);
-        const int32_t *row = a.table + (int64_t)p.b * 2 * a.max_pages + e;
-        *kid = *vid = -1;
-        if (t < p.n) { *kid = row[0]; *vid = row[a.max_pages]; }
+        const int32_t *row = a.table + (int64_t)p.b * 2 * a.max_pages + (t < p.n ? e : 0);   // (there is a first entry)
+        *kid = row[0];
+        *vid = row[a.max_pages];
     };
     auto to_units = [&](const TreePos &p, int32_t kid, int32_t vid, uint32_t *ku, uint32_t *vu) -> uint64_t {
         const int32_t t = p.j * NT + (lane & (NT - 1));
         int32_t e, slot;
         page_of(a, t, &e, &slot);
-        const bool ok = kid >= 0 && vid >= 0 && kid < a.num_pages && vid < a.num_pages;
+        const bool ok = t < p.n && kid >= 0 && vid >= 0 && kid < a.num_pages && vid < a.num_pages;
         if (t < p.n && !ok) bad = DEV_ERR_PAGE;
         *ku = ok ? (uint32_t)kid * page_units + (uint32_t)slot * tok_units : 0u;
         *vu = ok ? (uint32_t)vid * page_units + (uint32_t)slot * tok_units : 0u;

@@ -16,24 +16,19 @@ struct SeqRows {
 
 // Sequence b's rows and length.  A range outside [0, T] counts as empty; a length below 0, above the
 // capacity or (when not 0) below the number of new rows counts as 0.
-__device__ __forceinline__ SeqRows seq_rows(const KvArgs &a, int32_t b) {
+__device__ __forceinline__ SeqRows seq_rows(const KvArgs &a, int32_t s0, int32_t s1, int32_t n) {
     SeqRows s;
-    s.err = 0;
-    if (a.q_start) {
-        const int32_t s0 = a.q_start[b], s1 = a.q_start[b + 1];
-        const bool bad = s0 < 0 || s1 < s0 || s1 > a.T;
-        s.first = bad ? 0 : s0;
-        s.m = bad ? 0 : s1 - s0;
-        s.err = bad ? DEV_ERR_LEN : 0;
-    } else {
-        s.first = b;
-        s.m = 1;
-    }
-    const int32_t n = a.lens[b];
-    const bool bad = n < 0 || n > a.cap || (n > 0 && n < s.m);
+    bool bad = s0 < 0 || s1 < s0 || s1 > a.T;
+    s.first = bad ? 0 : s0;
+    s.m = bad ? 0 : s1 - s0;
+    s.err = bad ? DEV_ERR_LEN : 0;
+    bad = n < 0 || n > a.cap || (n > 0 && n < s.m);
     s.n = bad ? 0 : n;
     if (bad) s.err = DEV_ERR_LEN;
     return s;
+}
+__device__ __forceinline__ SeqRows seq_rows(const KvArgs &a, int32_t b) {
+    return a.q_start ? seq_rows(a, a.q_start[b], a.q_start[b + 1], a.lens[b]) : seq_rows(a, b, b + 1, a.lens[b]);
 }
 
 // Page index of token t, and t's place in that page.

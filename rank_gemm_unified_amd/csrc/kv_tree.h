@@ -11,6 +11,7 @@ namespace lorapool {
 
 struct KvTreeSplit {
     int32_t R;                // ranges of a block's tiles, at most
+    int32_t hw;               // heads of a workgroup's waves
     int32_t ncb;              // blocks of CW rows of one K/V head
     int32_t rows_ld;          // rows of a piece: ncb * CW
     int32_t max_nodes, words; // 64-bit words of a row's mask
@@ -21,13 +22,21 @@ struct KvTreeSplit {
 };
 
 // Sequence b's rows and length; more new tokens than a tree may have count as none.
-__device__ __forceinline__ SeqRows tree_rows(const KvArgs &a, const KvTreeSplit &tr, int32_t b) {
-    SeqRows s = seq_rows(a, b);
+__device__ __forceinline__ SeqRows tree_rows(const KvTreeSplit &tr, SeqRows s) {
     if (s.m > tr.max_nodes) {
         s.m = 0;
         s.err = DEV_ERR_LEN;
     }
     return s;
+}
+__device__ __forceinline__ SeqRows tree_rows(const KvArgs &a, const KvTreeSplit &tr, int32_t b) { return tree_rows(tr, seq_rows(a, b)); }
+
+// The same for a sequence that is the same in every lane, by scalar loads: a vector load amid those of K and V would have
+// to wait for all of them.
+typedef const __attribute__((address_space(4))) int32_t *scalar_ptr;
+__device__ __forceinline__ SeqRows tree_rows_scalar(const KvArgs &a, const KvTreeSplit &tr, int32_t b) {
+    const scalar_ptr starts = (scalar_ptr)(uintptr_t)a.q_start, lens = (scalar_ptr)(uintptr_t)a.lens;
+    return tree_rows(tr, seq_rows(a, starts[b], starts[b + 1], lens[b]));
 }
 // Tiles of a sequence in the block of rows that begins at row r0.
 template <int TT>
@@ -39,14 +48,14 @@ __device__ __forceinline__ int32_t node_of(const KvArgs &a, const KvTreeSplit &t
     return a.group == 1 ? r : (int32_t)__umulhi((uint32_t)r, tr.group_magic);
 }
 
-// Where a workgroup's range begins: sequence and tile of it; its tiles (0: there is no such range).  All threads call.
-struct TreeBegin { int32_t b, j, count; };
+// Where `n` equal parts of a range begin: sequence and tile of it.  Returns the range's tiles (0: there is no such range).
+// All threads call.
+struct TreeBegin { int32_t b, j; };
+__device__ __forceinline__ int32_t part_of(int32_t count, int32_t i, int32_t n) { return (int32_t)(((int64_t)count * i) / n); }
 template <int TT, int THREADS>
-__device__ __forceinline__ TreeBegin tree_begin(const KvArgs &a, const KvTreeSplit &tr, int32_t r0, int32_t range) {
+__device__ __forceinline__ int32_t tree_begin(const KvArgs &a, const KvTreeSplit &tr, int32_t r0, int32_t range, int32_t n, TreeBegin *at) {
     __shared__ int64_t sum[THREADS / 64];
-    __shared__ int32_t sh_b, sh_j;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if (tid == 0) sh_b = sh_j = 0;
     const int32_t per = (a.n_seq + THREADS - 1) / THREADS, f0 = min(a.n_seq, tid * per), f1 = min(a.n_seq, f0 + per);
     int64_t mine = 0;
     for (int32_t b = f0; b < f1; ++b) mine += tree_tiles<TT>(a, tree_rows(a, tr, b), r0);
@@ -65,27 +74,30 @@ __device__ __forceinline__ TreeBegin tree_begin(const KvArgs &a, const KvTreeSpl
         total += sum[i];
     }
     const Ranges rg = ranges_of(total, tr.R);
-    if (range >= rg.R) return TreeBegin{0, 0, 0};
+    if (range >= rg.R) return 0;
     const int64_t s = rg.start(range);
-    if (mine > 0 && s >= excl && s < excl + mine) {        // one thread
-        int64_t at = excl;
-        int32_t b = f0;
-        for (; b < f1; ++b) {
-            const int32_t t = tree_tiles<TT>(a, tree_rows(a, tr, b), r0);
-            if (s < at + t) break;
-            at += t;
+    const int32_t count = uniform((int32_t)(rg.start(range + 1) - s));
+    for (int32_t i = 0; i < n; ++i) {
+        const int64_t x = s + part_of(count, i, n);        // (inside the range: i < n)
+        if (mine > 0 && x >= excl && x < excl + mine) {    // one thread
+            int64_t to = excl;
+            int32_t b = f0;
+            for (; b < f1; ++b) {
+                const int32_t t = tree_tiles<TT>(a, tree_rows(a, tr, b), r0);
+                if (x < to + t) break;
+                to += t;
+            }
+            at[i] = TreeBegin{b, (int32_t)(x - to)};
         }
-        sh_b = b;
-        sh_j = (int32_t)(s - at);
     }
     __syncthreads();
-    return TreeBegin{uniform(sh_b), uniform(sh_j), uniform((int32_t)(rg.start(range + 1) - s))};
+    return count;
 }
 
 struct TreePos { int32_t b, j, n, m, first, tiles; };      // a sequence and a tile of it
 template <int TT>
 __device__ __forceinline__ TreePos tree_pos(const KvArgs &a, const KvTreeSplit &tr, int32_t r0, int32_t b, int32_t j) {
-    const SeqRows s = tree_rows(a, tr, b);
+    const SeqRows s = tree_rows_scalar(a, tr, b);
     return TreePos{b, j, uniform(s.n), uniform(s.m), uniform(s.first), uniform(tree_tiles<TT>(a, s, r0))};
 }
 template <int TT>
