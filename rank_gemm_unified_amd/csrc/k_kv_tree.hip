@@ -488,13 +488,18 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
 }
 
 // Put the pieces of a sequence (blockIdx.y) together: out = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s.  A thread takes
-// four dims of a row; blockIdx.x: a K/V head and JOIN_ROWS of its rows, which lie in one block of CW.
-constexpr int JOIN_ROWS = 8;
-template <typename E, int HD>
+// four dims of a row; G groups of threads take every G-th piece of the same row each, and are joined in LDS: where a sequence has
+// many pieces, a row's thread would read them one behind the other (one sequence in 32 pieces, 16 rows of 32 heads: 15.4 us).
+// blockIdx.x: a K/V head and some of its rows, which lie in one block of CW.
+template <int HD> constexpr int join_slots() { return 1024 / HD; }   // rows that 256 threads take
+template <typename E, int HD, int G>
 __global__ __launch_bounds__(256) void k_kv_tree_join(KvArgs a, KvAttend at, KvTreeSplit tr, int32_t tt, int32_t cw) {
+    constexpr int ROWS = join_slots<HD>() / G;
     __shared__ int64_t sh[8];
+    __shared__ float2 sh_ml[G > 1 ? 256 : 1];
+    __shared__ f32x4_t sh_v[G > 1 ? 256 : 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int32_t b = blockIdx.y, kvh = blockIdx.x % a.n_kv, first = blockIdx.x / a.n_kv * JOIN_ROWS, r0 = first / cw * cw;
+    const int32_t b = blockIdx.y, kvh = blockIdx.x % a.n_kv, first = blockIdx.x / a.n_kv * ROWS, r0 = first / cw * cw;
     const SeqRows sq = tree_rows(a, tr, b);
     const int32_t rows = sq.m * a.group, nt = (sq.n + tt - 1) / tt;
     if (first >= rows) return;
@@ -522,38 +527,48 @@ __global__ __launch_bounds__(256) void k_kv_tree_join(KvArgs a, KvAttend at, KvT
         p = pieces_of(before, before + nt, ranges_of(total, tr.R));
         if (p.r0 == p.r1) return;                          // one range saw it whole
     }
-    for (int32_t x = tid; x < JOIN_ROWS * (HD / 4); x += 256) {
-        const int32_t r = first + x / (HD / 4), d = 4 * (x % (HD / 4));
-        if (r >= rows) break;
-        float m = -INFINITY, l = 0.f;
-        f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        for (int32_t s = p.r0; s <= p.r1; s += 8) {        // eight loads at once
+    const int32_t r = first + tid / (HD / 4) % ROWS, d = 4 * (tid % (HD / 4)), g = tid / (HD / 4) / ROWS;
+    float m = -INFINITY, l = 0.f;
+    f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    auto add = [&](float2 ml, f32x4_t v) {
+        const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+        const float c = exp2_hw(m - ms), w = exp2_hw(ml.x - ms);
+        l = l * c + ml.y * w;
+        acc = acc * c + v * w;
+        m = mn;
+    };
+    if (r < rows)
+        for (int32_t s = p.r0 + g; s <= p.r1; s += 8 * G) {   // eight loads at once
             float2 ml[8];
             f32x4_t v[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const int32_t su = min(s + u, p.r1);
+                const int32_t su = min(s + u * G, p.r1);
                 const int64_t pl = (((int64_t)su * 2 + (su == p.r0 ? p.s0 : 0)) * a.n_kv + kvh) * tr.rows_ld + r;
                 ml[u] = tr.part_ml[pl];
                 v[u] = *(const f32x4_t *)(tr.part_o + pl * HD + d);
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                if (s + u > p.r1) break;
-                const float mn = fmaxf(m, ml[u].x), ms = mn == -INFINITY ? 0.f : mn;
-                const float c = exp2_hw(m - ms), w = exp2_hw(ml[u].x - ms);
-                l = l * c + ml[u].y * w;
-                acc = acc * c + v[u] * w;
-                m = mn;
+                if (s + u * G > p.r1) break;
+                add(ml[u], v[u]);
             }
         }
-        const int32_t node = node_of(a, tr, r);
-        E *o = (E *)at.out + (int64_t)(sq.first + node) * at.ldo + (int64_t)(kvh * a.group + r - node * a.group) * HD + d;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        if (l == 0.f) acc = f32x4_t{0.f, 0.f, 0.f, 0.f};   // no weight: zero, also where a value is not finite
-        if constexpr (sizeof(E) == 2) *(uint2 *)o = make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
-        else *(f32x4_t *)o = acc * inv;
+    if constexpr (G > 1) {
+        sh_ml[tid] = make_float2(m, l);
+        sh_v[tid] = acc;
+        __syncthreads();
+        if (g > 0) return;
+#pragma unroll
+        for (int u = 1; u < G; ++u) add(sh_ml[tid + u * ROWS * (HD / 4)], sh_v[tid + u * ROWS * (HD / 4)]);
     }
+    if (r >= rows) return;
+    const int32_t node = node_of(a, tr, r);
+    E *o = (E *)at.out + (int64_t)(sq.first + node) * at.ldo + (int64_t)(kvh * a.group + r - node * a.group) * HD + d;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (l == 0.f) acc = f32x4_t{0.f, 0.f, 0.f, 0.f};       // no weight: zero, also where a value is not finite
+    if constexpr (sizeof(E) == 2) *(uint2 *)o = make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
+    else *(f32x4_t *)o = acc * inv;
 }
 
 // ---- host ----------------------------------------------------------------------------------------
@@ -576,7 +591,7 @@ TreePlan tree_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int3
     const int64_t hu = (int64_t)n_kv * p.ncb, slots = p.nb || hd == 256 ? 256 : 512;
     // A workgroup a CU, two of the kernel for many rows.
     p.hw = p.nb == 0 ? 1 : n_kv % 4 == 0 ? 4 : n_kv % 2 == 0 ? 2 : 1;
-    p.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, slots * p.hw / hu));
+    p.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(tiles, std::max<int64_t>(64, tiles / 4)), slots * p.hw / hu));
     p.local = n_seq * hu <= slots && max_len <= (p.nb ? 1024 : 512);
     // Room for at least `slots` workgroups' pieces, so that what serves the largest call serves them all: the ranges of
     // more rows are fewer.
@@ -619,8 +634,14 @@ hipError_t run(int dtype, const KvArgs &a, const KvAttend &at, const KvTreeArgs 
     else if (pl.nb == 1) e = few<E, HD, 1>(a, at, tr, pl.local, s);
     else if constexpr (HD < 256 && sizeof(E) == 4) e = few<E, HD, 2>(a, at, tr, pl.local, s);
     if (e != hipSuccess || pl.local) return e;
-    const unsigned chunks = (unsigned)(((int64_t)ta.max_nodes * a.group + JOIN_ROWS - 1) / JOIN_ROWS);
-    hipLaunchKernelGGL((k_kv_tree_join<E, HD>), dim3(chunks * a.n_kv, (unsigned)a.n_seq), dim3(256), 0, s, a, at, tr, pl.tt, pl.cw);
+    // All threads of a workgroup to one row where a sequence is in more than eight pieces on average.
+    constexpr int SLOTS = join_slots<HD>();
+    const int64_t rows = (int64_t)ta.max_nodes * a.group;
+    if (pl.R > 8 * a.n_seq)
+        hipLaunchKernelGGL((k_kv_tree_join<E, HD, SLOTS>), dim3((unsigned)(rows * a.n_kv), (unsigned)a.n_seq), dim3(256), 0, s, a, at, tr, pl.tt, pl.cw);
+    else
+        hipLaunchKernelGGL((k_kv_tree_join<E, HD, 1>), dim3((unsigned)((rows + SLOTS - 1) / SLOTS * a.n_kv), (unsigned)a.n_seq), dim3(256), 0, s, a, at,
+                           tr, pl.tt, pl.cw);
     return hipGetLastError();
 }
 

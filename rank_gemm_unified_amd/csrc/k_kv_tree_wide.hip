@@ -149,7 +149,10 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_tree_wide(KvA
     mask_at(tr, row_of(p0), p0.j * NT - (p0.n - p0.m), &mlo, &mhi);
     fetch(0, ku, vu);
     for (int32_t i = 0; i < count; ++i) {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // this step's K and V are in
+        // this step's K and V are in; by a builtin, so that the compiler knows that what else was loaded is in too, and
+        // does not wait for it once more behind the next step's loads
+        __builtin_amdgcn_s_waitcnt(0x0070);                // vmcnt(0) lgkmcnt(0)
+        asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         const int32_t s0 = p0.j * NT - (p0.n - p0.m);      // the step's first token as a node
@@ -234,7 +237,6 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_tree_wide(KvA
                 if (k + 3 < KQ) __builtin_amdgcn_sched_group_barrier(0x100, NB, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
-            if (i + 1 == end && more) load_q(p1);          // the next sequence's
             float sc = scale2;
             if (!(scale2 > 0.f)) {                         // the largest logit need not be the largest product's
                 sc = 1.f;
@@ -315,9 +317,8 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_tree_wide(KvA
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-        } else if (i + 1 == end && more) {
-            load_q(p1);
         }
+        if (i + 1 == end && more) load_q(p1);              // the next sequence's
         p0 = p1;
         p1 = p2;
         there = there1;
