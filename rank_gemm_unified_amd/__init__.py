@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import NamedTuple
+from collections import namedtuple
 
 import numpy as np
 
@@ -503,25 +503,48 @@ def run_pool_ops(pool, ops, ranks, adapter_weights, stream=None):
 
 # ---- what the calls of a step of drafted tokens take and give ----------------------------------------
 
-class KvPlan(NamedTuple):
-    """A planned step (Pool.kv_plan): int32 step_lens [n_seq], q_start [n_seq + 1], positions [T]; int64 slots
-    [layers, 2, T], mask [T, words] or None; and int32 lens, held [n_seq] and state [4] after it."""
-    step_lens: object
-    q_start: object
-    slots: object
-    positions: object
-    mask: object
-    lens: object
-    held: object
-    state: object
+def _whole(name, t, shape, dtype, device):
+    """A contiguous tensor of that shape (-1: any size) and type, on that device."""
+    if t.dtype is not dtype or t.get_device() != device or device < 0 or t.dim() != len(shape) or not t.is_contiguous() \
+            or any(a != b != -1 for a, b in zip(t.shape, shape)):
+        raise ValueError(f"{name}: contiguous {dtype} {shape} on one device is wanted, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-class KvAccepted(NamedTuple):
-    """What Pool.kv_accept keeps: int32 lens, n_path, next [n_seq] and path [n_seq, max_nodes]."""
-    lens: object
-    path: object
-    n_path: object
-    next: object
+class KvPlan(namedtuple("KvPlan", "step_lens q_start slots positions mask lens held state")):
+    """A planned step, and the buffers that Pool.kv_plan writes it to: int32 step_lens [n_seq], q_start [n_seq + 1], positions
+    [T]; int64 slots [layers, 2, T], mask [T, words] or None; int32 lens, held [n_seq] and state [4] after it.  Checked here,
+    once: the tensors keep their shapes."""
+
+    def __new__(cls, step_lens, q_start, slots, positions, mask, lens, held, state):
+        self = super().__new__(cls, step_lens, q_start, slots, positions, mask, lens, held, state)
+        dev, n, i32, i64 = step_lens.get_device(), step_lens.numel(), torch.int32, torch.int64
+        _whole("step_lens", step_lens, (n,), i32, dev)
+        _whole("q_start", q_start, (n + 1,), i32, dev)
+        _whole("slots", slots, (-1, 2, -1), i64, dev)
+        T = slots.shape[2]
+        _whole("positions", positions, (T,), i32, dev)
+        if mask is not None:
+            _whole("mask", mask, (T, -1), i64, dev)
+        _whole("lens", lens, (n,), i32, dev)
+        _whole("held", held, (n,), i32, dev)
+        _whole("state", state, (4,), i32, dev)
+        self._sizes = (dev, n, slots.shape[0], T, 0 if mask is None else mask.shape[1])
+        return self
+
+
+class KvAccepted(namedtuple("KvAccepted", "lens path n_path next")):
+    """What Pool.kv_accept keeps, and the buffers that it writes it to: int32 lens, n_path, next [n_seq] and path [n_seq,
+    max_nodes].  Checked here, once: the tensors keep their shapes."""
+
+    def __new__(cls, lens, path, n_path, next):
+        self = super().__new__(cls, lens, path, n_path, next)
+        dev, n, i32 = lens.get_device(), lens.numel(), torch.int32
+        _whole("lens", lens, (n,), i32, dev)
+        _whole("path", path, (n, -1), i32, dev)
+        _whole("n_path", n_path, (n,), i32, dev)
+        _whole("next", next, (n,), i32, dev)
+        self._sizes = (dev, n, path.shape[1])
+        return self
 
 
 class Rope:
@@ -534,6 +557,8 @@ class Rope:
                 or not table.is_cuda:
             raise ValueError(f"table: contiguous float32 [n_positions, rot_dim / 2, 2] on the device is wanted, not "
                              f"{table.dtype} {tuple(table.shape)} on {table.device}")
+        if table.shape[0] < 1 or table.shape[1] % 8 or table.shape[1] < 8:
+            raise ValueError(f"table: at least one position and a multiple of 8 pairs are wanted, not {tuple(table.shape)}")
         self.table = table
         self.arg = lora_rope_t(table.data_ptr(), table.shape[0], 2 * table.shape[1],
                                LORA_ROPE_NEIGHBOURS if interleaved else LORA_ROPE_HALVES)
@@ -567,6 +592,7 @@ class Pool:
         self.handle = lora_pool_create(self.pages, num_pages, hidden, dtype, max_rank, n_slots, max_adapters,
                                        self.table, free_order)
         self._ws = None
+        self._device = -2 if self.pages is None else self.pages.get_device()   # (a tensor on the host says -1)
 
     def close(self):
         if self.handle:
@@ -627,7 +653,7 @@ class Pool:
     def _where(self, stream):
         """(stream handle, whether the call runs on the current stream)."""
         if stream is None:
-            return _current_stream(self.pages.get_device()), True
+            return _current_stream(self._device), True
         return (stream if isinstance(stream, int) else stream.cuda_stream), False
 
     def _empty(self, here, stream, shape, dtype):
@@ -647,15 +673,14 @@ class Pool:
     def _kv_rows(self, what, t, width):
         """Rows of `width` elements of the pool's type: how far they lie apart."""
         shape, stride = t.shape, t.stride()
-        if len(shape) != 2 or shape[1] != width or t.dtype is not self.tdtype or not t.is_cuda \
-                or t.get_device() != self.pages.get_device() or (stride[1] != 1 and shape[0]):
+        if len(shape) != 2 or shape[1] != width or t.dtype is not self.tdtype or t.get_device() != self._device \
+                or (stride[1] != 1 and shape[0]):
             raise ValueError(f"{what}: rows of {width} {self.tdtype} elements on {self.pages.device} are wanted, not "
                              f"{tuple(shape)} {t.dtype} on {t.device}, strides {stride}")
         return stride[0]
 
     def _kv_ints(self, what, t, shape, dtype):
-        if t.shape != shape or t.dtype is not dtype or not t.is_cuda or t.get_device() != self.pages.get_device() \
-                or not t.is_contiguous():
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != self._device or not t.is_contiguous():
             raise ValueError(f"{what}: contiguous {dtype} {shape} on {self.pages.device} is wanted, not {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
 
@@ -789,17 +814,9 @@ class Pool:
             out = KvPlan(new((n,), i32), new((n + 1,), i32), new((layers, 2, T), i64), new((T,), i32),
                          None if parents is None else new((T, words), i64), new((n,), i32), new((n,), i32), new((4,), i32))
         else:
-            self._kv_ints("step_lens", out.step_lens, (n,), i32)
-            self._kv_ints("q_start", out.q_start, (n + 1,), i32)
-            self._kv_ints("slots", out.slots, (layers, 2, T), i64)
-            self._kv_ints("positions", out.positions, (T,), i32)
-            self._kv_ints("lens", out.lens, (n,), i32)
-            self._kv_ints("held", out.held, (n,), i32)
-            self._kv_ints("state", out.state, (4,), i32)
-            if parents is not None:
-                if out.mask is None:
-                    raise ValueError("parents without a mask to write")
-                self._kv_ints("mask", out.mask, (T, words), i64)
+            if out._sizes[:4] != (self._device, n, layers, T) or (parents is not None and out._sizes[4] != words):
+                raise ValueError(f"out: a plan of {n} sequences, {layers} layers, {T} rows and {words} words of mask on "
+                                 f"{self.pages.device} is wanted, not {out._sizes[1:]} on device {out._sizes[0]}")
         lora_kv_plan(self.handle, layout, layers, n, counts.data_ptr(), lens.data_ptr(), held.data_ptr(), table.data_ptr(), mp,
                      mp * layout.tokens_per_page if max_len is None else max_len, stock.data_ptr(), groups, state.data_ptr(),
                      T, None if parents is None else parents.data_ptr(), max_nodes, out.step_lens.data_ptr(),
@@ -887,10 +904,9 @@ class Pool:
                 with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=self.pages.device)):
                     out.lens.copy_(lens)
         else:
-            self._kv_ints("lens", out.lens, (n,), i32)
-            self._kv_ints("path", out.path, (n, max_nodes), i32)
-            self._kv_ints("n_path", out.n_path, (n,), i32)
-            self._kv_ints("next", out.next, (n,), i32)
+            if out._sizes != (self._device, n, max_nodes):
+                raise ValueError(f"out: {n} sequences and {max_nodes} nodes on {self.pages.device} are wanted, not "
+                                 f"{out._sizes[1:]} on device {out._sizes[0]}")
         lora_kv_accept(self.handle, layout, layers, n, table.data_ptr(), mp, q_start.data_ptr(), lens.data_ptr(), T,
                        tokens.data_ptr(), targets.data_ptr(), parents.data_ptr(), max_nodes, out.lens.data_ptr(),
                        out.path.data_ptr(), out.n_path.data_ptr(), out.next.data_ptr(), stream=handle)

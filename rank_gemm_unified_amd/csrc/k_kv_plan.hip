@@ -71,39 +71,64 @@ __global__ __launch_bounds__(256) void k_kv_plan(KvPlan p, int32_t per_layers, i
     int err = 0;
 
     // ---- sums over the sequences: this thread's begin at `mine` ----
-    auto scan = [&](int64_t &x, int k) {                   // exclusive; returns the total
-        int64_t incl = x;
+    // All three at once, as if every row had room; where they have not (T says fewer) the sequences behind T take nothing,
+    // and the sums are formed again.
+    Sums mine{0, 0, 0}, all;
+    auto sum_up = [&](Sums &x) {                           // exclusive; returns the totals
+        int64_t v[3] = {x.rows, x.take, x.give}, total[3];
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int64_t y = __shfl_up(incl, o, 64);
-            if (lane >= o) incl += y;
+        for (int k = 0; k < 3; ++k) {
+            int64_t incl = v[k];
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int64_t y = __shfl_up(incl, o, 64);
+                if (lane >= o) incl += y;
+            }
+            if (lane == 63) sh[wave][k] = incl;
+            v[k] = incl - v[k];
         }
-        if (lane == 63) sh[wave][k] = incl;
         __syncthreads();
-        int64_t before = incl - x, total = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            before += i < wave ? sh[i][k] : 0;
-            total += sh[i][k];
+        for (int k = 0; k < 3; ++k) {
+            total[k] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[k] += i < wave ? sh[i][k] : 0;
+                total[k] += sh[i][k];
+            }
         }
-        x = before;
-        return total;
+        x = Sums{v[0], v[1], v[2]};
+        return Sums{total[0], total[1], total[2]};
     };
-    Sums mine{0, 0, 0};
-    for (int32_t b = b0; b < b1; ++b) mine.rows += rows_of(p, b, &err);
-    const int64_t rows = scan(mine.rows, 0);
-    {
+    for (int32_t b = b0; b < b1; ++b) {
+        const Want w = want_of(p, b, 0);
+        mine.rows += w.c;
+        mine.take += w.take;
+        mine.give += w.give;
+        err |= w.err;
+    }
+    all = sum_up(mine);
+    if (all.rows > p.T) {
         int64_t end = mine.rows;
+        const int64_t first = end;
+        mine.take = mine.give = 0;
         for (int32_t b = b0; b < b1; ++b) {
-            end += rows_of(p, b, &err);
+            int e = 0;
+            end += rows_of(p, b, &e);
             const Want w = want_of(p, b, end);
             mine.take += w.take;
             mine.give += w.give;
             err |= w.err;
         }
+        mine.rows = 0;
+        __syncthreads();
+        all.take = all.give = 0;
+        const Sums again = sum_up(mine);
+        mine.rows = first;
+        all.take = again.take;
+        all.give = again.give;
     }
-    scan(mine.take, 1);
-    const int64_t given = scan(mine.give, 2);
+    const int64_t rows = all.rows, given = all.give;
     int32_t head = p.state[0], free = p.state[1];
     const bool ring = head >= 0 && head < p.groups && free >= 0 && free <= p.groups;
     if (!ring) {

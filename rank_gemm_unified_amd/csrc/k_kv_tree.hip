@@ -592,7 +592,7 @@ TreePlan tree_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int3
     // A workgroup a CU, two of the kernel for many rows.
     p.hw = p.nb == 0 ? 1 : n_kv % 4 == 0 ? 4 : n_kv % 2 == 0 ? 2 : 1;
     p.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(tiles, std::max<int64_t>(64, tiles / 4)), slots * p.hw / hu));
-    p.local = n_seq * hu <= slots && max_len <= (p.nb ? 1024 : 512);
+    p.local = n_seq * hu <= 256 && max_len <= (p.nb ? 1024 : 512);
     // Room for at least `slots` workgroups' pieces, so that what serves the largest call serves them all: the ranges of
     // more rows are fewer.
     const size_t pieces = 2 * (size_t)std::min<int64_t>(tiles * hu, std::max<int64_t>(slots * p.hw, hu)) * p.cw;
