@@ -913,4 +913,4 @@ class Pool:
         return out
 
 
-from .kv_cache import KvCache  # noqa: E402,F401
+from .kv_cache import KvCache, KvDraftCache  # noqa: E402,F401

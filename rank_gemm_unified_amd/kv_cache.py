@@ -184,3 +184,106 @@ class KvCache:
             self.scores[:, row] = 0
         self._in_place(now)
         self._rg.lora_pool_free_kv(self.pool.handle, rid)
+
+
+class KvDraftCache:
+    """The KV caches of up to max_seqs sequences whose steps are planned on the GPU: page tables, lengths and free pages live
+    there, so that a step follows the one before without a word to the host, and can be captured into a graph whole.  For
+    steps of drafted tokens (trees, of which the model keeps a path), single tokens (trees of one node) and prompts.
+
+        cache = KvDraftCache(pool, layers, layout, max_seqs, max_tokens, groups, request, rope)
+        cache.plan(counts, T)                         # new tokens of each sequence, T rows in all: a prompt
+        q = cache.write(layer, q, k, v); o = cache.attend(layer, q)           # per layer, row by row as counts say
+        cache.plan(counts, T, parents, max_nodes)     # a step of drafted trees: node 0 the token chosen last
+        ... write, attend ...
+        kept = cache.accept(tokens, targets)          # kept.path, n_path, next; the lengths are the kept tokens'
+        cache.finish(rows)                            # their pages come back with the next plan
+
+    counts: int32 [max_seqs] on the device, 0 for sequences that rest.  `groups` page groups (tokens_per_page tokens in all
+    layers each) are taken from the pool under the id `request`, used in no other cache of it, and shared by the sequences;
+    a sequence that they do not suffice for sits the step out (lora_kv_plan: its output is zero, its length stays; refused()
+    says how many).  `lens`, `table`, `held`, `stock` and `state` are the same tensors throughout; `step` is the latest plan.
+
+    Everything runs on the current stream and in its order; using the cache from another one is the caller's to order.  What a
+    captured step reads and writes besides (rows, counts, parents, `step`) is its graph's."""
+
+    def __init__(self, pool, layers, layout, max_seqs, max_tokens, groups, request, rope=None):
+        import rank_gemm_unified_amd as rg
+        if pool.pages is None:
+            raise ValueError("a bookkeeping-only pool holds no KV vectors")
+        tpp = layout.tokens_per_page
+        if not 1 <= max_tokens <= rg.LORA_MAX_KV_TOKENS - tpp:
+            raise ValueError(f"max_tokens {max_tokens} not in [1, {rg.LORA_MAX_KV_TOKENS - tpp}]")
+        if groups < 1 or max_seqs < 1:
+            raise ValueError(f"{groups} page groups for {max_seqs} sequences")
+        self._rg, self.pool, self.layers, self.layout, self.max_seqs = rg, pool, layers, layout, max_seqs
+        self.max_tokens, self.request, self.rope, self._parents = max_tokens, request, rope, None
+        ids = []
+        try:
+            for _ in range(groups):
+                ids.append(rg.lora_pool_grow_kv(pool.handle, request, layers))
+        except rg.LoraError:
+            for group in reversed(ids):                    # the last taken first: the free list as it was
+                rg.lora_pool_drop_kv(pool.handle, request, group[::-1])
+            if ids:
+                rg.lora_pool_free_kv(pool.handle, request)
+            raise
+        i32 = dict(dtype=torch.int32, device=pool.pages.device)
+        self.stock = torch.tensor(ids, **i32).view(groups, layers, 2)
+        self.table = torch.full((layers, max_seqs, 2, -(-max_tokens // tpp)), -1, **i32)
+        self.lens, self.held = torch.zeros(max_seqs, **i32), torch.zeros(max_seqs, **i32)
+        self.state = torch.tensor([0, groups, 0, 0], **i32)
+        self.step = None
+
+    def plan(self, counts, T, parents=None, max_nodes=None):
+        """Plan a step of counts [max_seqs] new tokens, T rows at least (Pool.kv_plan).  parents: int32 [T], of trees of up to
+        max_nodes nodes (None: 64); None: rows in a line, each seeing those before it."""
+        max_nodes = 0 if parents is None else 64 if max_nodes is None else max_nodes
+        words, new = (max_nodes + 63) // 64, lambda shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=self.lens.device)
+        step = self._rg.KvPlan(new(self.max_seqs), new(self.max_seqs + 1), new((self.layers, 2, T), torch.int64), new(T),
+                               new((T, words), torch.int64) if words else None, self.lens, self.held, self.state)
+        self.pool.kv_plan(self.layout, counts, self.lens, self.held, self.table, self.stock, self.state, T, self.max_tokens,
+                          parents, max_nodes, out=step)
+        self.step, self._parents, self._nodes = step, parents, max_nodes
+
+    def write(self, layer, q, k, v, q_out=None):
+        """Layer `layer`'s rows of the step: K and V to their pages, and q, all turned by their positions if the cache has a
+        Rope (Pool.kv_write_rope).  Returns the q to attend with."""
+        if self.rope is None:
+            self.pool.kv_write(self.layout, k, v, self.table[layer], self.step.step_lens, self.step.q_start)
+            return q
+        return self.pool.kv_write_rope(self.layout, self.rope, q, k, v, self.step.slots[layer], self.step.positions, q_out)
+
+    def attend(self, layer, q, scale=None, max_len=None, out=None):
+        """The step's attention in layer `layer` (Pool.kv_attend_tree, or kv_attend_chunk without parents).  max_len None: the
+        longest a sequence may become."""
+        max_len = self.max_tokens if max_len is None else max_len
+        args = dict(scale=scale, max_len=max_len, out=out)
+        if self._parents is None:
+            return self.pool.kv_attend_chunk(self.layout, q, self.table[layer], self.step.step_lens, self.step.q_start, **args)
+        return self.pool.kv_attend_tree(self.layout, q, self.table[layer], self.step.step_lens, self.step.q_start, self.step.mask,
+                                        self._nodes, **args)
+
+    def accept(self, tokens, targets):
+        """Keep the path of each tree that the model agrees with (Pool.kv_accept): tokens, targets int32 [T], what each node
+        stands for and what the model chose behind it."""
+        if self._parents is None:
+            raise ValueError("the step has no trees")
+        new, n = lambda *shape: torch.empty(shape, dtype=torch.int32, device=self.lens.device), self.max_seqs
+        return self.pool.kv_accept(self.layout, self.table, self.step.step_lens, self.step.q_start, tokens, targets, self._parents,
+                                   self._nodes, out=self._rg.KvAccepted(self.lens, new(n, self._nodes), new(n), new(n)))
+
+    def finish(self, rows):
+        """Sequences done: their rows are free, and the next plan takes their pages back.  rows: a list, or an int64 tensor on
+        the device."""
+        self.lens.index_fill_(0, torch.as_tensor(rows, dtype=torch.int64, device=self.lens.device), 0)
+
+    def refused(self):
+        """Sequences that sat the latest step out although they had new tokens (waits for the device)."""
+        return int(self.state[2])
+
+    def close(self):
+        """Every page back to the pool, when the device is done with them: whatever takes them next may write them on any
+        stream."""
+        torch.cuda.synchronize(self.lens.device)
+        self._rg.lora_pool_free_kv(self.pool.handle, self.request)
