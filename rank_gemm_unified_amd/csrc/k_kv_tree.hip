@@ -583,16 +583,21 @@ TreePlan tree_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int3
     TreePlan p;
     const int group = n_heads / n_kv;
     const int64_t rows = (int64_t)max_nodes * group;
+    const int64_t blocks = (rows + WIDE_ROWS - 1) / WIDE_ROWS;
     p.nb = rows <= 16 ? 1 : rows <= 32 && hd < 256 && dtype == LORA_F32 ? 2 : 0;
-    p.cw = p.nb ? 16 * p.nb : WIDE_ROWS;
-    p.tt = p.nb ? (dtype == LORA_F32 && hd > 64 ? 16 : 32) : (dtype == LORA_F32 ? 32 : 64);
+    p.local = n_seq * n_kv * (p.nb ? 1 : blocks) <= 256 && max_len <= (p.nb ? 1024 : 512);
+    // Neighbouring heads a workgroup.  Two of the kernel for many rows where 64 are enough and the call keeps every workgroup
+    // busy for several steps (16 trees of 32 nodes, 32 heads, behind up to 2000 tokens: 89 us one head each, 85 two; one tree of
+    // 16, 32 heads on 8, behind 1000: 14 and 18.8).
+    const bool two = rows <= WIDE_ROWS / 2 && n_kv % 2 == 0 && dtype != LORA_F32 && (max_len + 63) / 64 * n_seq * n_kv >= 4 * 512;
+    p.hw = p.nb ? (n_kv % 4 == 0 ? 4 : n_kv % 2 == 0 ? 2 : 1) : two && !p.local ? 2 : 1;
+    p.cw = p.nb ? 16 * p.nb : WIDE_ROWS / p.hw;
+    p.tt = p.nb ? (dtype == LORA_F32 && hd > 64 ? 16 : 32) : (dtype == LORA_F32 ? 32 : 64) / p.hw;
     const int64_t tiles = (max_len + p.tt - 1) / p.tt * n_seq;
     p.ncb = (int32_t)((rows + p.cw - 1) / p.cw);
     const int64_t hu = (int64_t)n_kv * p.ncb, slots = p.nb || hd == 256 ? 256 : 512;
     // A workgroup a CU, two of the kernel for many rows.
-    p.hw = p.nb == 0 ? 1 : n_kv % 4 == 0 ? 4 : n_kv % 2 == 0 ? 2 : 1;
     p.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(tiles, std::max<int64_t>(64, tiles / 4)), slots * p.hw / hu));
-    p.local = n_seq * hu <= 256 && max_len <= (p.nb ? 1024 : 512);
     // Room for at least `slots` workgroups' pieces, so that what serves the largest call serves them all: the ranges of
     // more rows are fewer.
     const size_t pieces = 2 * (size_t)std::min<int64_t>(tiles * hu, std::max<int64_t>(slots * p.hw, hu)) * p.cw;

@@ -12,16 +12,19 @@
 
 namespace lorapool {
 
-// LOCAL: one whole sequence (blockIdx.y), no pieces.
-template <typename E, int HD, bool LOCAL>
+// LOCAL: one whole sequence (blockIdx.y), no pieces.  HEADS: two neighbouring heads share the workgroup where 64 rows are enough
+// for each: two waves a head, steps of half the tokens, and pieces of the pages twice as long that are read at one time.
+template <typename E, int HD, int HEADS, bool LOCAL>
 __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_tree_wide(KvArgs a, KvAttend at, KvTreeSplit tr) {
     using C = Chunk<E, HD>;
-    constexpr int NT = C::NT, NB = C::NB, RB = C::RB, CH = C::CH, KQ = C::KQ, ND = HD / 32;
+    constexpr int TILE = C::NT, NT = TILE / HEADS, NB = NT / 32;   // rows of a tile in LDS, head by head; tokens of a step
+    constexpr int RB = C::RB, CH = C::CH, KQ = C::KQ, ND = HD / 32, WPH = 4 / HEADS, ROWS = 32 * WPH;
     constexpr bool BF = C::BF;
     extern __shared__ __align__(256) char smem[];
     __shared__ unsigned long long sh_flag;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 31, hh = lane >> 5;
-    const int32_t kvh = blockIdx.x % a.n_kv, rest = blockIdx.x / a.n_kv, r0 = rest % tr.ncb * WIDE_ROWS, range = rest / tr.ncb;
+    const int32_t head0 = blockIdx.x % (a.n_kv / HEADS) * HEADS, rest = blockIdx.x / (a.n_kv / HEADS), mine = wave / WPH, kvh = head0 + mine;
+    const int32_t r0 = rest % tr.ncb * ROWS, rw = r0 + 32 * (wave % WPH), range = rest / tr.ncb;   // rw: the wave's first row
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         int bits = 0;
         for (int32_t b = tid; b < a.n_seq; b += 256) bits |= tree_rows(a, tr, b).err;
@@ -42,10 +45,10 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_tree_wide(KvA
     int32_t begin = 0, end = min(count, seg.tiles - from);
     bool first_piece = true;
 
-    const char *base = a.pages + (int64_t)kvh * RB;
+    const char *base = a.pages + (int64_t)head0 * RB;
     const uint32_t page_units = (uint32_t)(a.page_bytes >> 7), tok_units = (uint32_t)(a.tok_bytes >> 7);
     const float scale2 = at.scale * 1.4426950408889634f;
-    const int32_t r = r0 + 32 * wave + col;                // this lane's row
+    const int32_t r = rw + col;                // this lane's row
     int bad = 0;
     // LDS as it stands for every wave; loads that are on their way to it are not waited for
     auto meet = [] {
@@ -76,9 +79,10 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_tree_wide(KvA
 #pragma unroll
         for (int x = 0; x < C::PER; ++x) {
             const int at0 = (wave * C::PER + x) * 1024, byte = at0 + lane * 16, t = byte / RB, c = (byte % RB) / 16;
-            const uint32_t k = __shfl(ku, t, 64), v = __shfl(vu, t, 64);
-            lds_gload16(base + ((uint64_t)k << 7) + 16 * C::k_swz(t, c), (lds_void *)(kb + at0));
-            lds_gload16(base + ((uint64_t)v << 7) + 16 * C::v_swz(t, c), (lds_void *)(vb + at0));
+            const uint32_t k = __shfl(ku, t % NT, 64), v = __shfl(vu, t % NT, 64);
+            const char *of = base + t / NT * RB;
+            lds_gload16(of + ((uint64_t)k << 7) + 16 * C::k_swz(t, c), (lds_void *)(kb + at0));
+            lds_gload16(of + ((uint64_t)v << 7) + 16 * C::v_swz(t, c), (lds_void *)(vb + at0));
         }
     };
     auto row_of = [&](const TreePos &p) { return p.first + node_of(a, tr, r < p.m * a.group ? r : r0); };
@@ -169,48 +173,48 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_tree_wide(KvA
             if (s1 + NT > 0) mask_at(tr, row_of(p1), s1, &mlo, &mhi);
         }
         constexpr uint64_t ALL = NT == 64 ? ~0ull : 0xffffffffull;
-        const char *kb = smem + (i & 1) * C::BUF;
-        char *vb = smem + (2 + (i & 1)) * C::BUF;
+        char *v_tile = smem + (2 + (i & 1)) * C::BUF;
+        const char *kb = smem + (i & 1) * C::BUF + mine * (NT * RB), *vb = v_tile + mine * (NT * RB);   // this wave's head's
         if (there != ALL) {                                // rows of tokens that are not there must not reach the products
-            for (int x = tid; x < NT * CH; x += 256)
-                if (!((there >> (x / CH)) & 1)) store16(vb + 16 * x, u32x4_t{0, 0, 0, 0});
+            for (int x = tid; x < TILE * CH; x += 256)
+                if (!((there >> (x / CH % NT)) & 1)) store16(v_tile + 16 * x, u32x4_t{0, 0, 0, 0});
             meet();
         }
         if (nodes) {                                       // infinities and NaN of nodes: not by the products, but to the
             if (tid == 0) sh_flag = 0;                     // rows that see them
             meet();
-            for (int x = tid; x < NT * CH; x += 256) {
-                const u32x4_t y = load16(vb + 16 * x);
-                if (s0 + x / CH >= 0 && (not_finite<E>(y[0]) | not_finite<E>(y[1]) | not_finite<E>(y[2]) | not_finite<E>(y[3])))
+            for (int x = tid; x < TILE * CH; x += 256) {
+                const u32x4_t y = load16(v_tile + 16 * x);
+                if (s0 + x / CH % NT >= 0 && (not_finite<E>(y[0]) | not_finite<E>(y[1]) | not_finite<E>(y[2]) | not_finite<E>(y[3])))
                     atomicOr(&sh_flag, 1ull << (x / CH));
             }
             meet();
             if (const unsigned long long flags = sh_flag) {
                 for (unsigned long long f = flags; f; f &= f - 1) {
                     const int t = __ffsll((long long)f) - 1;
-                    if (sees >> t & 1) {
+                    if (t / NT == mine && sees >> (t % NT) & 1) {
 #pragma unroll
                         for (int d = 0; d < ND; ++d)
 #pragma unroll
                             for (int x = 0; x < 16; ++x) {
                                 const int byte = (32 * d + 8 * (x / 4) + 4 * hh + (x & 3)) * (int)sizeof(E);
-                                const float y = to_f32(*(const E *)(vb + t * RB + 16 * C::v_swz(t, byte / 16) + byte % 16));
+                                const float y = to_f32(*(const E *)(v_tile + t * RB + 16 * C::v_swz(t, byte / 16) + byte % 16));
                                 if (y - y != 0.f) acc[d][x] += y;
                             }
                     }
                 }
                 meet();
-                for (int x = tid; x < NT * CH; x += 256)
+                for (int x = tid; x < TILE * CH; x += 256)
                     if (flags >> (x / CH) & 1) {
-                        u32x4_t y = load16(vb + 16 * x);
+                        u32x4_t y = load16(v_tile + 16 * x);
 #pragma unroll
                         for (int z = 0; z < 4; ++z) y[z] ^= not_finite<E>(y[z]);
-                        store16(vb + 16 * x, y);
+                        store16(v_tile + 16 * x, y);
                     }
                 meet();
             }
         }
-        if (r0 + 32 * wave < seg.m * a.group) {            // else the wave has no rows
+        if (rw < seg.m * a.group) {                         // else the wave has no rows
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
@@ -352,8 +356,11 @@ hipError_t run(const KvArgs &a, const KvAttend &at, const KvTreeSplit &tr, bool 
         hipLaunchKernelGGL(kernel, grid, dim3(256), LDS, s, a, at, tr);
         return hipGetLastError();
     };
-    const unsigned hu = (unsigned)(a.n_kv * tr.ncb);
-    return local ? launch(k_kv_tree_wide<E, HD, true>, dim3(hu, (unsigned)a.n_seq)) : launch(k_kv_tree_wide<E, HD, false>, dim3(hu * tr.R));
+    const unsigned hu = (unsigned)(a.n_kv / tr.hw * tr.ncb);
+    if (local) return launch(k_kv_tree_wide<E, HD, 1, true>, dim3(hu, (unsigned)a.n_seq));
+    if constexpr (sizeof(E) == 2)
+        if (tr.hw == 2) return launch(k_kv_tree_wide<E, HD, 2, false>, dim3(hu * tr.R));
+    return launch(k_kv_tree_wide<E, HD, 1, false>, dim3(hu * tr.R));
 }
 
 template <typename E>
