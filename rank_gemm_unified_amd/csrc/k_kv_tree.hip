@@ -58,7 +58,7 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
         total = count = tree_tiles<TT>(a, tree_rows_scalar(a, tr, b0), r0);
         begin = 0;
     } else {
-        total = tree_begin<TT, THREADS>(a, tr, r0, range, n_parts, parts);
+        total = tree_begin<E, TT, THREADS>(a, at, tr, r0, CW, head0, hw, range, n_parts, parts);
         if (total == 0) return;
         range_b = uniform(parts[0].b);
         b0 = uniform(parts[part].b);
@@ -490,43 +490,55 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
 // Put the pieces of a sequence (blockIdx.y) together: out = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s.  A thread takes
 // four dims of a row; G groups of threads take every G-th piece of the same row each, and are joined in LDS: where a sequence has
 // many pieces, a row's thread would read them one behind the other (one sequence in 32 pieces, 16 rows of 32 heads: 15.4 us).
-// blockIdx.x: a K/V head and some of its rows, which lie in one block of CW.
+// blockIdx.x: a K/V head and some of its rows, which lie in one block of CW.  blockIdx.y: a sequence, or, where the sequences are
+// more than the places between two ranges, one of those: the first that lies inside the sequence.
 template <int HD> constexpr int join_slots() { return 1024 / HD; }   // rows that 256 threads take
 template <typename E, int HD, int G>
-__global__ __launch_bounds__(256) void k_kv_tree_join(KvArgs a, KvAttend at, KvTreeSplit tr, int32_t tt, int32_t cw) {
+__global__ __launch_bounds__(256) void k_kv_tree_join(KvArgs a, KvAttend at, KvTreeSplit tr, int32_t tt_log, int32_t cw, int by_range) {
     constexpr int ROWS = join_slots<HD>() / G;
-    __shared__ int64_t sh[8];
+    __shared__ int64_t sh[4], sh_before;
+    __shared__ int32_t sh_seq;
     __shared__ float2 sh_ml[G > 1 ? 256 : 1];
     __shared__ f32x4_t sh_v[G > 1 ? 256 : 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int32_t b = blockIdx.y, kvh = blockIdx.x % a.n_kv, first = blockIdx.x / a.n_kv * ROWS, r0 = first / cw * cw;
-    const SeqRows sq = tree_rows(a, tr, b);
-    const int32_t rows = sq.m * a.group, nt = (sq.n + tt - 1) / tt;
-    if (first >= rows) return;
+    const int32_t kvh = blockIdx.x % a.n_kv, first = blockIdx.x / a.n_kv * ROWS, r0 = first / cw * cw;
+    const int32_t per = (a.n_seq + 255) / 256, f0 = min(a.n_seq, tid * per), f1 = min(a.n_seq, f0 + per);
+    auto tiles_of = [&](const SeqRows &s) { return s.m * a.group > r0 ? (s.n + (1 << tt_log) - 1) >> tt_log : 0; };
     int64_t before = 0, total = 0;
-    for (int32_t x = tid; x < a.n_seq; x += 256) {
-        const SeqRows s = tree_rows(a, tr, x);
-        const int32_t t = s.m * a.group > r0 ? (s.n + tt - 1) / tt : 0;
-        total += t;
-        before += x < b ? t : 0;
-    }
+    for (int32_t b = f0; b < f1; ++b) before += tiles_of(tree_rows(a, tr, b));
+    int64_t incl = before;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        total += __shfl_xor(total, o, 64);
-        before += __shfl_xor(before, o, 64);
+    for (int o = 1; o < 64; o <<= 1) {
+        const int64_t y = __shfl_up(incl, o, 64);
+        if (lane >= o) incl += y;
     }
-    if (lane == 0) {
-        sh[wave] = total;
-        sh[4 + wave] = before;
+    if (lane == 63) sh[wave] = incl;
+    if (tid == 0) sh_seq = -1;
+    __syncthreads();
+    before = incl - before;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        before += i < wave ? sh[i] : 0;
+        total += sh[i];
+    }
+    const Ranges rg = ranges_of(total, tr.R);
+    // the sequence, by the thread that has it, if more than one range has a piece of it
+    const int64_t place = by_range && (int32_t)blockIdx.y + 1 < rg.R ? rg.start(blockIdx.y + 1) : -1;
+    for (int32_t b = f0; b < f1; ++b) {
+        const int32_t t = tiles_of(tree_rows(a, tr, b));
+        if (by_range ? place > before && place < before + t && rg.start(blockIdx.y) <= before : b == (int32_t)blockIdx.y && t > 0) {
+            sh_seq = b;
+            sh_before = before;
+        }
+        before += t;
     }
     __syncthreads();
-    total = sh[0] + sh[1] + sh[2] + sh[3];
-    before = sh[4] + sh[5] + sh[6] + sh[7];
-    Pieces p{0, -1, 0};
-    if (nt) {
-        p = pieces_of(before, before + nt, ranges_of(total, tr.R));
-        if (p.r0 == p.r1) return;                          // one range saw it whole
-    }
+    const int32_t b = uniform(sh_seq);
+    if (b < 0) return;
+    const SeqRows sq = tree_rows_scalar(a, tr, b);
+    const int32_t rows = sq.m * a.group, nt = tiles_of(sq);
+    const Pieces p = pieces_of(sh_before, sh_before + nt, rg);
+    if (first >= rows || p.r0 == p.r1) return;             // one range saw it whole
     const int32_t r = first + tid / (HD / 4) % ROWS, d = 4 * (tid % (HD / 4)), g = tid / (HD / 4) / ROWS;
     float m = -INFINITY, l = 0.f;
     f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -641,12 +653,15 @@ hipError_t run(int dtype, const KvArgs &a, const KvAttend &at, const KvTreeArgs 
     if (e != hipSuccess || pl.local) return e;
     // All threads of a workgroup to one row where a sequence is in more than eight pieces on average.
     constexpr int SLOTS = join_slots<HD>();
+    if (pl.R == 1) return e;                               // one range sees every sequence whole
     const int64_t rows = (int64_t)ta.max_nodes * a.group;
+    const int by_range = pl.R - 1 < a.n_seq, tt_log = __builtin_ctz(pl.tt);
+    const unsigned y = (unsigned)(by_range ? pl.R - 1 : a.n_seq);
     if (pl.R > 8 * a.n_seq)
-        hipLaunchKernelGGL((k_kv_tree_join<E, HD, SLOTS>), dim3((unsigned)(rows * a.n_kv), (unsigned)a.n_seq), dim3(256), 0, s, a, at, tr, pl.tt, pl.cw);
+        hipLaunchKernelGGL((k_kv_tree_join<E, HD, SLOTS>), dim3((unsigned)(rows * a.n_kv), y), dim3(256), 0, s, a, at, tr, tt_log, pl.cw, by_range);
     else
-        hipLaunchKernelGGL((k_kv_tree_join<E, HD, 1>), dim3((unsigned)((rows + SLOTS - 1) / SLOTS * a.n_kv), (unsigned)a.n_seq), dim3(256), 0, s, a, at,
-                           tr, pl.tt, pl.cw);
+        hipLaunchKernelGGL((k_kv_tree_join<E, HD, 1>), dim3((unsigned)((rows + SLOTS - 1) / SLOTS * a.n_kv), y), dim3(256), 0, s, a, at, tr, tt_log,
+                           pl.cw, by_range);
     return hipGetLastError();
 }
 

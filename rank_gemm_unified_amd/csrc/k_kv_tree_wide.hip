@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_tree_wide(KvA
     if constexpr (LOCAL) {
         count = tree_tiles<NT>(a, tree_rows(a, tr, b0), r0);
     } else {
-        count = tree_begin<NT, 256>(a, tr, r0, range, 1, &w);
+        count = tree_begin<E, NT, 256>(a, at, tr, r0, ROWS, head0, HEADS, range, 1, &w);
         if (count == 0) return;
         b0 = uniform(w.b);
         from = uniform(w.j);

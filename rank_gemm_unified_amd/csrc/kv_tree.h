@@ -48,17 +48,35 @@ __device__ __forceinline__ int32_t node_of(const KvArgs &a, const KvTreeSplit &t
     return a.group == 1 ? r : (int32_t)__umulhi((uint32_t)r, tr.group_magic);
 }
 
+// Zero rows of a sequence without tokens, by one thread: nothing else comes by (a program's step has few, if any).
+template <typename E>
+__device__ __forceinline__ void zero_rows(const KvArgs &a, const KvAttend &at, const KvTreeSplit &tr, const SeqRows &s, int32_t r0, int32_t cw,
+                                          int32_t head0, int32_t heads) {
+    for (int32_t r = r0; r < min(r0 + cw, s.m * a.group); ++r) {
+        const int32_t node = node_of(a, tr, r);
+        for (int32_t h = head0; h < head0 + heads; ++h) {
+            E *o = (E *)at.out + (int64_t)(s.first + node) * at.ldo + (int64_t)(h * a.group + r - node * a.group) * a.head_dim;
+            for (int32_t d = 0; d < a.head_dim; d += 16 / (int)sizeof(E)) store16(o + d, u32x4_t{0, 0, 0, 0});
+        }
+    }
+}
+
 // Where `n` equal parts of a range begin: sequence and tile of it.  Returns the range's tiles (0: there is no such range).
-// All threads call.
+// The first range's workgroups also write the rows of sequences without tokens.  All threads call.
 struct TreeBegin { int32_t b, j; };
 __device__ __forceinline__ int32_t part_of(int32_t count, int32_t i, int32_t n) { return (int32_t)(((int64_t)count * i) / n); }
-template <int TT, int THREADS>
-__device__ __forceinline__ int32_t tree_begin(const KvArgs &a, const KvTreeSplit &tr, int32_t r0, int32_t range, int32_t n, TreeBegin *at) {
+template <typename E, int TT, int THREADS>
+__device__ __forceinline__ int32_t tree_begin(const KvArgs &a, const KvAttend &att, const KvTreeSplit &tr, int32_t r0, int32_t cw, int32_t head0,
+                                              int32_t heads, int32_t range, int32_t n, TreeBegin *at) {
     __shared__ int64_t sum[THREADS / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int32_t per = (a.n_seq + THREADS - 1) / THREADS, f0 = min(a.n_seq, tid * per), f1 = min(a.n_seq, f0 + per);
     int64_t mine = 0;
-    for (int32_t b = f0; b < f1; ++b) mine += tree_tiles<TT>(a, tree_rows(a, tr, b), r0);
+    for (int32_t b = f0; b < f1; ++b) {
+        const SeqRows s = tree_rows(a, tr, b);
+        mine += tree_tiles<TT>(a, s, r0);
+        if (range == 0 && s.n == 0 && s.m > 0) zero_rows<E>(a, att, tr, s, r0, cw, head0, heads);
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
