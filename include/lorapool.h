@@ -577,8 +577,10 @@ size_t lora_kv_attend_tree_workspace_size(const lora_pool *pool, const lora_kv_l
  *   mask         device uint64 [T][(max_nodes + 63) / 64], as lora_kv_plan writes it; any other set of nodes will do.
  *                Bits of nodes that a sequence does not have are not looked at
  *   max_nodes    no sequence has more new tokens (1 .. LORA_MAX_TREE): one that does counts as empty, and is recorded
- * A row that sees nothing comes out as zero.  Weights and the rest as lora_kv_attend; an infinite value of a node whose
- * weight is zero makes a row that sees it NaN or that infinity.  Errors: LORA_EINVAL, LORA_EHIP.
+ * A row that sees nothing comes out as zero.  bfloat16 pools: the weights enter the product with V as lora_kv_attend's
+ * where max_nodes * n_heads / n_kv_heads is at most 16, as lora_kv_attend_chunk's (rounded once) where it is more.  An
+ * infinite value of a node whose weight is zero makes a row that sees it NaN or that infinity.  The rest as lora_kv_attend.
+ * Errors: LORA_EINVAL, LORA_EHIP.
  */
 int lora_kv_attend_tree(lora_pool *pool, const lora_kv_layout_t *layout, const void *q, int64_t ldq,
                         const int32_t *table, int32_t max_pages, const int32_t *q_start, const int32_t *lens,
@@ -596,7 +598,8 @@ int lora_kv_attend_tree(lora_pool *pool, const lora_kv_layout_t *layout, const v
  *                sequences without new tokens
  *   next         device int32 [n_seq]: targets of the path's last node: the next tree's root; -1 where the path is empty
  * Pages that hold moved tokens belong to one sequence alone.  A token on a bad page does not move, and is recorded; a
- * parent that is no earlier node makes its node nobody's child.  Errors: LORA_EINVAL, LORA_EHIP.
+ * parent that is no earlier node makes its node nobody's child.  A step's path is kept once: a second call would move what
+ * has moved.  T == 0: every path is empty; tokens, targets and parents may be NULL.  Errors: LORA_EINVAL, LORA_EHIP.
  */
 int lora_kv_accept(lora_pool *pool, const lora_kv_layout_t *layout, int32_t layers, int32_t n_seq, const int32_t *table,
                    int32_t max_pages, const int32_t *q_start, const int32_t *lens, int64_t T, const int32_t *tokens,

@@ -531,6 +531,10 @@ class KvPlan(namedtuple("KvPlan", "step_lens q_start slots positions mask lens h
         self._sizes = (dev, n, slots.shape[0], T, 0 if mask is None else mask.shape[1])
         return self
 
+    @classmethod
+    def _make(cls, fields):                                # (_replace goes this way: checked too)
+        return cls(*fields)
+
 
 class KvAccepted(namedtuple("KvAccepted", "lens path n_path next")):
     """What Pool.kv_accept keeps, and the buffers that it writes it to: int32 lens, n_path, next [n_seq] and path [n_seq,
@@ -545,6 +549,10 @@ class KvAccepted(namedtuple("KvAccepted", "lens path n_path next")):
         _whole("next", next, (n,), i32, dev)
         self._sizes = (dev, n, path.shape[1])
         return self
+
+    @classmethod
+    def _make(cls, fields):
+        return cls(*fields)
 
 
 class Rope:
@@ -662,7 +670,7 @@ class Pool:
             return self.pages.new_empty(shape, dtype=dtype)
         torch, dev = self.torch, self.pages.device
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=dev)
+            stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=dev)
 
@@ -814,7 +822,7 @@ class Pool:
             out = KvPlan(new((n,), i32), new((n + 1,), i32), new((layers, 2, T), i64), new((T,), i32),
                          None if parents is None else new((T, words), i64), new((n,), i32), new((n,), i32), new((4,), i32))
         else:
-            if out._sizes[:4] != (self._device, n, layers, T) or (parents is not None and out._sizes[4] != words):
+            if out._sizes != (self._device, n, layers, T, words):
                 raise ValueError(f"out: a plan of {n} sequences, {layers} layers, {T} rows and {words} words of mask on "
                                  f"{self.pages.device} is wanted, not {out._sizes[1:]} on device {out._sizes[0]}")
         lora_kv_plan(self.handle, layout, layers, n, counts.data_ptr(), lens.data_ptr(), held.data_ptr(), table.data_ptr(), mp,
@@ -901,7 +909,8 @@ class Pool:
             if here:
                 out.lens.copy_(lens)
             else:
-                with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=self.pages.device)):
+                with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=self.pages.device) if handle
+                                       else torch.cuda.default_stream(self.pages.device)):
                     out.lens.copy_(lens)
         else:
             if out._sizes != (self._device, n, max_nodes):

@@ -624,8 +624,10 @@ hipError_t few(const KvArgs &a, const KvAttend &at, const KvTreeSplit &tr, bool 
     const unsigned hu = (unsigned)(a.n_kv * tr.ncb);
     auto launch = [&](auto kernel, dim3 grid) {
         const int lds = (local ? 1 : 2) * C::LDS;
-        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
+        if (lds > 64 * 1024) {                             // has to be asked for, on each device
+            const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+            if (e != hipSuccess) return e;
+        }
         hipLaunchKernelGGL(kernel, grid, dim3(64 * C::NW), lds, s, a, at, tr);
         return hipGetLastError();
     };

@@ -336,18 +336,20 @@ extern "C" int lora_kv_write_rope(lora_pool *p, const lora_kv_layout_t *l, const
     if (!aligned(slots, 8) || !aligned(positions, 4))
         return set_error(LORA_EINVAL, "%s: misaligned pointer (slots: 8 B, positions: 4 B)", fn);
     const Span qo = rows_span(q_out, q ? T : 0, ldqo, wide, p->elem), pg = pages_span(p);
-    const struct { Span span; int64_t ld, width; } read[] = {
+    const struct { Span span; int64_t ld, width; } read[] = {   // width 0: not a matrix's columns
         {rows_span(k, T, ldk, width, p->elem), ldk, width}, {rows_span(v, T, ldv, width, p->elem), ldv, width},
-        {rows_span(q, q ? T : 0, ldq, wide, p->elem), q == q_out && ldq == ldqo ? ldq : -1, q == q_out ? 0 : wide},   // in place: no overlap
-        {{(const char *)slots, (size_t)T * 16}, -1, 0}, {{(const char *)positions, (size_t)T * 4}, -1, 0},
-        {{(const char *)rope->table, (size_t)rope->n_positions * rope->rot_dim * 4}, -1, 0}};
+        {rows_span(q, q ? T : 0, ldq, wide, p->elem), ldq, wide}, {{(const char *)slots, (size_t)T * 16}, 0, 0},
+        {{(const char *)positions, (size_t)T * 4}, 0, 0}, {{(const char *)rope->table, (size_t)rope->n_positions * rope->rot_dim * 4}, 0, 0}};
     for (const auto &r : read) {
         if (pg.meets(r.span)) return set_error(LORA_EINVAL, "%s: an input lies in the pool's pages", fn);
-        if (!qo.meets(r.span)) continue;
+        if (!qo.meets(r.span) || (&r == &read[2] && q == q_out && (T == 1 || ldq == ldqo))) continue;   // in place
         // q_out may be a column range of the matrix that k and v are others of
-        const int64_t ld = ldqo * p->elem, at = r.ld == ldqo ? (((const char *)r.span.at - qo.at) % ld + ld) % ld : 0;
-        if (r.ld != ldqo || (r.width > 0 && (at < wide * p->elem || at + r.width * p->elem > ld)))
-            return set_error(LORA_EINVAL, "%s: q_out overlaps another argument", fn);
+        bool apart = T > 1 && r.width > 0 && r.ld == ldqo;
+        if (apart) {
+            const int64_t ld = ldqo * p->elem, at = ((r.span.at - qo.at) % ld + ld) % ld;
+            apart = at >= wide * p->elem && at + r.width * p->elem <= ld;
+        }
+        if (!apart) return set_error(LORA_EINVAL, "%s: q_out overlaps another argument", fn);
     }
     if (qo.meets(pg)) return set_error(LORA_EINVAL, "%s: q_out lies in the pool's pages", fn);
     if (p->bookkeeping_only) return set_error(LORA_EINVAL, "%s: bookkeeping-only pool", fn);
@@ -377,7 +379,8 @@ extern "C" int lora_kv_accept(lora_pool *p, const lora_kv_layout_t *l, int32_t l
     const char *fn = "lora_kv_accept";
     if (int rc = check_layers(fn, layers)) return rc;
     const int rc0 = begin(p, fn, l, n_seq, T);
-    if (rc0) return rc0 < 0 ? rc0 : LORA_OK;
+    if (rc0 < 0) return rc0;
+    if (n_seq == 0) return LORA_OK;                         // no rows: paths of length 0 are still to be written
     KvAccept c{};
     if (int rc = common(p, fn, l, table, max_pages, q_start, lens, n_seq, T, (int64_t)max_pages * l->tokens_per_page, &c.a)) return rc;
     if (int rc = check_nodes(fn, max_nodes)) return rc;
@@ -387,7 +390,7 @@ extern "C" int lora_kv_accept(lora_pool *p, const lora_kv_layout_t *l, int32_t l
         {targets, tb, false}, {parents, tb, false}, {p->pages, pages_span(p).bytes, true}, {lens_out, nb, true}, {path, nb * max_nodes, true},
         {n_path, nb, true}, {next, nb, true}};
     for (int i = 0; i < 11; ++i) {
-        if (!sp[i].at && i != 6) return set_error(LORA_EINVAL, "%s: NULL pointer argument", fn);
+        if (!sp[i].at && i != 6 && (T > 0 || i < 3 || i > 5)) return set_error(LORA_EINVAL, "%s: NULL pointer argument", fn);
         if (!aligned(sp[i].at, 4)) return set_error(LORA_EINVAL, "%s: misaligned pointer (4 B)", fn);
         for (int j = 0; j < i; ++j)
             if ((sp[i].written || sp[j].written) && Span{(const char *)sp[i].at, sp[i].bytes}.meets({(const char *)sp[j].at, sp[j].bytes}))

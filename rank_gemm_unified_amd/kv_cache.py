@@ -244,7 +244,7 @@ class KvDraftCache:
                                new((T, words), torch.int64) if words else None, self.lens, self.held, self.state)
         self.pool.kv_plan(self.layout, counts, self.lens, self.held, self.table, self.stock, self.state, T, self.max_tokens,
                           parents, max_nodes, out=step)
-        self.step, self._parents, self._nodes = step, parents, max_nodes
+        self.step, self._parents, self._nodes, self._kept = step, parents, max_nodes, False
 
     def write(self, layer, q, k, v, q_out=None):
         """Layer `layer`'s rows of the step: K and V to their pages, and q, all turned by their positions if the cache has a
@@ -266,9 +266,12 @@ class KvDraftCache:
 
     def accept(self, tokens, targets):
         """Keep the path of each tree that the model agrees with (Pool.kv_accept): tokens, targets int32 [T], what each node
-        stands for and what the model chose behind it."""
+        stands for and what the model chose behind it.  Once a step."""
         if self._parents is None:
             raise ValueError("the step has no trees")
+        if self._kept:
+            raise ValueError("the step's paths are kept already")
+        self._kept = True
         new, n = lambda *shape: torch.empty(shape, dtype=torch.int32, device=self.lens.device), self.max_seqs
         return self.pool.kv_accept(self.layout, self.table, self.step.step_lens, self.step.q_start, tokens, targets, self._parents,
                                    self._nodes, out=self._rg.KvAccepted(self.lens, new(n, self._nodes), new(n), new(n)))

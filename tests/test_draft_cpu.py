@@ -44,7 +44,8 @@ def test_good_arguments_reach_the_last_check(which):
     ("write", dict(q=AT[0], q_out=AT[0], ldq=768, ldqo=768, k=AT[0] + 1024, ldk=768, v=AT[0] + 1280, ldv=768)),   # one matrix, in place
     ("write", dict(q=AT[0], q_out=AT[2] + 256, ldqo=768, k=AT[2], ldk=768, v=AT[2] + 1280, ldv=768)),
     ("write", dict(rope=rg.lora_rope_t(AT[20], 1, 16, rg.LORA_ROPE_NEIGHBOURS))), ("tree", dict(max_nodes=256)),
-    ("tree", dict(max_nodes=1, max_len=1)), ("accept", dict(max_nodes=256))])
+    ("tree", dict(max_nodes=1, max_len=1)), ("accept", dict(max_nodes=256)),
+    ("accept", dict(T=0, tokens=None, targets=None, parents=None))])
 def test_other_good_arguments(which, change):
     assert _call(which, **change) == rg.LORA_EINVAL and "bookkeeping-only" in rg.lora_last_error()
 
@@ -70,7 +71,8 @@ REFUSED = [
     ("write", dict(q=None)), ("write", dict(q_out=None)), ("write", dict(k=None)), ("write", dict(v=None)), ("write", dict(slots=None)),
     ("write", dict(positions=None)), ("write", dict(slots=AT[4] + 4)), ("write", dict(positions=AT[5] + 2)), ("write", dict(k=AT[2] + 8)),
     ("write", dict(ldq=508)), ("write", dict(ldqo=256)), ("write", dict(ldk=132)), ("write", dict(ldv=64)), ("write", dict(T=-1)),
-    ("write", dict(q_out=AT[0] + 16)), ("write", dict(q_out=AT[0], ldqo=520)), ("write", dict(q_out=AT[2])), ("write", dict(q_out=AT[5] - 1024)),
+    ("write", dict(q_out=AT[0] + 16)), ("write", dict(q_out=AT[0], ldqo=520)),
+    ("write", dict(q_out=AT[0], k=AT[0], ldk=512)), ("write", dict(q_out=AT[0], v=AT[0], ldv=512)), ("write", dict(T=1, q_out=AT[0], k=AT[0])), ("write", dict(q_out=AT[2])), ("write", dict(q_out=AT[5] - 1024)),
     ("write", dict(q_out=AT[20])), ("write", dict(q=AT[0], q_out=AT[0], ldq=768, ldqo=768, k=AT[0] + 768, ldk=768)),
     ("tree", dict(q=None)), ("tree", dict(out=None)), ("tree", dict(table=None)), ("tree", dict(lens=None)), ("tree", dict(q_start=None)),
     ("tree", dict(mask=None)), ("tree", dict(mask=AT[4] + 4)), ("tree", dict(max_nodes=0)), ("tree", dict(max_nodes=257)),
@@ -82,7 +84,7 @@ REFUSED = [
     ("tree", dict(max_pages=1000, max_len=2000, workspace=AT[0])), ("tree", dict(max_pages=1000, max_len=2000, workspace=AT[5])),
     ("accept", dict(layers=0)), ("accept", dict(n_seq=-1)), ("accept", dict(max_pages=0)), ("accept", dict(T=-1)), ("accept", dict(max_nodes=0)),
     ("accept", dict(max_nodes=257)), ("accept", dict(lens_out=AT[2])), ("accept", dict(path=AT[8] - 8)), ("accept", dict(next=AT[8])),
-    ("accept", dict(n_path=AT[0])), ("accept", dict(tokens=AT[3] + 1)),
+    ("accept", dict(n_path=AT[0])), ("accept", dict(T=0, next=None)), ("accept", dict(T=0, table=None)), ("accept", dict(tokens=AT[3] + 1)),
 ] + [("plan", {k: None}) for k in ("counts", "lens", "held", "table", "stock", "state", "step_lens", "q_start", "lens_out", "held_out", "state_out")] \
   + [("plan", {k: AT[15] + 2}) for k in ("counts", "held", "table", "state", "parents", "q_start", "held_out")] \
   + [("accept", {k: None}) for k in ("table", "q_start", "lens", "tokens", "targets", "parents", "lens_out", "path", "n_path", "next")]
@@ -94,9 +96,16 @@ def test_refused(which, change):
     assert "bookkeeping-only" not in rg.lora_last_error() and "lora_kv" in rg.lora_last_error()
 
 
+def test_one_row_has_no_stride():
+    """Of a single row the distance to the next means nothing, zero and below included: in place it is q's own, elsewhere apart."""
+    for change in (dict(q_out=AT[0], ldq=512, ldqo=0), dict(q_out=AT[0], ldq=-8, ldqo=0), dict(q_out=AT[0] + 1024, ldqo=0)):
+        assert _call("write", T=1, **change) == rg.LORA_EINVAL and "bookkeeping-only" in rg.lora_last_error()
+    for change in (dict(q_out=AT[0] + 16, ldq=0, ldqo=0), dict(q_out=AT[2], ldk=0, ldqo=0), dict(q_out=AT[3] - 512, ldqo=0, ldv=0)):
+        assert _call("write", T=1, **change) == rg.LORA_EINVAL and "overlaps" in rg.lora_last_error()
+
+
 def test_nothing_to_do_and_null_arguments():
-    for which, change in [("plan", dict(n_seq=0)), ("write", dict(T=0)), ("tree", dict(n_seq=0)), ("tree", dict(T=0)), ("accept", dict(T=0)),
-                          ("accept", dict(n_seq=0))]:
+    for which, change in [("plan", dict(n_seq=0)), ("write", dict(T=0)), ("tree", dict(n_seq=0)), ("tree", dict(T=0)), ("accept", dict(n_seq=0))]:
         assert _call(which, **change) == rg.LORA_OK, (which, change)
     for which, (fn, args) in CALLS.items():
         assert _call(which, pool=None) == rg.LORA_EINVAL and "pool is NULL" in rg.lora_last_error()

@@ -480,3 +480,240 @@ def test_acceptance_of_bad_numbers():
     # node 2's parent is none; a tree of nine is over the most; a length below the rows counts as 0
     assert got.n_path.tolist() == [2, 2, 0, 0] and got.next.tolist() == [1, 1, -1, -1] and got.lens.tolist() == [2, 2, 9, 1]
     assert torch.equal(pool.pages, before)
+
+
+def test_paths_of_a_step_without_rows_are_empty():
+    lay = rg.lora_kv_layout_t(8, 2, 64, 2)
+    pool = rg.Pool(64, 256, rg.LORA_F32, max_rank=1)
+    none = dev([])
+    got = pool.kv_accept(lay, dev(np.arange(16).reshape(1, 2, 2, 4)), dev([0, 3]), dev([0, 0, 0]), none, none, none, 3)
+    assert got.path.tolist() == [[-1] * 3] * 2 and got.n_path.tolist() == [0, 0] and got.next.tolist() == [-1, -1] and got.lens.tolist() == [0, 3]
+
+
+# ---- every form of the attention, its limits ------------------------------------------------------------------------
+
+# Rows of a K/V head: up to 16 by the first kernel in one block (float32 up to 32 in two, except for heads of 256), more by the
+# other; heads a workgroup 4, 2, 1 and 2 (17 to 64 rows of bfloat16 and enough tokens), 1; ranges on every workgroup, on fewer, one
+# alone; pieces joined by sequences or by the places between ranges, one thread or all of a workgroup to a row.
+@pytest.mark.parametrize("geo,dtype,lens,new", [
+    ("mha64", "bf16", [1500, 1100], [3, 16]), ("mqa128", "bf16", [2100], [4]), ("gqa64", "bf16", [1300], [4]),
+    ("mha64", "f32", [1200, 1030], [17, 32]), ("mqa128", "f32", [1100], [8]), ("gqa64", "f32", [1300, 64], [5, 8]),
+    ("dim256", "f32", [700, 1100], [16, 9]), ("kv8", "bf16", [1990, 2000, 1000, 30, 1, 700, 900, 1600], [16, 5, 9, 16, 1, 3, 2, 16]),
+    ("mha128", "bf16", [700, 1010, 33, 900], [17, 40, 33, 64]), ("mha128", "f32", [600, 33], [20, 33]),
+    ("gqa64", "bf16", [200] * 40, [2] * 40), ("mha64", "bf16", [40 + b % 90 for b in range(150)], [b % 4 for b in range(150)]),
+    ("kv8", "bf16", [5000], [64]), ("dim256", "bf16", [3000], [64])],
+    ids=lambda x: x if isinstance(x, str) else f"{len(x)}x{max(x)}")
+def test_every_form(geo, dtype, lens, new):
+    check(Trees(geo, dtype, lens, new, seed=len(lens)), geo)
+
+
+def test_sequences_that_are_all_empty():
+    for geo, dtype, nodes in (("mha64", "bf16", 4), ("mha64", "f32", 20), ("mha64", "bf16", 40)):
+        for pages in (1, 4000):                             # whole sequences at a time, and in ranges
+            c = Trees(geo, dtype, [0, 0, 0], [nodes, 1, 2], extra_pages=pages)
+            out = c.run(out=torch.full_like(c.q, 7.0))
+            assert (out == 0).all() and c.errors() == rg.LORA_OK
+            c.d_start, c.nodes = dev([0, 0, 0, 0]), nodes
+            assert (c.run(out=torch.full_like(c.q, 7.0)) == 7).all() and c.errors() == rg.LORA_OK
+
+
+def test_the_most_sequences_and_heads():
+    """65535 sequences of a token each: the output is that token's V.  1024 heads on one and 1024 on their own."""
+    n = rg.LORA_MAX_SEQS
+    lay = rg.lora_kv_layout_t(1, 1, 64, 1)
+    pool = rg.Pool(2 * n, 64, rg.LORA_F32, max_rank=1)
+    pool.pages.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    z = dict(dtype=torch.int32, device="cuda")
+    stock = torch.randperm(2 * n, generator=torch.Generator().manual_seed(2)).int().view(n, 1, 2).cuda()
+    table, one, none = torch.full((1, n, 2, 1), -1, **z), torch.ones(n, **z), torch.zeros(n, **z)
+    plan = pool.kv_plan(lay, one, none, none, table, stock, dev([5, n, 0, 0]), n, parents=none, max_nodes=1)
+    ring = torch.roll(stock, -5, 0)
+    assert torch.equal(table.view(n, 2), ring.view(n, 2)) and plan.state.tolist() == [5, 0, 0, 0]
+    assert torch.equal(plan.slots[0].t(), ring.view(n, 2).long()) and torch.equal(plan.q_start, torch.arange(n + 1, **z))
+    out = pool.kv_attend_tree(lay, torch.randn((n, 64), device="cuda"), table[0], plan.step_lens, plan.q_start, plan.mask, 1)
+    assert torch.equal(out, pool.pages[ring[:, 0, 1].long()])
+    kept = pool.kv_accept(lay, table, plan.step_lens, plan.q_start, one, one, none, 1)
+    assert (kept.n_path == 1).all() and (kept.lens == 1).all() and rg.lora_check_device_errors(pool.handle, check=False) == rg.LORA_OK
+    for kv in (1, 1024):
+        lay = rg.lora_kv_layout_t(1024, kv, 64, 1)
+        pool = rg.Pool(100, 64 * kv, rg.LORA_BF16, max_rank=1)
+        pool.pages.normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+        q = torch.randn((2, 65536), device="cuda").bfloat16()
+        bits, lens = [1, 3], [40]
+        table = np.arange(100, dtype=np.int32).reshape(1, 2, 50)
+        want, tol = draft_ref.attend(pool.pages, lay, q, table, lens, [0, 2], bits, 0.125, kv_ref.ROUNDED[torch.bfloat16, kv == 1])
+        close(pool.kv_attend_tree(lay, q, dev(table), dev(lens), dev([0, 2]), dev([[b] for b in bits], np.int64), 2), want, tol,
+              torch.bfloat16, f"1024 heads on {kv}")
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_pages_behind_four_gib(dtype):
+    """A pool of more than 2^32 bytes whose sequences' pages are its last ones: written, read and moved there."""
+    H, many = 4096, (1 << 32) // (4096 * (2 if dtype == "bf16" else 4)) + 300
+    lay, dt = rg.lora_kv_layout_t(4, 2, 64, 32), DT[dtype]
+    pool = rg.Pool(many, H, rg.LORA_BF16 if dtype == "bf16" else rg.LORA_F32, max_rank=1)
+    last = pool.pages[-300:]
+    last.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    small = rg.Pool(300, H, rg.LORA_BF16 if dtype == "bf16" else rg.LORA_F32, max_rank=1)
+    small.pages.copy_(last)
+    table = np.random.default_rng(1).permutation(300)[:2 * 2 * 70].reshape(1, 2, 2, 70).astype(np.int32)
+    rope, g = rg.Rope.of(3000, 64), torch.Generator(device="cuda").manual_seed(2)
+    for m in (5, 40):
+        T, old = 2 * m, (2000, 61)
+        q, k, v = (torch.randn((T, w), generator=g, device="cuda").to(dt) for w in (256, 128, 128))
+        pos = np.concatenate([o + np.arange(m) for o in old])
+        seq = np.arange(T) // m
+        bits = draft_ref.mask_rows(draft_ref.random_trees(np.random.default_rng(m), [m, m]), [m, m])
+        got = []
+        for of, at in ((pool, many - 300), (small, 0)):
+            tab = table + at
+            slots = np.stack([tab[0, seq, r, pos // 32].astype(np.int64) * 32 + pos % 32 for r in range(2)])
+            turned = of.kv_write_rope(lay, rope, q, k, v, dev(slots, np.int64), dev(pos))
+            lens, start = dev([o + m for o in old]), dev([0, m, 2 * m])
+            out = of.kv_attend_tree(lay, turned, dev(tab[0]), lens, start, dev([[b] for b in bits], np.int64), m)
+            of.kv_accept(lay, dev(tab), lens, start, dev([1] * T), dev([1] * T), dev(draft_ref.random_trees(np.random.default_rng(m), [m, m])), m)
+            assert rg.lora_check_device_errors(of.handle, check=False) == rg.LORA_OK
+            got += [out, of.pages[-300:]]
+        assert torch.equal(got[0], got[2]) and torch.equal(got[1], got[3])
+
+
+# ---- streams, graphs and refusals -----------------------------------------------------------------------------------
+
+class Step:
+    """A step of the four calls over one pool, one layer, into given buffers, whose numbers can be drawn anew."""
+
+    def __init__(self, max_pages, most=20):
+        self.most = most
+        self.layout, self.n, self.T, groups = rg.lora_kv_layout_t(8, 2, 64, 2), 3, 64, 3000
+        self.pool = rg.Pool(2 * groups, 256, rg.LORA_BF16, max_rank=1)
+        self.pool.pages.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+        z = dict(dtype=torch.int32, device="cuda")
+        new = lambda *s: torch.zeros(s, **z)  # noqa: E731
+        n, T = self.n, self.T
+        self.table, self.stock = new(1, n, 2, max_pages), torch.randperm(2 * groups, generator=torch.Generator().manual_seed(4)).int().view(-1, 1, 2).cuda()
+        self.buffers = [new(n), new(n), new(n), self.table, self.stock, dev([0, groups, 0, 0]), new(T)] + \
+            [torch.zeros((T, w), dtype=torch.bfloat16, device="cuda") for w in (512, 128, 128)] + [new(T), new(T)]
+        self.plan = rg.KvPlan(new(n), new(n + 1), torch.zeros((1, 2, T), dtype=torch.int64, device="cuda"), new(T),
+                              torch.zeros((T, 1), dtype=torch.int64, device="cuda"), self.buffers[1], self.buffers[2], self.buffers[5])
+        self.kept = rg.KvAccepted(self.buffers[1], new(n, most), new(n), new(n))
+
+    def draw(self, seed):
+        most = self.most
+        rng, g = np.random.default_rng(seed), torch.Generator(device="cuda").manual_seed(seed)
+        counts = [int(x) for x in rng.integers(1, most, self.n)]
+        counts[seed % self.n] = 0 if seed % 2 else most
+        parents = draft_ref.random_trees(rng, counts)
+        self.buffers[0].copy_(dev(counts))
+        self.buffers[6].copy_(dev(parents + [0] * (self.T - len(parents))))
+        for t in self.buffers[7:10]:
+            t.normal_(generator=g)
+        for t in self.buffers[10:]:
+            t.copy_(dev(rng.integers(0, 2, self.T)))
+
+    def all(self):
+        return [self.pool.pages, *self.buffers[1:6], *[t for t in self.plan if t is not None], *self.kept]
+
+    def run(self, rope, **kw):
+        counts, lens, held, table, stock, state, parents, q, k, v, tokens, targets = self.buffers
+        pool, lay, plan, most = self.pool, self.layout, self.plan, self.most
+        pool.kv_plan(lay, counts, lens, held, table, stock, state, self.T, parents=parents, max_nodes=most, out=plan, **kw)
+        turned = pool.kv_write_rope(lay, rope, q, k, v, plan.slots[0], plan.positions, **kw)
+        out = pool.kv_attend_tree(lay, turned, table[0], plan.step_lens, plan.q_start, plan.mask, most, **kw)
+        pool.kv_accept(lay, table, plan.step_lens, plan.q_start, tokens, targets, parents, most, out=self.kept, **kw)
+        return out
+
+
+@pytest.mark.parametrize("max_pages,most", [(100, 4), (900, 4), (100, 20), (900, 20)])       # sequences whole, and in ranges
+def test_captured_calls_replayed(max_pages, most):
+    """One graph of the four calls, replayed with new numbers, beside the same calls run eagerly on a pool of the same contents."""
+    rope, two = rg.Rope.of(2000, 64), [Step(max_pages, most), Step(max_pages, most)]
+    start = [t.clone() for t in two[0].all()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        two[0].draw(0)
+        two[0].run(rope)
+    torch.cuda.current_stream().wait_stream(side)
+    for t, s in zip(two[0].all(), start):
+        t.copy_(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = two[0].run(rope)
+    for t, s in zip(two[0].all(), start):
+        assert torch.equal(t, s)                            # nothing ran yet
+    for seed in range(8):
+        for s in two:
+            s.draw(seed)
+        graph.replay()
+        eager = two[1].run(rope)
+        torch.randn(1000, device="cuda").sum().item()
+        rows = int(two[1].plan.q_start[-1])
+        assert torch.equal(out[:rows], eager[:rows]) and all(torch.equal(a, b) for a, b in zip(two[0].all(), two[1].all())), seed
+    for s in two:
+        assert rg.lora_check_device_errors(s.pool.handle, check=False) == rg.LORA_OK
+
+
+@pytest.mark.parametrize("kind", ["stream", "handle", "default", "zero"])
+def test_calls_on_a_given_stream(kind):
+    rope, here, there = rg.Rope.of(2000, 64), Step(900), Step(900)
+    stream = torch.cuda.Stream() if kind in ("stream", "handle") else torch.cuda.default_stream()
+    other = torch.cuda.Stream()
+    given = {"stream": stream, "handle": stream.cuda_stream, "default": stream, "zero": 0}[kind]
+    for seed in range(3):
+        here.draw(seed)
+        there.draw(seed)
+        want = here.run(rope)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):                      # the current one is not the call's
+            got = there.run(rope, stream=given)
+        torch.cuda.synchronize()
+        rows = int(here.plan.q_start[-1])
+        assert torch.equal(got[:rows], want[:rows]) and all(torch.equal(a, b) for a, b in zip(here.all(), there.all()))
+    with torch.cuda.stream(other):                          # into new tensors
+        b = there.buffers
+        p = there.pool.kv_plan(there.layout, b[0], b[1], b[2], b[3], b[4], b[5], there.T, parents=b[6], max_nodes=20, stream=given)
+        kept = there.pool.kv_accept(there.layout, b[3], p.step_lens, p.q_start, b[10], b[11], b[6], 20, stream=given)
+    torch.cuda.synchronize()
+    resting = b[0] == 0
+    assert torch.equal(kept.lens[resting], p.step_lens[resting]) and (kept.n_path[~resting] > 0).all()
+
+
+def test_arguments_refused():
+    s, rope = Step(100), rg.Rope.of(50, 64)
+    c, counts, lens, held, table, stock, state, parents, q, k, v, tokens, targets = s.pool, *s.buffers
+    plan = lambda **kw: c.kv_plan(**{**dict(layout=s.layout, counts=counts, lens=lens, held=held, table=table, stock=stock, state=state,  # noqa: E731
+                                            T=s.T, parents=parents, max_nodes=20), **kw})
+    p = plan()
+    write = lambda **kw: c.kv_write_rope(**{**dict(layout=s.layout, rope=rope, q=q, k=k, v=v, slots=p.slots[0], positions=p.positions), **kw})  # noqa: E731
+    tree = lambda **kw: c.kv_attend_tree(**{**dict(layout=s.layout, q=q, table=table[0], lens=p.step_lens, q_start=p.q_start, mask=p.mask,  # noqa: E731
+                                                   max_nodes=20), **kw})
+    keep = lambda **kw: c.kv_accept(**{**dict(layout=s.layout, table=table, lens=p.step_lens, q_start=p.q_start, tokens=tokens, targets=targets,  # noqa: E731
+                                              parents=parents, max_nodes=20), **kw})
+    bad = [(plan, dict(counts=counts.long())), (plan, dict(counts=counts.cpu())), (plan, dict(lens=lens[:2])), (plan, dict(held=held.float())),
+           (plan, dict(table=table[:, :, :, ::2])), (plan, dict(stock=stock[:, :, :1])), (plan, dict(state=state[:3])), (plan, dict(T=5)),
+           (plan, dict(parents=parents[::2])), (plan, dict(out=s.plan, T=63, parents=parents[:63])), (plan, dict(out=s.plan, parents=None)),
+           (plan, dict(out=s.plan, max_nodes=65)), (plan, dict(out=s.plan._replace(mask=None))),
+           (write, dict(q=q.float())), (write, dict(k=k[:, :64])), (write, dict(v=v[1:])), (write, dict(slots=p.slots[0].int())),
+           (write, dict(slots=p.slots[0, :, :9])), (write, dict(positions=p.positions.cpu())), (write, dict(q=None, q_out=q)),
+           (write, dict(q_out=q[:9])), (write, dict(q_out=q.t())), (tree, dict(q=q.float())), (tree, dict(q=q[:, :256])),
+           (tree, dict(table=table)), (tree, dict(lens=p.step_lens[:2])), (tree, dict(q_start=p.q_start[:3])), (tree, dict(mask=p.mask.int())),
+           (tree, dict(mask=p.mask[:9])), (tree, dict(max_nodes=65)), (tree, dict(out=q[:9])), (tree, dict(out=q.cpu())),
+           (tree, dict(workspace=torch.empty(9))), (keep, dict(tokens=tokens.long())), (keep, dict(targets=targets[:9])),
+           (keep, dict(parents=parents.cpu())), (keep, dict(table=table[0])), (keep, dict(lens=held[:1])), (keep, dict(out=s.kept, max_nodes=19))]
+    for i, (call, change) in enumerate(bad):
+        with pytest.raises((ValueError, IndexError)):
+            call(**change)
+            print("taken:", i, list(change))
+    for call, change in ((plan, dict(max_nodes=0)), (plan, dict(max_len=300)), (write, dict(q_out=q[:, :], k=q[:, :128])), (tree, dict(max_len=0)),
+                         (tree, dict(scale=float("nan"))), (tree, dict(out=q)), (keep, dict(max_nodes=0))):
+        with pytest.raises((rg.LoraError, ValueError)):
+            call(**change)
+            print("taken:", list(change))
+    z = dict(dtype=torch.int32, device="cuda")
+    for make in (lambda: rg.KvAccepted(*[torch.zeros(3, **z)] * 4), lambda: s.plan._replace(positions=torch.zeros(9, **z)),
+                 lambda: rg.KvPlan(*s.plan[:7], torch.zeros(4, dtype=torch.int32)), lambda: rg.Rope(torch.zeros((5, 8, 2))),
+                 lambda: rg.Rope(torch.zeros((5, 8, 2), device="cuda").double()), lambda: rg.Rope(torch.zeros((5, 7, 2), device="cuda")),
+                 lambda: rg.Rope(torch.zeros((0, 8, 2), device="cuda"))):
+        with pytest.raises(ValueError):
+            make()
+    assert rg.lora_check_device_errors(c.handle, check=False) == rg.LORA_OK

@@ -187,6 +187,8 @@ def test_single_tokens_and_sequences_that_come_and_go():
         tokens = dev(roots)
         cache.plan(dev([1, 1]), 2, parents, 1)
         kept = cache.accept(tokens, model.chosen(cache, tokens))
+        with pytest.raises(ValueError, match="kept already"):
+            cache.accept(tokens, tokens)
         for b in range(2):
             got[b].append(roots[b])
         roots = kept.next.tolist()
