@@ -1,13 +1,19 @@
-// Attention of a tree of new tokens per sequence over the paged cache (the verification of drafted tokens).
+// Attention of a tree of new tokens per sequence over the paged cache (the verification of drafted tokens): up to 16 rows of a
+// K/V head, and the pieces' joining for all; more rows are k_kv_tree_wide.hip's.
 //
 // A sequence's m nodes times the query heads that share a K/V head are the rows of a matrix product with the K/V
 // head's tokens, node by node: row r is head r % group of node r / group.  4 * rows * head_dim operations for 2 *
 // head_dim elements of K and V: up to a hundred rows or so HBM bounds it.  The tiles (TT tokens) of all sequences, one
 // sequence behind the other, are cut into equal ranges whatever the lengths; one workgroup takes one range of one K/V
-// head and up to 16 NB rows, its waves every NW-th tile of it, K and V of the next tile in flight.  Where a sequence
-// ends the waves' sums are joined in LDS, so that only what a range has of a sequence it did not see whole goes to
-// the workspace (rows * head_dim numbers of 32 bits, once a workgroup and not once a wave); k_kv_tree_join puts those
-// pieces together.  No atomics: results do not change from call to call.
+// head and up to 16 NB rows, or of up to four neighbouring heads, whose pieces of a page are then read at one time; its waves
+// an equal part of the range each, K and V of the next tile in flight.  Where a sequence ends the waves' sums are joined in
+// LDS, so that only what a range has of a sequence it did not see whole goes to the workspace (rows * head_dim numbers of 32
+// bits, once a workgroup and not once a wave); k_kv_tree_join puts those pieces together.  No atomics: results do not change
+// from call to call.  Weights of bfloat16 pools are two bfloat16 numbers (off by 2^-15 of themselves at most): the second
+// product is nearly free beside the reads.
+// 64 trees of 16 nodes behind up to 1031 tokens, 32 heads of 128: 133 us for 648 MB (4.9 TB/s); the first kernel here takes 116
+// of them (5.6 TB/s), then the pieces wait for the slowest range and are joined in 8.  One tree behind 203 tokens: 9.5 us, the
+// chain length -> page ids -> K -> softmax -> V -> join in LDS.
 #include <algorithm>
 
 #include "kv_tree.h"
@@ -596,25 +602,43 @@ TreePlan tree_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int3
     const int group = n_heads / n_kv;
     const int64_t rows = (int64_t)max_nodes * group;
     const int64_t blocks = (rows + WIDE_ROWS - 1) / WIDE_ROWS;
+    // Up to 16 rows in one block of the kernel for few rows, float32 up to 32 in two: bfloat16 of 32 rows took 172 us so, by the
+    // other kernel 139 (float32, 32 trees of 32 nodes, 16 heads of 64 behind up to 500 tokens: 41 and 53).
     p.nb = rows <= 16 ? 1 : rows <= 32 && hd < 256 && dtype == LORA_F32 ? 2 : 0;
-    p.local = n_seq * n_kv * (p.nb ? 1 : blocks) <= 256 && max_len <= (p.nb ? 1024 : 512);
-    // Neighbouring heads a workgroup.  Two of the kernel for many rows where 64 are enough and the call keeps every workgroup
-    // busy for several steps (16 trees of 32 nodes, 32 heads, behind up to 2000 tokens: 89 us one head each, 85 two; one tree of
-    // 16, 32 heads on 8, behind 1000: 14 and 18.8).
-    const bool two = rows <= WIDE_ROWS / 2 && n_kv % 2 == 0 && dtype != LORA_F32 && (max_len + 63) / 64 * n_seq * n_kv >= 4 * 512;
-    p.hw = p.nb ? (n_kv % 4 == 0 ? 4 : n_kv % 2 == 0 ? 2 : 1) : two && !p.local ? 2 : 1;
+    // Whole sequences, one workgroup each of a head and block of rows, need no pieces and no second launch, but their longest has
+    // to be a small part of a workgroup's share.  `whole` workgroups against ranges, us:
+    //   few rows, one a CU: 32 of 1000 tokens 18 and 21.5, of 2000 29 and 22.6; 256 of 1900 51 and 60; 512 of up to 500 25 and 32,
+    //   of up to 2000 86 and 80; 1024 of up to 500 54.5 and 53; 2048 of up to 1031 150 and 135
+    //   many rows, two a CU: 8 of 500 23 and 16; 64 of 500 23.4 and 26.5 (heads of 256: 44 and 32); 128 of up to 1000 39 and 34.5;
+    //   256 of up to 1000 42 and 51, of up to 2000 74 and 69; 512 of up to 2000 92 and 102; 2048 of up to 300 67 and 93, of up to
+    //   1000 157 and 184; 1024 of up to 4000 280 and 282
+    //   many rows, float32: 32 of 500 47 and 23; 512 of 190 38 and 43, of up to 500 77 and 71
+    const int64_t whole = (int64_t)n_seq * n_kv * (p.nb ? 1 : blocks);
+    if (p.nb) p.local = whole <= 512 && max_len <= (whole >= 128 && whole <= 256 ? 2048 : 1024);
+    else if (dtype == LORA_F32) p.local = max_len <= std::max<int64_t>(64, std::min<int64_t>(2048, whole / 2));
+    else p.local = max_len <= std::max<int64_t>(whole >= 64 && hd < 256 ? 512 : 256, std::min<int64_t>(2048, 4 * whole));
+    // No workspace: where every smaller call takes its sequences whole too, so that what serves a larger call serves it.
+    const bool none = whole <= 512 && max_len <= (p.nb ? 1024 : dtype == LORA_F32 ? 64 : 256);
+    // Neighbouring heads a workgroup: four of the kernel for few rows (64 trees of 16 nodes, 32 heads, in ranges: 8, 4, 2, 1 of them
+    // 140, 138, 140, 149).  Two of the kernel for many rows where 64 are enough and the call keeps every workgroup busy for several
+    // steps: in ranges (16 trees of 32 nodes, 32 heads, behind up to 2000 tokens: 85, one head each 89; one tree of 16, 32 heads on
+    // 8, behind 1000: 18.8 and 14), and whole where two a CU are left (1024 whole of up to 500 tokens 52, one head each 62; 512 of
+    // up to 2000 108 and 92).
+    const bool two = rows <= WIDE_ROWS / 2 && n_kv % 2 == 0 && dtype != LORA_F32 && (p.local ? whole >= 1024 : (max_len + 63) / 64 * n_seq * n_kv >= 4 * 512);
+    p.hw = p.nb ? (n_kv % 4 == 0 ? 4 : n_kv % 2 == 0 ? 2 : 1) : two ? 2 : 1;
     p.cw = p.nb ? 16 * p.nb : WIDE_ROWS / p.hw;
     p.tt = p.nb ? (dtype == LORA_F32 && hd > 64 ? 16 : 32) : (dtype == LORA_F32 ? 32 : 64) / p.hw;
     const int64_t tiles = (max_len + p.tt - 1) / p.tt * n_seq;
     p.ncb = (int32_t)((rows + p.cw - 1) / p.cw);
     const int64_t hu = (int64_t)n_kv * p.ncb, slots = p.nb || hd == 256 ? 256 : 512;
-    // A workgroup a CU, two of the kernel for many rows.
+    // A workgroup a CU, two of the kernel for many rows; but ranges of four tiles at least, where that leaves 64 (one
+    // sequence of 20000 tokens, 8 heads on one, 16 nodes: 24.7 us, without the limit 38.6; of 6000, 32 heads on 8, 4 nodes 24.6 and 27.8).
     p.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(tiles, std::max<int64_t>(64, tiles / 4)), slots * p.hw / hu));
     // Room for at least `slots` workgroups' pieces, so that what serves the largest call serves them all: the ranges of
     // more rows are fewer.
     const size_t pieces = 2 * (size_t)std::min<int64_t>(tiles * hu, std::max<int64_t>(slots * p.hw, hu)) * p.cw;
     p.off_ml = (pieces * hd * 4 + 255) & ~size_t(255);
-    p.total = p.local ? 0 : p.off_ml + ((pieces * 8 + 255) & ~size_t(255));
+    p.total = none ? 0 : p.off_ml + ((pieces * 8 + 255) & ~size_t(255));
     return p;
 }
 
@@ -653,7 +677,8 @@ hipError_t run(int dtype, const KvArgs &a, const KvAttend &at, const KvTreeArgs 
     else if (pl.nb == 1) e = few<E, HD, 1>(a, at, tr, pl.local, s);
     else if constexpr (HD < 256 && sizeof(E) == 4) e = few<E, HD, 2>(a, at, tr, pl.local, s);
     if (e != hipSuccess || pl.local) return e;
-    // All threads of a workgroup to one row where a sequence is in more than eight pieces on average.
+    // All threads of a workgroup to one row where a sequence is in more than eight pieces on average (one of 30000 tokens, 8 heads,
+    // 4 nodes: 43 us, by one thread 83; 8 of 1000, 32 nodes, in four pieces each: 42 and 29.7).
     constexpr int SLOTS = join_slots<HD>();
     if (pl.R == 1) return e;                               // one range sees every sequence whole
     const int64_t rows = (int64_t)ta.max_nodes * a.group;
