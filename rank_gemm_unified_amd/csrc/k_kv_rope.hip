@@ -1,8 +1,8 @@
 // New tokens' rows after the projections: q and k turned by their positions (rotary embedding), K and V to their slots.
 //
 // A pair (a, b) of a head's elements becomes (a c - b s, a s + b c), c and s from the caller's table.  A copy with three
-// multiplications an element: bound by the bytes moved, 16 bytes a lane and load; for few tokens by the chain position ->
-// table -> store.
+// multiplications an element: bound by the bytes moved, 16 bytes a lane and load (8 x 512 tokens of 32 heads of 128: 41.5 us
+// for 202 MB, 4.9 TB/s); for few tokens by the chain position -> table -> store (64 of them 3.5 us).
 #include <algorithm>
 
 #include "kv_device.h"

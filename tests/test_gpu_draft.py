@@ -493,15 +493,18 @@ def test_paths_of_a_step_without_rows_are_empty():
 # ---- every form of the attention, its limits ------------------------------------------------------------------------
 
 # Rows of a K/V head: up to 16 by the first kernel in one block (float32 up to 32 in two, except for heads of 256), more by the
-# other; heads a workgroup 4, 2, 1 and 2 (17 to 64 rows of bfloat16 and enough tokens), 1; ranges on every workgroup, on fewer, one
-# alone; pieces joined by sequences or by the places between ranges, one thread or all of a workgroup to a row.
+# other; heads a workgroup 4, 2, 1 and 2 (17 to 64 rows of bfloat16 and enough tokens), 1; whole sequences or ranges; pieces joined by
+# sequences or by the places between ranges, one thread or all of a workgroup to a row.
 @pytest.mark.parametrize("geo,dtype,lens,new", [
     ("mha64", "bf16", [1500, 1100], [3, 16]), ("mqa128", "bf16", [2100], [4]), ("gqa64", "bf16", [1300], [4]),
     ("mha64", "f32", [1200, 1030], [17, 32]), ("mqa128", "f32", [1100], [8]), ("gqa64", "f32", [1300, 64], [5, 8]),
     ("dim256", "f32", [700, 1100], [16, 9]), ("kv8", "bf16", [1990, 2000, 1000, 30, 1, 700, 900, 1600], [16, 5, 9, 16, 1, 3, 2, 16]),
     ("mha128", "bf16", [700, 1010, 33, 900], [17, 40, 33, 64]), ("mha128", "f32", [600, 33], [20, 33]),
     ("gqa64", "bf16", [200] * 40, [2] * 40), ("mha64", "bf16", [40 + b % 90 for b in range(150)], [b % 4 for b in range(150)]),
-    ("kv8", "bf16", [5000], [64]), ("dim256", "bf16", [3000], [64])],
+    ("kv8", "bf16", [5000], [64]), ("dim256", "bf16", [3000], [64]), ("kv8", "bf16", [30 + b % 50 for b in range(140)], [1 + b % 4 for b in range(140)]),
+    ("mha128", "f32", [300 - 7 * b for b in range(18)], [33 - b for b in range(18)]), ("mha128", "bf16", [20 + b for b in range(32)], [20 - b % 5 for b in range(32)]),
+    ("gqa64", "bf16", [5 + b % 90 for b in range(512)], [b % 6 for b in range(512)]), ("dim256", "bf16", [9 + b % 70 for b in range(512)], [b % 10 for b in range(512)]),
+    ("gqa64", "f32", [9 + b % 60 for b in range(260)], [b % 10 for b in range(260)])],
     ids=lambda x: x if isinstance(x, str) else f"{len(x)}x{max(x)}")
 def test_every_form(geo, dtype, lens, new):
     check(Trees(geo, dtype, lens, new, seed=len(lens)), geo)
