@@ -182,6 +182,33 @@ def test_hidden_nodes_reach_no_row(where, dtype, value):
             assert not torch.isfinite(out[seeing]).any()
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("geo,lens,new", [
+    ("gqa64", [11 + b % 60 for b in range(512)], [5 + b % 2 for b in range(512)]),           # two heads a workgroup, sequences whole
+    ("kv8", [1990, 2000, 1000, 30, 17, 700, 900, 1600], [16, 9, 16, 9, 16, 13, 10, 16]),     # and in ranges
+    ("mha128", [700, 41, 90], [9, 16, 12]), ("mha64", [1300, 64], [30, 20])])
+def test_a_node_of_one_key_head_reaches_its_rows_alone(geo, lens, new, value):
+    """V of one node of one K/V head of each sequence is not finite: rows that see the node are not there, and nowhere else."""
+    c = Trees(geo, "bf16", lens, new, seed=len(lens))
+    want, tol = c.ref()
+    dim, nkv, tpp = c.layout.head_dim, c.layout.n_kv_heads, c.layout.tokens_per_page
+    wide = c.layout.n_heads // nkv * dim                    # columns of a K/V head's query heads
+    clean = np.ones(want.shape, bool)
+    for b in range(0, c.n, 3):
+        node, kvh = 2 + b % 3, b % nkv
+        t = c.lens[b] - c.new[b] + node
+        at = (t % tpp * nkv + kvh) * dim
+        c.pool.pages[int(c.table[b, 1, t // tpp]), at: at + dim] = value
+        for i in range(c.new[b]):
+            if c.bits[c.starts[b] + i] >> node & 1:
+                clean[c.starts[b] + i, kvh * wide: (kvh + 1) * wide] = False
+    out = c.run()
+    dirty = torch.as_tensor(~clean, device="cuda")
+    assert dirty.any() and not torch.isfinite(out[dirty]).any()
+    close(torch.where(dirty, 0.0, out), np.where(clean, want, 0), np.where(clean, tol, 0), c.dt, geo)
+    assert c.errors() == rg.LORA_OK
+
+
 def test_bad_pages_and_lengths_are_recorded():
     c = Trees("gqa64", "bf16", [50, 40, 30, 20], [5, 4, 3, 2], seed=2)
     c.table[0, 0, 3] = 10 ** 6
