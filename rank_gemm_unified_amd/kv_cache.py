@@ -271,10 +271,11 @@ class KvDraftCache:
             raise ValueError("the step has no trees")
         if self._kept:
             raise ValueError("the step's paths are kept already")
-        self._kept = True
         new, n = lambda *shape: torch.empty(shape, dtype=torch.int32, device=self.lens.device), self.max_seqs
-        return self.pool.kv_accept(self.layout, self.table, self.step.step_lens, self.step.q_start, tokens, targets, self._parents,
+        kept = self.pool.kv_accept(self.layout, self.table, self.step.step_lens, self.step.q_start, tokens, targets, self._parents,
                                    self._nodes, out=self._rg.KvAccepted(self.lens, new(n, self._nodes), new(n), new(n)))
+        self._kept = True
+        return kept
 
     def finish(self, rows):
         """Sequences done: their rows are free, and the next plan takes their pages back.  rows: a list, or an int64 tensor on

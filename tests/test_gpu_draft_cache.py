@@ -186,7 +186,10 @@ def test_single_tokens_and_sequences_that_come_and_go():
     for _ in range(6):
         tokens = dev(roots)
         cache.plan(dev([1, 1]), 2, parents, 1)
-        kept = cache.accept(tokens, model.chosen(cache, tokens))
+        chosen = model.chosen(cache, tokens)
+        with pytest.raises(ValueError, match="tokens"):
+            cache.accept(tokens.long(), chosen)             # a refused call keeps nothing
+        kept = cache.accept(tokens, chosen)
         with pytest.raises(ValueError, match="kept already"):
             cache.accept(tokens, tokens)
         for b in range(2):
