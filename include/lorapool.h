@@ -577,8 +577,7 @@ size_t lora_kv_attend_tree_workspace_size(const lora_pool *pool, const lora_kv_l
  *   mask         device uint64 [T][(max_nodes + 63) / 64], as lora_kv_plan writes it; any other set of nodes will do.
  *                Bits of nodes that a sequence does not have are not looked at
  *   max_nodes    no sequence has more new tokens (1 .. LORA_MAX_TREE): one that does counts as empty, and is recorded
- * A row that sees nothing comes out as zero.  bfloat16 pools: the weights enter the product with V as lora_kv_attend's
- * where max_nodes * n_heads / n_kv_heads is at most 16, as lora_kv_attend_chunk's (rounded once) where it is more.  An
+ * A row that sees nothing comes out as zero.  bfloat16 pools: the weights enter the product with V as lora_kv_attend's.  An
  * infinite value of a node whose weight is zero makes a row that sees it NaN or that infinity.  The rest as lora_kv_attend.
  * Errors: LORA_EINVAL, LORA_EHIP.
  */

@@ -357,19 +357,14 @@ __global__ __launch_bounds__((64 * TreeTile<E, HD, NB>::NW), (TreeTile<E, HD, NB
         if constexpr (BF) {
 #pragma unroll
             for (int q = 0; q < TT / 32; ++q) {
-                // weights as the sum of two bfloat16 numbers, off by at most 2^-15: the first their leading bits, cut off,
-                // the second the rest, rounded, and raised to 2^-126 where it is less, unless the weight itself is: an
-                // infinite value times a weight stays that infinity, and a weight of zero stays zero.
                 u32x4_t hi[NB], lo[NB];
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const float a0 = S[b][2 * q + x / 2][2 * (x & 1)], a1 = S[b][2 * q + x / 2][2 * (x & 1) + 1];
-                        const uint32_t h0 = __float_as_uint(a0) & 0xffff0000u, h1 = __float_as_uint(a1) & 0xffff0000u;
-                        hi[b][x] = h0 >> 16 | h1;
-                        const float f0 = __uint_as_float(h0), f1 = __uint_as_float(h1);
-                        lo[b][x] = pack2(__builtin_amdgcn_fmed3f(a0 - f0, f0, 0x1p-126f), __builtin_amdgcn_fmed3f(a1 - f1, f1, 0x1p-126f));
+                        const uint2 w = split2(S[b][2 * q + x / 2][2 * (x & 1)], S[b][2 * q + x / 2][2 * (x & 1) + 1]);
+                        hi[b][x] = w.x;
+                        lo[b][x] = w.y;
                     }
                 constexpr int WV = HD == 64 ? 4 : 8;
 #pragma unroll

@@ -5,10 +5,11 @@
 // pages straight to LDS (16 bytes a lane, gathered row by row, the next step's while this one's are used); a wave's rows
 // stay in registers, as columns:
 //     S^T = K Q^T   (rows tokens, columns query rows)       out^T += V^T P^T   (rows dims)
-// so that the weights are in place as the right operand of the second product.  They are rounded to bfloat16 once (2^-8 of
-// themselves at most; the running maximum follows at once, so that a row's largest is one and is not rounded): a second
-// product for the rest would be felt here.  Two workgroups a CU: one's softmax runs under the other's products and loads (one
-// a CU with four stages in LDS: 277 us for what takes 185).
+// so that the weights are in place as the right operand of the second product, bfloat16 ones as two numbers (split2), as for the few
+// rows: what a row comes out as does not hang on how many rows the call may have.  Rounded to one number they would be off by
+// 2^-8 of themselves, and the call would take 185 us instead of 210 below, 97 instead of 105 for 16 trees of 64 nodes behind up to
+// 2000 tokens and 32 heads, 90 instead of 92 for 32 nodes.  Two workgroups a CU: one's softmax runs under the other's products
+// and loads.
 // 8 trees of 32 nodes behind up to 32768 tokens, 32 heads of 128 on 8: 170 to 185 us for 750 MB (4.2 TB/s), 83 Gflop; the loads
 // alone take 150 of the 165 in here, the pieces' join 13.  Steps of 32 tokens with three of them in flight: 197.
 #include "kv_tile.h"
@@ -272,8 +273,7 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_tree_wide(KvA
 #pragma unroll
                 for (int x = 0; x < 16; ++x) mt = fmaxf(mt, S[nb][x]);
             mt = fmaxf(mt, other_half(mt)) * sc;
-            // bfloat16: the running maximum follows at once, so that a row's largest weight is one and is not rounded
-            if (__any(mt > m + (BF ? 0.f : 8.f))) {
+            if (__any(mt > m + 8.f)) {                     // (weights of up to 2^8 do no harm)
                 const float mn = fmaxf(m, mt), ms = mn == -INFINITY ? 0.f : mn;
                 // (before a row's first weight the accumulators hold zeros, or infinities of nodes)
                 const float c = m == -INFINITY ? 1.f : exp2_hw(m - ms);
@@ -297,23 +297,34 @@ __global__ __launch_bounds__(256, (Chunk<E, HD>::WAVES)) void k_kv_tree_wide(KvA
             l += ps;
             if constexpr (BF) {
                 const int i16 = lane & 15;
+                typedef short s16x8_t __attribute__((ext_vector_type(8)));
 #pragma unroll
                 for (int s = 0; s < NT / 16; ++s) {
-                    u32x4_t p;                             // this lane's eight weights: tokens 16 s + 4 hh + 0..3 and 8 on
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) p[x] = pack2(S[s / 2][8 * (s & 1) + 2 * x], S[s / 2][8 * (s & 1) + 2 * x + 1]);
+                    u32x4_t hi, lo;                        // this lane's eight weights: tokens 16 s + 4 hh + 0..3 and 8 on
                     const int t = 16 * s + 4 * hh + (i16 >> 2);
+                    s16x8_t v[ND];
 #pragma unroll
                     for (int d = 0; d < ND; ++d) {
                         const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
                         const char *ad = vb + t * RB + 16 * C::v_swz(t, c) + 8 * (i16 & 1);
                         const s16x4_t v0 = read_tr((lds_s16x4 *)ad);
                         const s16x4_t v1 = read_tr((lds_s16x4 *)(ad + 8 * RB));
-                        typedef short s16x8_t __attribute__((ext_vector_type(8)));
-                        const s16x8_t v = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
-                        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v),
-                                                                         __builtin_bit_cast(bf16x8_t, p), acc[d], 0, 0, 0);
+                        v[d] = s16x8_t{v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
                     }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint2 w = split2(S[s / 2][8 * (s & 1) + 2 * x], S[s / 2][8 * (s & 1) + 2 * x + 1]);
+                        hi[x] = w.x;
+                        lo[x] = w.y;
+                    }
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+                        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v[d]),
+                                                                         __builtin_bit_cast(bf16x8_t, hi), acc[d], 0, 0, 0);
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+                        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v[d]),
+                                                                         __builtin_bit_cast(bf16x8_t, lo), acc[d], 0, 0, 0);
                 }
             } else {
 #pragma unroll

@@ -146,7 +146,17 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {   // the parts of a
     else return ((w & 0x7f80u) == 0x7f80u ? w & 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? w & 0xffff0000u : 0u);
 }
 
-// More than 32 rows (k_kv_tree_wide.hip)
+// Two weights as the sums of two bfloat16 numbers each, off by at most 2^-15: x the first ones, their leading bits, cut off; y the
+// second, the rest, rounded, and raised to 2^-126 where it is less, unless the weight itself is: an infinite value times a
+// weight stays that infinity, and a weight of zero stays zero.
+__device__ __forceinline__ uint2 split2(float a0, float a1) {
+    const uint32_t u0 = __float_as_uint(a0), u1 = __float_as_uint(a1);
+    const float f0 = __uint_as_float(u0 & 0xffff0000u), f1 = __uint_as_float(u1 & 0xffff0000u);
+    return make_uint2(__builtin_amdgcn_perm(u1, u0, 0x07060302u),
+                      pack2(__builtin_amdgcn_fmed3f(a0 - f0, f0, 0x1p-126f), __builtin_amdgcn_fmed3f(a1 - f1, f1, 0x1p-126f)));
+}
+
+// More than 16 rows, float32 also heads of up to 128 more than 32 (k_kv_tree_wide.hip)
 constexpr int WIDE_ROWS = 128;
 hipError_t launch_tree_wide(int dtype, const KvArgs &a, const KvAttend &at, const KvTreeSplit &tr, bool local, hipStream_t s);
 
