@@ -600,7 +600,8 @@ class Pool:
         self.handle = lora_pool_create(self.pages, num_pages, hidden, dtype, max_rank, n_slots, max_adapters,
                                        self.table, free_order)
         self._ws = None
-        self._device = -2 if self.pages is None else self.pages.get_device()   # (a tensor on the host says -1)
+        # -2: no tensor's device (one on the host says -1), so that no call takes any
+        self._device = self.pages.get_device() if self.pages is not None and self.pages.is_cuda else -2
 
     def close(self):
         if self.handle:
