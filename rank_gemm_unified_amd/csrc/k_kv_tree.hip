@@ -629,9 +629,12 @@ TreePlan tree_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int3
     // A workgroup a CU, two of the kernel for many rows; but ranges of four tiles at least, where that leaves 64 (one
     // sequence of 20000 tokens, 8 heads on one, 16 nodes: 24.7 us, without the limit 38.6; of 6000, 32 heads on 8, 4 nodes 24.6 and 27.8).
     p.R = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(tiles, std::max<int64_t>(64, tiles / 4)), slots * p.hw / hu));
-    // Room for at least `slots` workgroups' pieces, so that what serves the largest call serves them all: the ranges of
-    // more rows are fewer.
-    const size_t pieces = 2 * (size_t)std::min<int64_t>(tiles * hu, std::max<int64_t>(slots * p.hw, hu)) * p.cw;
+    // Room for at least `slots` workgroups' pieces, so that what serves the largest call serves them all: the ranges of more rows
+    // are fewer.  For many rows by blocks and steps of one head a workgroup, which two heads need no more than: the sizes for which
+    // `two` holds begin anywhere.
+    const int64_t cw = p.nb ? p.cw : WIDE_ROWS, step = p.tt * (p.nb ? 1 : p.hw), block_rows = (int64_t)n_kv * ((rows + cw - 1) / cw) * cw;
+    const size_t pieces = 2 * (size_t)std::min<int64_t>((max_len + step - 1) / step * n_seq * block_rows,
+                                                        std::max<int64_t>(slots * p.hw * p.cw, block_rows));
     p.off_ml = (pieces * hd * 4 + 255) & ~size_t(255);
     p.total = none ? 0 : p.off_ml + ((pieces * 8 + 255) & ~size_t(255));
     return p;

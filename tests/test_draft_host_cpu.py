@@ -22,3 +22,18 @@ def test_a_pool_on_the_host_takes_no_call(monkeypatch):
                  lambda: pool.kv_accept(L, table[None], one, start, one, one, one, 1)):
         with pytest.raises(ValueError, match="is wanted|are wanted"):
             call()
+
+
+@pytest.mark.parametrize("dtype", [rg.LORA_BF16, rg.LORA_F32])
+@pytest.mark.parametrize("layout", [(514, 514, 64, 1), (768, 768, 64, 1), (1022, 1022, 64, 1), (1024, 512, 64, 1), (1024, 1024, 64, 1),
+                                    (600, 600, 64, 1), (512, 512, 128, 1), (900, 300, 64, 1), (511, 511, 64, 1), (130, 130, 256, 1), (40, 40, 128, 1), (40, 8, 128, 5)])
+def test_a_tree_workspace_serves_every_smaller_call(layout, dtype):
+    """Never less for more sequences, nodes or tokens, up to the most heads: each size against the next larger ones."""
+    pool = rg.Pool(8, layout[1] * layout[2] * layout[3], dtype, max_rank=1, device=None)
+    lay, size = rg.lora_kv_layout_t(*layout), rg.lora_kv_attend_tree_workspace_size
+    seqs, nodes = [1, 2, 3, 4, 8, 31, 64, 65, 300, 4000], [1, 5, 6, 8, 9, 16, 17, 21, 22, 32, 33, 64, 65, 85, 86, 128, 129, 256]
+    lens = [1, 31, 32, 33, 64, 65, 256, 257, 512, 513, 1024, 1025, 2048, 2049, 5000, 10 ** 6]
+    got = {(i, j, k): size(pool.handle, lay, s, m, n) for i, s in enumerate(seqs) for j, m in enumerate(nodes) for k, n in enumerate(lens)}
+    for (i, j, k), n in got.items():
+        for more in ((i + 1, j, k), (i, j + 1, k), (i, j, k + 1)):
+            assert n <= got.get(more, n), (seqs[i], nodes[j], lens[k], more)
