@@ -34,7 +34,7 @@ __device__ __forceinline__ int32_t rows_of(const KvPlan &p, int32_t b, int *err)
     if (bad) *err = DEV_ERR_LEN;
     return bad ? 0 : c;
 }
-// `end`: rows up to this sequence's last; behind T it has no room and takes nothing.
+// `end`: rows up to this sequence's last; behind T it has no room, takes nothing and gives nothing.
 __device__ __forceinline__ Want want_of(const KvPlan &p, int32_t b, int64_t end) {
     Want w;
     w.err = 0;
@@ -47,12 +47,12 @@ __device__ __forceinline__ Want want_of(const KvPlan &p, int32_t b, int64_t end)
         w.err = DEV_ERR_LEN;
         return w;
     }
-    const bool fits = end <= p.T && w.c <= p.cap - w.n;
-    if (!fits) {
+    if (w.c > 0 && (end > p.T || w.c > p.cap - w.n)) {     // refused: its pages stay, those it has too much too
         w.err = DEV_ERR_LEN;
         w.valid = false;
+        return w;
     }
-    const int32_t pages = pages_of(p, fits ? w.n + w.c : w.n);
+    const int32_t pages = pages_of(p, w.n + w.c);
     w.take = max(0, pages - w.h);
     w.give = max(0, w.h - pages);
     return w;

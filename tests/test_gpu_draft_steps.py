@@ -1,0 +1,54 @@
+"""Steps of drafted tokens, call by call: sequences that sit a step out, paths over pages outside the pool, steps without
+sequences.  What is expected is written out by hand or worked out beside the call."""
+import numpy as np
+import pytest
+import torch
+
+import rank_gemm_unified_amd as rg
+from test_gpu_draft import GEO, Steps, dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def plan(s, counts, T=None, in_place=False, **kw):
+    """A plan of a Steps' tables; returns it with the changed table and stock."""
+    table, stock, lens, held, state = dev(s.table), dev(s.stock), dev(s.lens), dev(s.held), dev(s.state)
+    T, out = sum(counts) if T is None else T, None
+    if in_place:
+        z = dict(dtype=torch.int32, device="cuda")
+        out = rg.KvPlan(torch.empty(s.n, **z), torch.empty(s.n + 1, **z), torch.empty((s.layers, 2, T), dtype=torch.int64, device="cuda"),
+                        torch.empty(T, **z), None, lens, held, state)
+    got = s.pool.kv_plan(s.layout, dev(counts), lens, held, table, stock, state, T, out=out, **kw)
+    return got, table.cpu().numpy(), stock.cpu().numpy()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("layers", [1, 40])
+def test_a_sequence_that_does_not_fit_keeps_its_pages(layers, in_place):
+    """Four tokens in six pages of two: two of them are needed.  Over max_len, or behind T, the sequence is refused, and all six
+    stay with it; in a step that it takes part in four go back."""
+    for kw, counts in ((dict(max_len=6), [1, 3, 0, 1]), (dict(T=3), [1, 3, 0, 1])):
+        s = Steps(2, layers, [4, 4, 3, 6], [2, 6, 4, 3], 7, head=3)
+        got, table, stock = plan(s, counts, in_place=in_place, **kw)
+        assert rg.lora_check_device_errors(s.pool.handle, check=False) == rg.LORA_EDEVICE
+        assert got.lens.tolist() == [5, 4, 3, 6] and got.step_lens.tolist() == [5, 0, 0, 0], kw     # (sequence 3 does not fit either)
+        # sequence 0 takes a page, sequence 2, without new tokens, gives two back, sequence 1 none
+        assert got.held.tolist() == [3, 6, 2, 3] and got.state.tolist() == [4, 8, 2, 0]
+        assert np.array_equal(table[:, 1], s.table[:, 1]) and np.array_equal(table[:, 3], s.table[:, 3])
+        groups = len(s.stock)
+        back = [stock[(3 + 7 + i) % groups] for i in range(2)]
+        assert np.array_equal(np.stack(back), s.table[:, 2, :, 2:4].transpose(2, 0, 1))
+        rest = [i for i in range(groups) if i not in ((3 + 7) % groups, (3 + 8) % groups)]
+        assert np.array_equal(stock[rest], s.stock[rest])
+        assert (got.slots[:, :, 1:] == -1).all() and (got.slots[:, :, 0] >= 0).all()
+        # the next step has room: the pages that are too many go
+        s.table, s.stock, s.lens, s.held, s.state = table, stock, got.lens.tolist(), got.held.tolist(), got.state.tolist()
+        got, *_ = plan(s, [0, 1, 0, 0], in_place=in_place)
+        assert got.held.tolist() == [3, 3, 2, 3] and got.lens.tolist() == [5, 5, 3, 6] and got.state.tolist() == [4, 11, 0, 0]
+        assert rg.lora_check_device_errors(s.pool.handle, check=False) == rg.LORA_OK
