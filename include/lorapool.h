@@ -532,7 +532,7 @@ int lora_pool_drop_kv(lora_pool *pool, int64_t request_id, const int64_t *page_i
  * behind T; a parent that is no earlier node, where the walk to the root ends; page ids outside the pool, whose slots
  * are -1).  No page is taken or given twice as long as held, table, stock and state come from one another.
  * lens_out [n_seq], held_out [n_seq] and state_out [4] may be lens, held and state themselves.  T == 0 plans a step without
- * rows (pages may go back).  Errors: LORA_EINVAL, LORA_EHIP.
+ * rows (pages may go back), n_seq == 0 one without sequences: every slot is -1, q_start is 0.  Errors: LORA_EINVAL, LORA_EHIP.
  */
 int lora_kv_plan(lora_pool *pool, const lora_kv_layout_t *layout, int32_t layers, int32_t n_seq, const int32_t *counts,
                  const int32_t *lens, const int32_t *held, int32_t *table, int32_t max_pages, int64_t max_len,

@@ -299,6 +299,7 @@ __global__ __launch_bounds__(256) void k_kv_plan(KvPlan p, int32_t per_layers, i
     }
     __syncthreads();
     if (tid == 0) {
+        if (p.n_seq == 0) p.q_start[0] = 0;
         taken = back = refused = 0;
         for (int i = 0; i < 4; ++i) {
             taken = max(taken, sh[i][0]);

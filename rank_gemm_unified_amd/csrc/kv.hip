@@ -258,7 +258,7 @@ extern "C" int lora_kv_plan(lora_pool *p, const lora_kv_layout_t *l, int32_t lay
     if (int rc = check_layers(fn, layers)) return rc;
     const int rc0 = begin(p, fn, l, n_seq, T);
     if (rc0 < 0) return rc0;
-    if (n_seq == 0) return LORA_OK;
+    if (n_seq == 0 && p->bookkeeping_only) return LORA_OK;  // without sequences: rows without slots, the state as it was
     const int64_t cap = (int64_t)max_pages * l->tokens_per_page;
     if (max_pages < 1 || cap > LORA_MAX_KV_TOKENS)
         return set_error(LORA_EINVAL, "%s: max_pages %d: %lld tokens not in [1, %d]", fn, max_pages, (long long)cap,
@@ -274,10 +274,10 @@ extern "C" int lora_kv_plan(lora_pool *p, const lora_kv_layout_t *l, int32_t lay
     const size_t nb = (size_t)n_seq * 4, tb = (size_t)T * 4;
     // nothing that is written may overlap anything else, but for the three pairs that may be one buffer
     const struct { const void *at; size_t bytes; bool written, always; int align; } sp[] = {
-        {counts, nb, false, true, 4}, {lens, nb, false, true, 4}, {held, nb, false, true, 4}, {state, 16, false, true, 4},
-        {parents, tb, false, false, 4}, {lens_out, nb, true, true, 4}, {held_out, nb, true, true, 4}, {state_out, 16, true, true, 4},
-        {table, (size_t)layers * n_seq * 2 * max_pages * 4, true, true, 4}, {stock, (size_t)stock_groups * 2 * layers * 4, true, true, 4},
-        {step_lens, nb, true, true, 4}, {q_start, nb + 4, true, true, 4}, {slots, (size_t)layers * 2 * T * 8, true, T > 0, 8},
+        {counts, nb, false, nb > 0, 4}, {lens, nb, false, nb > 0, 4}, {held, nb, false, nb > 0, 4}, {state, 16, false, true, 4},
+        {parents, tb, false, false, 4}, {lens_out, nb, true, nb > 0, 4}, {held_out, nb, true, nb > 0, 4}, {state_out, 16, true, true, 4},
+        {table, (size_t)layers * n_seq * 2 * max_pages * 4, true, nb > 0, 4}, {stock, (size_t)stock_groups * 2 * layers * 4, true, true, 4},
+        {step_lens, nb, true, nb > 0, 4}, {q_start, nb + 4, true, true, 4}, {slots, (size_t)layers * 2 * T * 8, true, T > 0, 8},
         {positions, tb, true, T > 0, 4}, {mask, (size_t)T * words * 8, true, false, 8}};
     for (int i = 0; i < 15; ++i) {
         if (!sp[i].at && sp[i].always) return set_error(LORA_EINVAL, "%s: NULL pointer argument", fn);

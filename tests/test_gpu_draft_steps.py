@@ -52,3 +52,27 @@ def test_a_sequence_that_does_not_fit_keeps_its_pages(layers, in_place):
         got, *_ = plan(s, [0, 1, 0, 0], in_place=in_place)
         assert got.held.tolist() == [3, 3, 2, 3] and got.lens.tolist() == [5, 5, 3, 6] and got.state.tolist() == [4, 11, 0, 0]
         assert rg.lora_check_device_errors(s.pool.handle, check=False) == rg.LORA_OK
+
+
+@pytest.mark.parametrize("T", [0, 5, 700])
+@pytest.mark.parametrize("trees", [False, True])
+def test_a_step_without_sequences(T, trees):
+    """Every row is behind the last: it has no slot, and the state is the one that came in."""
+    lay, z = rg.lora_kv_layout_t(2, 1, 64, 2), dict(dtype=torch.int32, device="cuda")
+    pool = rg.Pool(64, 128, rg.LORA_BF16, max_rank=1)
+    stock, state, none = dev(np.arange(64).reshape(16, 2, 2)), dev([3, 9, 0, 0]), torch.empty(0, **z)
+    for in_place in (False, True):
+        out = rg.KvPlan(torch.empty(0, **z), torch.full((1,), 7, **z), torch.full((2, 2, T), 7, dtype=torch.int64, device="cuda"),
+                        torch.full((T,), 7, **z), torch.full((T, 1), 7, dtype=torch.int64, device="cuda") if trees else None,
+                        none, none, state if in_place else torch.full((4,), 7, **z))
+        got = pool.kv_plan(lay, none, none, none, torch.empty((2, 0, 2, 4), **z), stock, state, T, parents=torch.zeros(T, **z) if trees else None,
+                           max_nodes=8 if trees else 0, out=out)
+        assert (got.slots == -1).all() and (got.positions == 0).all() and got.q_start.tolist() == [0] and got.state.tolist() == [3, 9, 0, 0]
+        assert not trees or (got.mask == 0).all()
+    assert torch.equal(stock.flatten(), torch.arange(64, **z)) and rg.lora_check_device_errors(pool.handle, check=False) == rg.LORA_OK
+    for call in (dict(lens=None), dict(q_start=None), dict(state=None)):                # without sequences their lengths may be NULL
+        args = dict(layers=2, n_seq=0, counts=None, lens=None, held=None, table=None, max_pages=4, max_len=8, stock=stock, stock_groups=16,
+                    state=state, T=0, parents=None, max_nodes=0, step_lens=None, q_start=dev([7]), slots=None, positions=None, mask=None,
+                    lens_out=None, held_out=None, state_out=state)
+        rc = rg.lora_kv_plan(pool.handle, lay, **{**args, **call}, check=False)
+        assert (rc == rg.LORA_OK) == ("lens" in call)
