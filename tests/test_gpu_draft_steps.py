@@ -76,3 +76,38 @@ def test_a_step_without_sequences(T, trees):
                     lens_out=None, held_out=None, state_out=state)
         rc = rg.lora_kv_plan(pool.handle, lay, **{**args, **call}, check=False)
         assert (rc == rg.LORA_OK) == ("lens" in call)
+
+
+@pytest.mark.parametrize("bad", [64, 2 ** 31 - 1, -1, -2 ** 31])
+@pytest.mark.parametrize("place", [3, 1])                   # of the move from place 3 to 2: its source; of 2 to 1: its destination
+@pytest.mark.parametrize("geo", ["mha64", "group16"])
+def test_moves_from_and_to_a_page_outside_the_pool(geo, place, bad):
+    """Two trees whose paths are 0, 2, 3, in two layers.  One page id, of V of one layer of the second tree, lies outside: that one
+    move does not happen and is recorded, and every other does.  No other number is bad."""
+    nh, nkv, dim, H, tpp = GEO[geo]
+    assert tpp == 1                                         # every place has a page of its own
+    lay = rg.lora_kv_layout_t(nh, nkv, dim, tpp)
+    pool = rg.Pool(64, H, rg.LORA_BF16, max_rank=1)
+    table = np.random.default_rng(1).permutation(64).astype(np.int32)[:48].reshape(2, 2, 2, 6)
+    parents, tokens, targets = [0, 0, 0, 2], [9, 5, 6, 7], [6, 0, 7, 8]
+    old, numbers = [0, 2], [dev(x * 2) for x in (tokens, targets, parents)]
+    for hurt in (False, True):
+        pool.pages.normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+        want, tab = pool.pages.clone(), table.copy()
+        if hurt:
+            tab[1, 1, 1, old[1] + place] = bad
+        for layer in range(2):
+            for b in range(2):
+                for r in range(2):
+                    for at, to in ((2, 1), (3, 2)):
+                        if hurt and (layer, b, r) == (1, 1, 1) and place in (at, to):
+                            continue
+                        w = nkv * dim
+                        want[int(table[layer, b, r, old[b] + to]), :w] = want[int(table[layer, b, r, old[b] + at]), :w].clone()
+        z = dict(dtype=torch.int32, device="cuda")
+        out = rg.KvAccepted(torch.zeros(2, **z), torch.zeros((2, 4), **z), torch.zeros(2, **z), torch.zeros(2, **z))
+        got = pool.kv_accept(lay, dev(tab), dev([4, 6]), dev([0, 4, 8]), *numbers, 4, out=out)
+        assert got.path.tolist() == [[0, 2, 3, -1]] * 2 and got.lens.tolist() == [3, 5] and got.next.tolist() == [8, 8]
+        assert rg.lora_check_device_errors(pool.handle, check=False) == (rg.LORA_EDEVICE if hurt else rg.LORA_OK)
+        assert not hurt or "page-id" in rg.lora_last_error()
+        assert torch.equal(pool.pages, want)
