@@ -891,10 +891,12 @@ class Pool:
                             0 if workspace is None else workspace.numel() * workspace.element_size(), stream=handle)
         return out
 
-    def kv_accept(self, layout, table, lens, q_start, tokens, targets, parents, max_nodes, out=None, stream=None):
+    def kv_accept(self, layout, table, lens, q_start, tokens, targets, parents, max_nodes, out=None, stream=None, cached=None):
         """Keep the path of each tree that the model agrees with (lora_kv_accept).  table: int32 [layers, n_seq, 2,
-        max_pages]; lens, q_start: the step's; tokens, targets, parents: int32 [T].  out: a KvAccepted to write into; None:
-        a new one, its lens of sequences without new tokens those of `lens`.  Returns it."""
+        max_pages]; lens, q_start: the step's; tokens, targets, parents: int32 [T].  out: a KvAccepted to write into, whose lens
+        of sequences that sit the step out stay; None: a new one, where they are those of `cached`, int32 [n_seq]: every
+        sequence's tokens, the plan's lens.  Without cached they are those of `lens`, 0 in a plan's step_lens, which the next
+        plan would take for a request that ended: only for steps that every sequence takes part in.  Returns the KvAccepted."""
         self._kv_pages()
         i32 = torch.int32
         layers, n, mp, T = table.shape[0], table.shape[1], table.shape[-1], tokens.shape[0]
@@ -903,16 +905,21 @@ class Pool:
         self._kv_ints("q_start", q_start, (n + 1,), i32)
         for name, t in (("tokens", tokens), ("targets", targets), ("parents", parents)):
             self._kv_ints(name, t, (T,), i32)
+        if cached is not None:
+            self._kv_ints("cached", cached, (n,), i32)
+            if out is not None:
+                raise ValueError("cached with out, whose lens it is")
         handle, here = self._where(stream)
         if out is None:
             new = lambda shape: self._empty(here, stream, shape, i32)  # noqa: E731
             out = KvAccepted(new((n,)), new((n, max_nodes)), new((n,)), new((n,)))
+            before = lens if cached is None else cached
             if here:
-                out.lens.copy_(lens)
+                out.lens.copy_(before)
             else:
                 with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=self.pages.device) if handle
                                        else torch.cuda.default_stream(self.pages.device)):
-                    out.lens.copy_(lens)
+                    out.lens.copy_(before)
         else:
             if out._sizes != (self._device, n, max_nodes):
                 raise ValueError(f"out: {n} sequences and {max_nodes} nodes on {self.pages.device} are wanted, not "

@@ -111,3 +111,33 @@ def test_moves_from_and_to_a_page_outside_the_pool(geo, place, bad):
         assert rg.lora_check_device_errors(pool.handle, check=False) == (rg.LORA_EDEVICE if hurt else rg.LORA_OK)
         assert not hurt or "page-id" in rg.lora_last_error()
         assert torch.equal(pool.pages, want)
+
+
+@pytest.mark.parametrize("given", [False, True])            # on a stream that is given, which is not the current one
+def test_lengths_of_sequences_that_sit_a_step_out(given):
+    """Plan, acceptance into new tensors, plan: one sequence rests, one finds no free page, one does not fit.  Their lengths and
+    pages are what they were, and no group is lost."""
+    s = Steps(2, 2, [4, 5, 8, 6], [2, 3, 4, 3], 1, head=2)
+    table, stock = dev(s.table), dev(s.stock)
+    stream = torch.cuda.Stream() if given else None
+    counts, T = [3, 0, 5, 2], 10
+    numbers = [dev(x) for x in ([1] * T, [1] * T, [0, 0, 1, 0, 0, 1, 2, 3, 0, 0])]
+    args = dict(max_len=12, max_nodes=5, stream=stream)
+    torch.cuda.synchronize()
+    p = s.pool.kv_plan(s.layout, dev(counts), dev(s.lens), dev(s.held), table, stock, dev(s.state), T, parents=numbers[2], **args)
+    torch.cuda.synchronize()
+    assert p.step_lens.tolist() == [0, 0, 0, 0] and p.state.tolist()[1:3] == [1, 3]      # two pages, one free: nobody is served
+    assert rg.lora_check_device_errors(s.pool.handle, check=False) == rg.LORA_EDEVICE    # (8 and 5 are over 12)
+    counts, T = [1, 0, 5, 2], 8
+    numbers = [dev(x) for x in ([1] * T, [1] * T, [0, 0, 0, 1, 2, 3, 0, 0])]
+    p = s.pool.kv_plan(s.layout, dev(counts), p.lens, p.held, table, stock, p.state, T, parents=numbers[2], **args)
+    kept = s.pool.kv_accept(s.layout, table, p.step_lens, p.q_start, *numbers, 5, stream=stream, cached=p.lens)
+    again = s.pool.kv_plan(s.layout, dev([0] * 4), kept.lens, p.held, table, stock, p.state, 0, max_len=12, stream=stream)
+    torch.cuda.synchronize()
+    assert p.step_lens.tolist() == [5, 0, 0, 0] and kept.n_path.tolist() == [1, 0, 0, 0]
+    assert kept.lens.tolist() == again.lens.tolist() == [5, 5, 8, 6] and again.held.tolist() == [3, 3, 4, 3] and again.state.tolist()[1] == 0
+    assert np.array_equal(table.cpu().numpy()[:, 1:], s.table[:, 1:])
+    call = lambda **kw: s.pool.kv_accept(s.layout, table, p.step_lens, p.q_start, *numbers, 5, **kw)  # noqa: E731
+    for kw in (dict(cached=p.lens[:3]), dict(cached=p.lens.long()), dict(cached=p.lens.cpu()), dict(cached=p.lens, out=kept)):
+        with pytest.raises(ValueError, match="cached"):
+            call(**kw)
