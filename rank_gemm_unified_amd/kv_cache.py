@@ -278,9 +278,13 @@ class KvDraftCache:
         return kept
 
     def finish(self, rows):
-        """Sequences done: their rows are free, and the next plan takes their pages back.  rows: a list, or an int64 tensor on
-        the device."""
-        self.lens.index_fill_(0, torch.as_tensor(rows, dtype=torch.int64, device=self.lens.device), 0)
+        """Sequences done: their rows are free, and the next plan takes their pages back.  A step that is planned already goes on
+        without them: their output is zero from here on, and nothing of theirs is kept.  rows: a list, or an int64 tensor on the
+        device."""
+        rows = torch.as_tensor(rows, dtype=torch.int64, device=self.lens.device)
+        self.lens.index_fill_(0, rows, 0)
+        if self.step is not None:
+            self.step.step_lens.index_fill_(0, rows, 0)
 
     def refused(self):
         """Sequences that sat the latest step out although they had new tokens (waits for the device)."""

@@ -1,0 +1,87 @@
+"""KvDraftCache: requests that end inside a step, steps that are captured in parts, paths that are kept once."""
+import pytest
+import torch
+
+import rank_gemm_unified_amd as rg
+from test_gpu_draft import dev
+
+pytestmark = pytest.mark.gpu
+
+LAYOUT, LAYERS = rg.lora_kv_layout_t(4, 2, 64, 2), 2
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def rows(T, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return [torch.randn((T, w), generator=g, device="cuda") for w in (256, 128, 128)]
+
+
+def make(groups=40, request=7, pool=None):
+    pool = pool or rg.Pool(400, 256, rg.LORA_F32, max_rank=1)
+    pool.pages.zero_()
+    return rg.KvDraftCache(pool, LAYERS, LAYOUT, 3, 60, groups, request, rg.Rope.of(64, 64))
+
+
+def layers(cache, q, k, v):
+    out = []
+    for layer in range(LAYERS):
+        out.append(cache.attend(layer, cache.write(layer, q, k, v)))
+    return out
+
+
+def pages_are_whole(cache, groups=40):
+    """What the lengths need is held, the rest is free, and no group is lost or held twice."""
+    cache.plan(dev([0, 0, 0]), 1)
+    held = [-(-int(n) // 2) for n in cache.lens]
+    head, free = cache.state.tolist()[:2]
+    assert cache.held.tolist() == held and free == groups - sum(held)
+    ids = [x for i in range(free) for x in cache.stock[(head + i) % groups].flatten().tolist()]
+    ids += [x for b in range(3) for e in range(held[b]) for x in cache.table[:, b, :, e].flatten().tolist()]
+    assert sorted(ids) == sorted(rg.lora_pool_kv_pages(cache.pool.handle, cache.request))
+    assert rg.lora_check_device_errors(cache.pool.handle, check=False) == rg.LORA_OK
+
+
+PARENTS, TOKENS, TARGETS = [0, 0, 0, 2], [9, 5, 6, 7], [6, 0, 7, 8]      # the path is 0, 2, 3
+
+
+@pytest.mark.parametrize("when", ["before the layers", "between the layers", "before the acceptance"])
+@pytest.mark.parametrize("as_list", [True, False])
+def test_a_request_that_ends_inside_a_step_stays_ended(when, as_list):
+    cache, other = make(), make()
+    numbers = [dev(x * 3) for x in (TOKENS, TARGETS, PARENTS)]
+    for c in (cache, other):
+        c.plan(dev([5, 7, 6]), 18)
+        layers(c, *rows(18, 1))
+        c.plan(dev([4, 4, 4]), 12, numbers[2], 4)
+    end = lambda: cache.finish([1] if as_list else torch.tensor([1], device="cuda"))  # noqa: E731
+    x = rows(12, 2)
+    want = layers(other, *x)
+    if when == "before the layers":
+        end()
+        got = layers(cache, *x)
+        assert all((g[4:8] == 0).all() for g in got)
+    elif when == "between the layers":
+        got = [cache.attend(0, cache.write(0, *x))]
+        end()
+        got.append(cache.attend(1, cache.write(1, *x)))
+        assert torch.equal(got[0], want[0]) and (got[1][4:8] == 0).all()
+    else:
+        got = layers(cache, *x)
+        end()
+        assert torch.equal(got[1], want[1])
+    for g, w in zip(got, want):
+        assert torch.equal(g[:4], w[:4]) and torch.equal(g[8:], w[8:])
+    kept = cache.accept(*numbers[:2])
+    assert cache.lens.tolist() == [8, 0, 9] and kept.n_path.tolist() == [3, 0, 3] and kept.next.tolist() == [8, -1, 8]
+    pages_are_whole(cache)
+    assert cache.held.tolist() == [4, 0, 5]
+    # another request in that row begins at place 0
+    cache.plan(dev([0, 3, 0]), 3)
+    assert cache.step.positions.tolist() == [0, 1, 2] and cache.lens.tolist() == [8, 3, 9]
+    first = cache.attend(0, cache.write(0, *rows(3, 4)))
+    assert torch.allclose(first[0].view(4, 64), rows(3, 4)[2][0].view(2, 64).repeat_interleave(2, 0), rtol=2 ** -22, atol=0)
