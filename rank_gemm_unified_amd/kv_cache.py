@@ -280,11 +280,16 @@ class KvDraftCache:
     def finish(self, rows):
         """Sequences done: their rows are free, and the next plan takes their pages back.  A step that is planned already goes on
         without them: their output is zero from here on, and nothing of theirs is kept.  rows: a list, or an int64 tensor on the
-        device."""
-        rows = torch.as_tensor(rows, dtype=torch.int64, device=self.lens.device)
-        self.lens.index_fill_(0, rows, 0)
+        device, whose numbers outside [0, max_seqs) are no row."""
+        n, rows = self.max_seqs, torch.as_tensor(rows, dtype=torch.int64)
+        if not rows.is_cuda and rows.numel() and not 0 <= int(rows.min()) <= int(rows.max()) < n:
+            raise ValueError(f"rows {rows.tolist()} not in [0, {n})")
+        rows = rows.to(self.lens.device).reshape(-1)
+        done = torch.zeros(n + 1, dtype=torch.bool, device=self.lens.device)     # (an index out of range would end the process)
+        done = done.index_fill_(0, torch.where((rows >= 0) & (rows < n), rows, n), True)[:n]
+        self.lens.masked_fill_(done, 0)
         if self.step is not None:
-            self.step.step_lens.index_fill_(0, rows, 0)
+            self.step.step_lens.masked_fill_(done, 0)
 
     def refused(self):
         """Sequences that sat the latest step out although they had new tokens (waits for the device)."""

@@ -37,3 +37,17 @@ def test_a_tree_workspace_serves_every_smaller_call(layout, dtype):
     for (i, j, k), n in got.items():
         for more in ((i + 1, j, k), (i, j + 1, k), (i, j, k + 1)):
             assert n <= got.get(more, n), (seqs[i], nodes[j], lens[k], more)
+
+
+def test_rows_that_finish():
+    """Numbers on the host that are no row are refused before anything changes."""
+    cache = object.__new__(rg.KvDraftCache)
+    cache.max_seqs, cache.step, cache.lens = 3, None, torch.tensor([4, 5, 6], dtype=torch.int32)
+    for bad in ([3], [0, -1], torch.tensor([1, 2 ** 40]), 7):
+        with pytest.raises(ValueError, match="not in"):
+            cache.finish(bad)
+        assert cache.lens.tolist() == [4, 5, 6]
+    cache.finish([])
+    assert cache.lens.tolist() == [4, 5, 6]
+    cache.finish([2, 0, 2])
+    assert cache.lens.tolist() == [0, 5, 0]

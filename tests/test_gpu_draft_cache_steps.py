@@ -85,3 +85,15 @@ def test_a_request_that_ends_inside_a_step_stays_ended(when, as_list):
     assert cache.step.positions.tolist() == [0, 1, 2] and cache.lens.tolist() == [8, 3, 9]
     first = cache.attend(0, cache.write(0, *rows(3, 4)))
     assert torch.allclose(first[0].view(4, 64), rows(3, 4)[2][0].view(2, 64).repeat_interleave(2, 0), rtol=2 ** -22, atol=0)
+
+
+def test_numbers_on_the_device_that_are_no_row_finish_none():
+    cache = make()
+    cache.plan(dev([5, 7, 6]), 18)
+    layers(cache, *rows(18, 1))
+    for some in ([], [-1], [3, 2 ** 40, -2 ** 40]):
+        cache.finish(torch.tensor(some, dtype=torch.int64, device="cuda"))
+    assert cache.lens.tolist() == cache.step.step_lens.tolist() == [5, 7, 6]
+    cache.finish(torch.tensor([3, 2, -1, 2], device="cuda"))
+    assert cache.lens.tolist() == cache.step.step_lens.tolist() == [5, 7, 0]
+    pages_are_whole(cache)
