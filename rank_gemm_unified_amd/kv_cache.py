@@ -205,7 +205,11 @@ class KvDraftCache:
     says how many).  `lens`, `table`, `held`, `stock` and `state` are the same tensors throughout; `step` is the latest plan.
 
     Everything runs on the current stream and in its order; using the cache from another one is the caller's to order.  What a
-    captured step reads and writes besides (rows, counts, parents, `step`) is its graph's."""
+    captured step reads and writes besides (rows, counts, parents, `step`) is its graph's: write(), attend() and accept() go with
+    the plan() called last, captured or not, and may be called after each replay of a graph that holds it.
+
+    Paths are kept once: accept() leaves the step without sequences (its step_lens go to 0), so that a second one, called or
+    replayed, finds nothing (empty paths) and moves nothing.  Called again on a step whose plan() was not captured, it raises."""
 
     def __init__(self, pool, layers, layout, max_seqs, max_tokens, groups, request, rope=None):
         import rank_gemm_unified_amd as rg
@@ -245,6 +249,7 @@ class KvDraftCache:
         self.pool.kv_plan(self.layout, counts, self.lens, self.held, self.table, self.stock, self.state, T, self.max_tokens,
                           parents, max_nodes, out=step)
         self.step, self._parents, self._nodes, self._kept = step, parents, max_nodes, False
+        self._captured = torch.cuda.is_current_stream_capturing()     # then its replays plan further steps, unseen
 
     def write(self, layer, q, k, v, q_out=None):
         """Layer `layer`'s rows of the step: K and V to their pages, and q, all turned by their positions if the cache has a
@@ -274,7 +279,8 @@ class KvDraftCache:
         new, n = lambda *shape: torch.empty(shape, dtype=torch.int32, device=self.lens.device), self.max_seqs
         kept = self.pool.kv_accept(self.layout, self.table, self.step.step_lens, self.step.q_start, tokens, targets, self._parents,
                                    self._nodes, out=self._rg.KvAccepted(self.lens, new(n, self._nodes), new(n), new(n)))
-        self._kept = True
+        self.step.step_lens.zero_()
+        self._kept = not (self._captured or torch.cuda.is_current_stream_capturing())
         return kept
 
     def finish(self, rows):

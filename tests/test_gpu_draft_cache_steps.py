@@ -97,3 +97,78 @@ def test_numbers_on_the_device_that_are_no_row_finish_none():
     cache.finish(torch.tensor([3, 2, -1, 2], device="cuda"))
     assert cache.lens.tolist() == cache.step.step_lens.tolist() == [5, 7, 0]
     pages_are_whole(cache)
+
+
+def same(one, two):
+    return all(torch.equal(a, b) for a, b in ((one.lens, two.lens), (one.held, two.held), (one.state, two.state), (one.table, two.table),
+                                              (one.stock, two.stock), (one.pool.pages, two.pool.pages)))
+
+
+def trees(seed):
+    """Counts, parents, tokens and targets of a step of up to four nodes a sequence, twelve rows."""
+    g = torch.Generator().manual_seed(seed)
+    counts = torch.randint(1, 5, (3,), generator=g).tolist()
+    counts[seed % 3] = 0 if seed % 2 else 4
+    fill = [0] * (12 - sum(counts))
+    parents = [0 if i == 0 else int(torch.randint(0, i, (1,), generator=g)) for c in counts for i in range(c)] + fill
+    return [dev(counts), dev(parents)] + [torch.randint(0, 2, (12,), generator=g).int().cuda() for _ in range(2)]
+
+
+@pytest.mark.parametrize("inside", ["plan", "plan and layers", "all", "acceptance"])
+def test_steps_captured_in_parts(inside):
+    """What is captured is replayed step after step, the rest is called between the replays, beside a cache that runs all of it
+    eagerly.  A path is kept once: a second acceptance of the same step, called or replayed, moves nothing."""
+    cache, other = make(), make()
+    for c in (cache, other):
+        c.plan(dev([5, 7, 6]), 18)
+        layers(c, *rows(18, 1))
+    numbers, x = trees(0), rows(12, 2)
+    counts, parents, tokens, targets = numbers
+    parts = [lambda c: c.plan(counts, 12, parents, 4), lambda c: layers(c, *x), lambda c: c.accept(tokens, targets)]
+    upto = {"plan": 1, "plan and layers": 2, "all": 3, "acceptance": 0}[inside]
+    before = [t.clone() for t in (cache.lens, cache.held, cache.state, cache.table, cache.stock, cache.pool.pages)]
+    side = torch.cuda.Stream()                              # sets the libraries up; what it changes is put back
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for part in parts:
+            part(cache)
+    torch.cuda.current_stream().wait_stream(side)
+    for t, b in zip((cache.lens, cache.held, cache.state, cache.table, cache.stock, cache.pool.pages), before):
+        t.copy_(b)
+    assert same(cache, other)
+    graph = torch.cuda.CUDAGraph()
+    if inside != "acceptance":
+        with torch.cuda.graph(graph):
+            done = [part(cache) for part in parts[:upto]]
+        assert same(cache, other)                           # nothing ran yet
+    for seed in range(6):
+        for t, new in zip(numbers, trees(seed)):
+            t.copy_(new)
+        for i, t in enumerate(x):
+            t.copy_(rows(12, 10 + seed)[i])
+        want = [part(other) for part in parts]
+        if inside == "acceptance":                          # of one step each, captured behind its layers
+            got = [part(cache) for part in parts[:2]]
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                got.append(parts[2](cache))
+            graph.replay()
+        else:
+            graph.replay()
+            got = done + [part(cache) for part in parts[upto:]]
+        assert same(cache, other), seed
+        kept = [t.clone() for t in got[2]]
+        assert all(torch.equal(a, b) for a, b in zip(kept, want[2]))
+        there = int(other.step.q_start[-1])                  # (rows behind the last hold anything)
+        assert torch.equal(got[1][1][:there], want[1][1][:there])
+        torch.randn(100, device="cuda").sum().item()         # the program's own work between replays
+        if inside == "acceptance":
+            graph.replay()
+            again = got[2]
+        else:
+            again = cache.accept(tokens, targets)
+        assert same(cache, other) and again.n_path.tolist() == [0, 0, 0] and (again.path == -1).all() and again.next.tolist() == [-1] * 3
+    assert int(cache.lens.max()) > 12                       # paths were kept
+    with pytest.raises(ValueError, match="kept already"):
+        other.accept(tokens, targets)
+    pages_are_whole(cache)
