@@ -42,7 +42,6 @@ struct KvTreeArgs {
 };
 
 struct KvPlan {
-    char *pages;
     int64_t num_pages;
     int32_t layers, n_seq, max_pages, tpp, T;
     uint32_t tpp_magic;       // as in KvArgs
@@ -62,7 +61,6 @@ struct KvRope {
     char *pages;
     int64_t num_pages, page_bytes;
     int32_t tpp, T;
-    uint32_t tpp_magic;
     int32_t n_heads, n_kv, head_dim, tok_bytes;
     const float *table;       // [n_positions][rot / 2][2]
     int32_t n_positions, rot, pairs;
