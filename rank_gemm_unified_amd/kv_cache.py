@@ -222,7 +222,11 @@ class KvDraftCache:
             raise ValueError(f"{groups} page groups for {max_seqs} sequences")
         self._rg, self.pool, self.layers, self.layout, self.max_seqs = rg, pool, layers, layout, max_seqs
         self.max_tokens, self.request, self.rope, self._parents = max_tokens, request, rope, None
-        ids = []
+        i32 = dict(dtype=torch.int32, device=pool.pages.device)
+        self.table = torch.full((layers, max_seqs, 2, -(-max_tokens // tpp)), -1, **i32)
+        self.lens, self.held = torch.zeros(max_seqs, **i32), torch.zeros(max_seqs, **i32)
+        self.state, self.stock = torch.tensor([0, groups, 0, 0], **i32), torch.empty((groups, layers, 2), **i32)
+        ids = []                                           # (the pool's pages are taken when nothing else can be too much)
         try:
             for _ in range(groups):
                 ids.append(rg.lora_pool_grow_kv(pool.handle, request, layers))
@@ -232,11 +236,7 @@ class KvDraftCache:
             if ids:
                 rg.lora_pool_free_kv(pool.handle, request)
             raise
-        i32 = dict(dtype=torch.int32, device=pool.pages.device)
-        self.stock = torch.tensor(ids, **i32).view(groups, layers, 2)
-        self.table = torch.full((layers, max_seqs, 2, -(-max_tokens // tpp)), -1, **i32)
-        self.lens, self.held = torch.zeros(max_seqs, **i32), torch.zeros(max_seqs, **i32)
-        self.state = torch.tensor([0, groups, 0, 0], **i32)
+        self.stock.copy_(torch.tensor(ids, dtype=torch.int32).view(groups, layers, 2))
         self.step = None
 
     def plan(self, counts, T, parents=None, max_nodes=None):
@@ -253,7 +253,7 @@ class KvDraftCache:
 
     def write(self, layer, q, k, v, q_out=None):
         """Layer `layer`'s rows of the step: K and V to their pages, and q, all turned by their positions if the cache has a
-        Rope (Pool.kv_write_rope).  Returns the q to attend with."""
+        Rope (Pool.kv_write_rope).  Returns the q to attend with: q_out, or, without a Rope, q itself."""
         if self.rope is None:
             self.pool.kv_write(self.layout, k, v, self.table[layer], self.step.step_lens, self.step.q_start)
             return q

@@ -172,3 +172,12 @@ def test_steps_captured_in_parts(inside):
     with pytest.raises(ValueError, match="kept already"):
         other.accept(tokens, targets)
     pages_are_whole(cache)
+
+
+def test_tables_that_do_not_fit_take_no_pages():
+    pool = rg.Pool(400, 256, rg.LORA_F32, max_rank=1)
+    with pytest.raises(torch.OutOfMemoryError):
+        rg.KvDraftCache(pool, 40, LAYOUT, 65535, 1 << 21, 3, 7)      # a table of 22 TB
+    assert pool.stats()["kv_pages"] == 0
+    cache = rg.KvDraftCache(pool, LAYERS, LAYOUT, 3, 60, 90, 7)
+    assert sorted(cache.stock.flatten().tolist()) == sorted(rg.lora_pool_kv_pages(pool.handle, 7))
