@@ -4,9 +4,10 @@
 // compares all nodes with the current one at once.  Every workgroup walks by itself (the chain of a few compares is
 // shorter than a second launch) and then moves the path's K and V rows in one layer.  Node path[i] goes to place i, and
 // path[i] >= i and rises, so no move overwrites what a later one reads; a thread reads eight rows' pieces before it
-// writes the first, and each thread has its own 16 bytes of every row.  64 trees of 16 nodes in 32 layers of 32 heads: 16.5 us
-// for 69 MB (4.2 TB/s), two rounds of workgroups, each the chain rows -> walk -> pages -> move (by 128 threads
-// a workgroup, in one round, the call takes 17.7 us, by 512 19.8, now 17.0); one tree: 4 us, that chain.
+// writes the first, and each thread has its own 16 bytes of every row.  64 trees of 16 nodes in 32 layers of 32 heads: a call
+// takes 17 to 18 us on several cards for 69 MB (its kernel in traces 16.5 and 17.1, 4.1 TB/s), two rounds of workgroups, each the
+// chain rows -> walk -> pages -> move (on a card where it takes 17.0: by 128 threads a workgroup, in one round, 17.7, by 512 19.8);
+// one tree: 4 us, that chain.
 #include "kv_device.h"
 
 namespace lorapool {

@@ -5,8 +5,8 @@
 // page groups, where the prefix sum says.  8 bytes written for each (layer, K/V, row) and a few read: the time is the
 // chain lengths -> sums -> page -> slot, so it is one launch: each workgroup takes 256 rows of some layers and forms
 // the sums over all sequences by itself.  In place the lengths are written by the workgroup that comes last, when
-// nobody reads them any more.  64 sequences of a token in 32 layers 7.4 us, with trees of 16 nodes 8.0, 8 prompts of 512 7.2
-// (4.2 MB).
+// nobody reads them any more.  64 sequences of a token in 32 layers 7.4 to 7.7 us, with trees of 16 nodes 8.0, 8 prompts of 512 7.2
+// (4.2 MB); in place, one behind the other in a replayed graph, 9.5 and, chains of 16 nodes, 13.5.
 #include <algorithm>
 
 #include "kv_device.h"

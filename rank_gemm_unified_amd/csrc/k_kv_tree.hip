@@ -11,8 +11,8 @@
 // bits, once a workgroup and not once a wave); k_kv_tree_join puts those pieces together.  No atomics: results do not change
 // from call to call.  Weights of bfloat16 pools are two bfloat16 numbers (off by 2^-15 of themselves at most): the second
 // product is nearly free beside the reads.
-// 64 trees of 16 nodes behind up to 1031 tokens, 32 heads of 128: 133 us for 648 MB (4.9 TB/s); the first kernel here takes 116
-// of them (5.6 TB/s), then the pieces wait for the slowest range and are joined in 8.  One tree behind 203 tokens: 9.5 us, the
+// 64 trees of 16 nodes behind up to 1031 tokens, 32 heads of 128: 133 to 152 us on several cards for 648 MB (4.3 to 4.9 TB/s); in a
+// trace the kernel here takes 133 to 136 of them, and the join 8.  One tree behind 203 tokens: 9.5 us, the
 // chain length -> page ids -> K -> softmax -> V -> join in LDS.
 #include <algorithm>
 
@@ -598,15 +598,15 @@ TreePlan tree_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int3
     const int64_t rows = (int64_t)max_nodes * group;
     const int64_t blocks = (rows + WIDE_ROWS - 1) / WIDE_ROWS;
     // Up to 16 rows in one block of the kernel for few rows, float32 up to 32 in two: bfloat16 of 32 rows took 172 us so, by the
-    // other kernel 139 (float32, 32 trees of 32 nodes, 16 heads of 64 behind up to 500 tokens: 41 and 53).
+    // other kernel 139, with weights of one number then (float32, 32 trees of 32 nodes, 16 heads of 64 behind up to 500 tokens: 41 and 53).
     p.nb = rows <= 16 ? 1 : rows <= 32 && hd < 256 && dtype == LORA_F32 ? 2 : 0;
     // Whole sequences, one workgroup each of a head and block of rows, need no pieces and no second launch, but their longest has
     // to be a small part of a workgroup's share.  `whole` workgroups against ranges, us:
     //   few rows, one a CU: 32 of 1000 tokens 18 and 21.5, of 2000 29 and 22.6; 256 of 1900 51 and 60; 512 of up to 500 25 and 32,
     //   of up to 2000 86 and 80; 1024 of up to 500 54.5 and 53; 2048 of up to 1031 150 and 135
-    //   many rows, two a CU: 8 of 500 23 and 16; 64 of 500 23.4 and 26.5 (heads of 256: 44 and 32); 128 of up to 1000 39 and 34.5;
-    //   256 of up to 1000 42 and 51, of up to 2000 74 and 69; 512 of up to 2000 92 and 102; 2048 of up to 300 67 and 93, of up to
-    //   1000 157 and 184; 1024 of up to 4000 280 and 282
+    //   many rows, two a CU: 8 of 500 24 and 16; 64 of 500 24 and 22 (heads of 256: 44.5 and 39); 128 of up to 1000 40.5 and 34;
+    //   256 of up to 1000 43 and 43, of up to 2000 76 and 60; 512 of up to 2000 101 and 103 (32 heads on 8: 119 and 124); 2048 of up
+    //   to 300 72 and 95, of up to 1000 159 and 186; 1024 of up to 4000 289 and 289
     //   many rows, float32: 32 of 500 47 and 23; 512 of 190 38 and 43, of up to 500 77 and 71
     const int64_t whole = (int64_t)n_seq * n_kv * (p.nb ? 1 : blocks);
     if (p.nb) p.local = whole <= 512 && max_len <= (whole >= 128 && whole <= 256 ? 2048 : 1024);
@@ -616,9 +616,10 @@ TreePlan tree_plan(int dtype, int n_heads, int n_kv, int hd, int32_t n_seq, int3
     const bool none = whole <= 512 && max_len <= (p.nb ? 1024 : dtype == LORA_F32 ? 64 : 256);
     // Neighbouring heads a workgroup: four of the kernel for few rows (64 trees of 16 nodes, 32 heads, in ranges: 8, 4, 2, 1 of them
     // 140, 138, 140, 149).  Two of the kernel for many rows where 64 are enough and the call keeps every workgroup busy for several
-    // steps: in ranges (16 trees of 32 nodes, 32 heads, behind up to 2000 tokens: 85, one head each 89; one tree of 16, 32 heads on
-    // 8, behind 1000: 18.8 and 14), and whole where two a CU are left (1024 whole of up to 500 tokens 52, one head each 62; 512 of
-    // up to 2000 108 and 92).
+    // steps: in ranges (16 trees of 32 nodes, 32 heads, behind up to 2000 tokens: 87, one head each 90; 64 of 16, 16 heads of 256 on
+    // 4, behind up to 1000 72 and 77, but 8 of 16, 32 heads on 8, behind up to 9000 72 and 65; one tree of 16, 32 heads on 8, behind
+    // 1000: 19 and 14.5), and whole where two a CU are left (1024 whole of up to 500 tokens 57, one head each 68; 512 of up to 2000
+    // 106 and 104, of 32 nodes 103 and 89).
     const bool two = rows <= WIDE_ROWS / 2 && n_kv % 2 == 0 && dtype != LORA_F32 && (p.local ? whole >= 1024 : (max_len + 63) / 64 * n_seq * n_kv >= 4 * 512);
     p.hw = p.nb ? (n_kv % 4 == 0 ? 4 : n_kv % 2 == 0 ? 2 : 1) : two ? 2 : 1;
     p.cw = p.nb ? 16 * p.nb : WIDE_ROWS / p.hw;

@@ -7,11 +7,12 @@
 //     S^T = K Q^T   (rows tokens, columns query rows)       out^T += V^T P^T   (rows dims)
 // so that the weights are in place as the right operand of the second product, bfloat16 ones as two numbers (split2), as for the few
 // rows: what a row comes out as does not hang on how many rows the call may have.  Rounded to one number they would be off by
-// 2^-8 of themselves, and the call would take 185 us instead of 210 below, 97 instead of 105 for 16 trees of 64 nodes behind up to
-// 2000 tokens and 32 heads, 90 instead of 92 for 32 nodes.  Two workgroups a CU: one's softmax runs under the other's products
-// and loads.
-// 8 trees of 32 nodes behind up to 32768 tokens, 32 heads of 128 on 8: 170 to 185 us for 750 MB (4.2 TB/s), 83 Gflop; the loads
-// alone take 150 of the 165 in here, the pieces' join 13.  Steps of 32 tokens with three of them in flight: 197.
+// 2^-8 of themselves, and the call would take 185 us instead of 208 below, 97 instead of 105 for 16 trees of 64 nodes behind up to
+// 2000 tokens and 32 heads, 90 instead of 92 for 32 nodes, 103 instead of 121 for 64 of 32 nodes, 32 heads on 8.  Two workgroups
+// a CU: one's softmax runs under the other's products and loads (one a CU with four stages in LDS took half as long again).
+// 8 trees of 32 nodes behind up to 32768 tokens, 32 heads of 128 on 8: 192 to 210 us on several cards for 750 MB (3.6 to
+// 3.9 TB/s) and 125 Gflop of products (102 us at the rate of a large one); in a trace 192 of 209 in here, 14 in the pieces' join.  The
+// loads alone took 150 on a card where the call with one number took 185.
 #include "kv_tile.h"
 #include "kv_tree.h"
 
